@@ -1,0 +1,634 @@
+"""The paged cache of the verification pass: its operators, measured case by case.
+
+attend    attention of a step's packed rows over the paged cache, a prefix that requests
+          share read once for all of them
+append    the step's K and V rows laid into the pages
+turnover  pages let go after an acceptance, then pages reserved for the next step's rows
+fork      finished branches freed, then others forked from their parents (sharing whole
+          pages and copying the last one, or copying them all)
+compact   live pages moved to the front of the cache, tables and counts following
+
+The cache is k [layers, n_pages, Hkv, page/16, D/8, 16, 8] and v [layers, n_pages, Hkv,
+page/16, D, 16]; table [rows, width] holds page ids (-1: none), len [rows] the tokens kept
+(-1: a vacant row), ref [n_pages] the number of tables that hold a page.  Row j of request r
+lies at row offsets[r] + lead * r + j of the packed tensors, n_r = offsets[r+1] - offsets[r]
++ lead rows in all, at positions len[r] + j.
+"""
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
+DEV = "cuda"
+
+
+def listed():
+    return [
+        # one token of four requests with short contexts: the latency of a small decoding step
+        dict(name="attend: 4 single tokens", op="attend", R=4, K=0, lead=1, H=32, Hkv=8, D=128, dtype="bf16", page=16,
+             own_len=700, groups=0, shared=0, vacant=0),
+        # a full verification step (256 requests, K = 7) behind one long system prompt
+        dict(name="attend: verify, shared 8192", op="attend", R=256, K=7, lead=1, H=64, Hkv=8, D=128, dtype="bf16", page=64,
+             own_len=1024, groups=1, shared=8192, vacant=6),
+        # two requests with very long contexts of their own, K = 15
+        dict(name="attend: 2 of 131072 tokens", op="attend", R=2, K=15, lead=1, H=64, Hkv=8, D=128, dtype="bf16", page=128,
+             own_len=131072, groups=0, shared=0, vacant=0),
+        # ragged pieces of prompts behind two templates, as many key heads as query heads
+        dict(name="attend: prompts, fp16", op="attend", R=6, K=777, lead=0, H=16, Hkv=16, D=64, dtype="fp16", page=16,
+             own_len=1500, groups=2, shared=1008, vacant=1),
+        # the rows of a full verification step
+        dict(name="append: verify", op="append", R=256, K=7, lead=1, Hkv=8, D=128, dtype="bf16", page=64, own_len=512, vacant=6),
+        # whole prompts of a few requests
+        dict(name="append: prompts", op="append", R=8, K=4099, lead=0, Hkv=8, D=128, dtype="fp16", page=128, own_len=300, vacant=0),
+        # a step of 64 requests with K = 15 over a small cache
+        dict(name="turnover: 64 requests", op="turnover", R=64, K=15, lead=1, page=16, own_len=2000, spare=0.9, vacant=3),
+        # a large engine: 1024 requests over a cache that is nearly full, so that some are refused
+        dict(name="turnover: 1024, nearly full", op="turnover", R=1024, K=15, lead=1, page=16, own_len=4000, spare=0.004, vacant=20),
+        # sixteen parents branch in four
+        dict(name="fork: 64 branches", op="fork", S=16, F=64, deep=False, layers=8, Hkv=8, D=128, dtype="bf16", page=64,
+             own_len=1000),
+        # contexts copied whole
+        dict(name="fork: 24 whole copies", op="fork", S=8, F=24, deep=True, layers=8, Hkv=4, D=64, dtype="fp16", page=32,
+             own_len=3001),
+        # a small cache after many requests have come and gone
+        dict(name="compact: 700 pages", op="compact", rows=20, n_pages=700, live=0.5, layers=2, Hkv=8, D=64, dtype="bf16", page=16),
+        # a large one, half full
+        dict(name="compact: 12000 pages", op="compact", rows=128, n_pages=12000, live=0.5, layers=4, Hkv=8, D=128, dtype="bf16",
+             page=32),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["attend", "attend", "attend", "append", "turnover", "fork", "compact"])
+    Hkv = rng.choice([1, 2, 3, 4, 8])
+    D, dtype, page = rng.choice([64, 128, 128, 256]), rng.choice(["bf16", "fp16"]), rng.choice([16, 32, 64, 128])
+    if op == "attend":
+        prompts = rng.random() < 0.3
+        R = _log(rng, 1, 12) if prompts else _log(rng, 1, 256)
+        c = dict(op=op, R=R, K=_log(rng, 2, 700) if prompts else rng.choice([0, 1, 3, 7, 15]), lead=0 if prompts else 1,
+                 H=Hkv * rng.choice([1, 2, 3, 5, 8]), Hkv=Hkv, D=D, dtype=dtype, page=page, own_len=_log(rng, 1, 200000 // R),
+                 groups=0, shared=0, vacant=rng.choice([0, R // 9]))
+        if rng.random() < 0.6:
+            c.update(groups=rng.randint(1, min(R, 3)), shared=page * _log(rng, 1, 8192 // page))
+        return c
+    if op == "append":
+        prompts = rng.random() < 0.4
+        R = _log(rng, 1, 8) if prompts else _log(rng, 1, 256)
+        return dict(op=op, R=R, K=_log(rng, 2, 4096) if prompts else rng.choice([0, 3, 7, 15]), lead=0 if prompts else 1, Hkv=Hkv,
+                    D=D, dtype=dtype, page=page, own_len=_log(rng, 1, 500), vacant=rng.choice([0, R // 9]))
+    if op == "turnover":
+        R = _log(rng, 1, 1024)
+        return dict(op=op, R=R, K=rng.choice([0, 3, 7, 15]), lead=1, page=page, own_len=_log(rng, 10, 4000),
+                    spare=rng.choice([0.001, 0.01, 0.2, 1.0]), vacant=rng.choice([0, R // 9]))
+    if op == "fork":
+        deep = rng.random() < 0.3
+        return dict(op=op, S=_log(rng, 1, 16), F=_log(rng, 1, 24 if deep else 200), deep=deep, layers=rng.randint(1, 8), Hkv=Hkv,
+                    D=min(D, 128), dtype=dtype, page=page, own_len=_log(rng, 5, 3000))
+    return dict(op=op, rows=_log(rng, 1, 128), n_pages=_log(rng, 100, 12000), live=rng.choice([0.1, 0.4, 0.7, 0.95]),
+                layers=rng.randint(1, 4), Hkv=min(Hkv, 4), D=min(D, 128), dtype=dtype, page=min(page, 32))
+
+
+# ---- the sizes of a case, the same whatever the seed -----------------------------------------------------------------------
+
+
+def _requests(c):
+    """[(tokens of its own before the step or -1, rows of the step)] of the case's requests, in no particular order."""
+    R, K, lead = c["R"], c["K"], c["lead"]
+    got = []
+    for i in range(R):
+        drafts = ((i * 7 + 3) % R) * (K + 1) // R if lead else 1 + ((i * 7 + 3) % R) * K // R
+        n_own = -1 if i < c["vacant"] else max(0, round(c["own_len"] * (i + 1) / R) - (0 if lead else 1))
+        got.append((n_own, (drafts if lead else min(drafts, K)) + lead))
+    return got
+
+
+def work(c):
+    if c["op"] == "attend":
+        H, Hkv, D, sh = c["H"], c["Hkv"], c["D"], c["shared"]
+        keys = pairs = rows = 0
+        for n_own, n in _requests(c):
+            if n_own >= 0:
+                keys += n_own + n
+                pairs += n * (sh + n_own) + n * (n + 1) // 2
+            rows += n
+        keys += sh * c["groups"]
+        return {"bytes": 2 * keys * Hkv * D * 2 + rows * H * (2 * D * 2 + 4), "flops": 4.0 * pairs * H * D}
+    if c["op"] == "append":
+        return {"bytes": sum(n for n_own, n in _requests(c) if n_own >= 0) * c["Hkv"] * c["D"] * 2 * 2 * 2, "flops": 0}
+    if c["op"] == "turnover":
+        n_pages = _turnover_pages(c)
+        return {"bytes": 4.0 * (n_pages + 4 * c["R"]), "flops": 0}
+    if c["op"] == "fork":
+        page_bytes = c["layers"] * c["Hkv"] * c["page"] * c["D"] * 2 * 2
+        copied = shared = 0
+        for f in range(c["F"]):
+            n = _parent_len(c, f % c["S"])
+            whole, part = n // c["page"], 1 if n % c["page"] else 0
+            copied += whole + part if c["deep"] else part
+            shared += whole + part
+        return {"bytes": 2.0 * copied * page_bytes + 12.0 * shared, "flops": 0}
+    live = round(c["n_pages"] * c["live"])
+    page_bytes = c["layers"] * c["Hkv"] * c["page"] * c["D"] * 2 * 2
+    moved = live * (c["n_pages"] - live) / c["n_pages"]  # as many as fall behind the first `live` pages by chance
+    return {"bytes": 2.0 * moved * page_bytes + 12.0 * c["n_pages"] + 8.0 * live, "flops": 0}
+
+
+def _parent_len(c, s):
+    return max(1, c["own_len"] - 37 * s * c["own_len"] // (40 * c["S"]))
+
+
+def _turnover_pages(c):
+    kept = sum(-(-max(n, 0) // c["page"]) for n, _ in _requests(c))
+    stale = sum(1 for i, (n, _) in enumerate(_requests(c)) if n >= 0 and i % 3 == 0)
+    return kept + stale + 1 + int(c["spare"] * kept)
+
+
+# ---- inputs -----------------------------------------------------------------------------------------------------------------
+
+
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(int(seed))
+
+
+def _i32(x):
+    return torch.as_tensor(x, dtype=torch.int32).to(DEV)
+
+
+def _normal(g, shape, dtype):
+    return torch.randn(shape, generator=g, device=DEV, dtype=torch.float32).to(dtype)
+
+
+def _kv(g, c, layers, n_pages):
+    """The whole cache filled: what lies in free pages and behind a sequence's end is some old token's."""
+    pb, D, t = c["page"] // 16, c["D"], DTYPES[c["dtype"]]
+    k = torch.empty((layers, n_pages, c["Hkv"], pb, D // 8, 16, 8), dtype=t, device=DEV)
+    v = torch.empty((layers, n_pages, c["Hkv"], pb, D, 16), dtype=t, device=DEV)
+    for x in (k, v):
+        x.normal_(generator=g)
+    return k, v
+
+
+def _handle(s, layers, n_pages, c, width):
+    """The framework's handle of the cache, which a user's program keeps as long as the buffers."""
+    from confidence_scheduled_verification_amd import binding as B
+    return B.PagedCache(layers, n_pages, c["page"], c.get("Hkv", 1), c.get("D", 64),
+                        B.DSPARK_F16 if c.get("dtype") == "fp16" else B.DSPARK_BF16, s["table"].shape[0], width,
+                        k=s.get("k"), v=s.get("v"), table=s["table"], len=s["len"], ref=s["ref"])
+
+
+def _place(order, pages_of, rows, width, n_pages):
+    """A table whose rows hold `pages_of[r]` pages each, dealt from `order`, and the counts."""
+    table = torch.full((rows, width), -1, dtype=torch.int32)
+    at = 0
+    for r, n in enumerate(pages_of):
+        table[r, :n] = order[at:at + n]
+        at += n
+    ref = torch.zeros(n_pages, dtype=torch.int32)
+    ref[order[:at].long()] = 1
+    return table, ref
+
+
+def _offsets(reqs, lead):
+    off = [0]
+    for _, n in reqs:
+        off.append(off[-1] + n - lead)
+    return _i32(off)
+
+
+def prepare(case, seed):
+    c, g = case, _gen(seed)
+    cpu = torch.Generator().manual_seed(int(seed) + 1)
+    s = {"op": c["op"], "case": c}
+    page = c["page"]
+    if c["op"] in ("attend", "append", "turnover"):
+        reqs = _requests(c)
+        reqs = [reqs[i] for i in torch.randperm(len(reqs), generator=cpu).tolist()]
+        R, lead = c["R"], c["lead"]
+        s.update(lead=lead, max_new=c["K"] + lead, offsets=_offsets(reqs, lead))
+    if c["op"] in ("attend", "append"):
+        sh, n_groups = c.get("shared", 0), c.get("groups", 0)
+        sp = sh // page
+        pages_of = [0 if n < 0 else -(-(n + m) // page) for n, m in reqs]
+        width = sp + max(pages_of) + 2
+        n_pages = sum(pages_of) + sp * n_groups + 3
+        order = torch.randperm(n_pages, generator=cpu).to(torch.int32)
+        own_table, ref = _place(order[sp * n_groups:], pages_of, R, width, n_pages)
+        table = own_table
+        s["rows"] = R * s["max_new"]
+        if n_groups:
+            bound = [i * R // n_groups for i in range(n_groups + 1)]
+            shared = order[:sp * n_groups].reshape(n_groups, sp)
+            table = torch.full((R, width), -1, dtype=torch.int32)
+            for i in range(n_groups):
+                table[bound[i]:bound[i + 1], :sp] = shared[i]
+                ref[shared[i].long()] += bound[i + 1] - bound[i]
+            table[:, sp:] = own_table[:, :width - sp]
+            s.update(group_off=_i32(bound), shared_table=shared.contiguous().to(DEV), shared_pages=_i32([sp] * n_groups))
+            width_g = max(b - a for a, b in zip(bound, bound[1:]))
+            s.update(sp=sp, n_groups=n_groups, width_g=width_g)
+        s.update(own_pages=max(1, max(pages_of)), table=table.to(DEV), ref=ref.to(DEV),
+                 len=_i32([n if n < 0 else n + sp * page * bool(n_groups) for n, _ in reqs]))
+        s["k"], s["v"] = _kv(g, c, 1, n_pages)
+        H, Hkv, D, t = c.get("H", 0), c["Hkv"], c["D"], DTYPES[c["dtype"]]
+        qkv = _normal(g, (s["rows"], (H + 2 * Hkv) * D), t)  # as one projection gives them
+        s["q"] = qkv[:, :H * D].unflatten(1, (H, D)) if H else None
+        s["k_new"] = qkv[:, H * D:(H + Hkv) * D].unflatten(1, (Hkv, D))
+        s["v_new"] = qkv[:, (H + Hkv) * D:].unflatten(1, (Hkv, D))
+        if c["op"] == "attend":
+            s["out"] = torch.zeros((s["rows"], H, D), dtype=t, device=DEV)
+            s["lse"] = torch.zeros((s["rows"], H), dtype=torch.float32, device=DEV)
+            s["scale"] = 1.0 / math.sqrt(D)
+        if own:
+            from confidence_scheduled_verification_amd import binding as B
+            s["cache"] = _handle(s, 1, n_pages, c, width)
+            if c["op"] == "attend":
+                s["ws"] = B.cache_workspace(s["cache"], R, H, s["max_new"], n_groups)
+        return s
+    if c["op"] == "turnover":
+        n_pages = _turnover_pages(c)
+        base = [-(-max(n, 0) // page) for n, _ in reqs]
+        at = {i: j for j, i in enumerate([i for i, (n, _) in enumerate(reqs) if n >= 0])}
+        n_stale = sum(1 for i, (n, _) in enumerate(_requests(c)) if n >= 0 and i % 3 == 0)
+        pages_of = [b + (1 if i in at and at[i] < n_stale else 0) for i, b in enumerate(base)]
+        width = max(base) + 2 + -(-s["max_new"] // page)
+        order = torch.randperm(n_pages, generator=cpu).to(torch.int32)
+        table, ref = _place(order, pages_of, c["R"], width, n_pages)
+        s.update(table=table.to(DEV), ref=ref.to(DEV), len=_i32([n for n, _ in reqs]), keep=_i32([n for n, _ in reqs]),
+                 granted=torch.zeros(c["R"], dtype=torch.int32, device=DEV))
+    elif c["op"] == "fork":
+        S, F = c["S"], c["F"]
+        lens = [_parent_len(c, i) for i in range(S)]
+        width = -(-max(lens) // page) + 1
+        pages_of = [-(-n // page) for n in lens]
+        extra = sum(pages_of[f % S] if c["deep"] else 1 for f in range(F))
+        n_pages = sum(pages_of) + extra + 5
+        order = torch.randperm(n_pages, generator=cpu).to(torch.int32)
+        rows = torch.randperm(S + F, generator=cpu)
+        by_row = [0] * (S + F)
+        ln = [0] * (S + F)
+        for i in range(S):
+            by_row[int(rows[i])] = pages_of[i]
+            ln[int(rows[i])] = lens[i]
+        table, ref = _place(order, by_row, S + F, width, n_pages)
+        s.update(table=table.to(DEV), ref=ref.to(DEV), len=_i32(ln), src=_i32([int(rows[f % S]) for f in range(F)]),
+                 dst=_i32(rows[S:]), zero=torch.zeros(F, dtype=torch.int32, device=DEV), deep=c["deep"],
+                 forked=torch.zeros(F, dtype=torch.int32, device=DEV))
+        s["k"], s["v"] = _kv(g, c, c["layers"], n_pages)
+    else:
+        n_pages, rows = c["n_pages"], c["rows"]
+        live = round(n_pages * c["live"])
+        pages_of = [live * (i + 1) // rows - live * i // rows for i in range(rows)]
+        width = max(pages_of) + 1
+        table, ref = _place(torch.randperm(n_pages, generator=cpu).to(torch.int32), pages_of, rows, width, n_pages)
+        s.update(table=table.to(DEV), ref=ref.to(DEV), len=_i32([n * page for n in pages_of]),
+                 page_map=torch.zeros(n_pages, dtype=torch.int32, device=DEV), n_live=torch.zeros(1, dtype=torch.int32, device=DEV))
+        s.update(table0=s["table"].clone(), ref0=s["ref"].clone())  # as the engine's step found them
+        s["k"], s["v"] = _kv(g, c, c["layers"], n_pages)
+    if own:
+        from confidence_scheduled_verification_amd import binding as B
+        s["cache"] = _handle(s, c.get("layers", 1), n_pages, c, width)
+        s["ws"] = B.pages_workspace(s["cache"], s["table"].shape[0])
+    return s
+
+
+# ---- the plain forms --------------------------------------------------------------------------------------------------------
+
+
+def _rows_of(s):
+    """Request and place of each packed row, whether it belongs to one, and each request's start and count."""
+    R, lead = s["len"].shape[0], s["lead"]
+    off = s["offsets"].long()
+    start = off[:-1] + lead * torch.arange(R, device=DEV)
+    count = off[1:] - off[:-1] + lead
+    t = torch.arange(s["rows"], device=DEV)
+    r = (torch.searchsorted(start, t, right=True) - 1).clamp(0, R - 1)
+    j = t - start[r]
+    return r, j, j < count[r], start, count
+
+
+def _gathered(s, ids):
+    """K and V of pages ids [A, W] as [A, Hkv, W * page, D] in float32."""
+    A = ids.shape[0]
+    Hkv, D = s["k"].shape[2], s["v"].shape[4]
+    ids = ids.clamp(min=0)
+    k = s["k"][0][ids].permute(0, 2, 1, 3, 5, 4, 6).reshape(A, Hkv, -1, D).float()
+    v = s["v"][0][ids].permute(0, 2, 1, 3, 5, 4).reshape(A, Hkv, -1, D).float()
+    return k, v
+
+
+def _attend(s):
+    R, n = s["len"].shape[0], s["max_new"]
+    H, D = s["q"].shape[1:]
+    Hkv, page = s["k"].shape[2], s["case"]["page"]
+    G = H // Hkv
+    row_r, row_j, row_ok, start, count = _rows_of(s)
+    j = torch.arange(n, device=DEV)
+    at = (start[:, None] + j).clamp(max=s["rows"] - 1)
+    q = s["q"][at].float().reshape(R, n, Hkv, G, D).permute(0, 2, 1, 3, 4).reshape(R, Hkv, n * G, D) * s["scale"]
+    ln = s["len"].long()
+    sp = s.get("sp", 0)
+    k, v = _gathered(s, s["table"][:, sp:sp + s["own_pages"]].long())
+    x = q @ k.transpose(2, 3)
+    pos = sp * page + torch.arange(x.shape[3], device=DEV)
+    sees = (pos <= (ln[:, None] + j)[:, :, None]) & (ln >= 0)[:, None, None]
+    x = x.masked_fill(~sees[:, None, :, None].expand(R, 1, n, G, -1).reshape(R, 1, n * G, -1), -math.inf)
+    m = x.amax(3, keepdim=True)
+    if sp:
+        first, last = s["group_off"][:-1].long(), s["group_off"][1:].long()
+        of = torch.searchsorted(last, torch.arange(R, device=DEV), right=True)
+        within = torch.arange(R, device=DEV) - first[of]
+        pick = (first[:, None] + torch.arange(s["width_g"], device=DEV)).clamp(max=R - 1)
+        kg, vg = _gathered(s, s["shared_table"].long())
+        qg = q[pick].permute(0, 2, 1, 3, 4).reshape(s["n_groups"], Hkv, -1, D)
+        y = qg @ kg.transpose(2, 3)
+        my = y.amax(3, keepdim=True)
+        e = torch.exp(y - my)
+        parts = [e @ vg, e.sum(3, keepdim=True), my]
+        oy, ly, my = (p.reshape(s["n_groups"], Hkv, s["width_g"], n * G, -1)[of, :, within] for p in parts)
+        my = my.masked_fill((ln < 0)[:, None, None, None], -math.inf)
+        top = torch.maximum(m, my)
+    else:
+        top = m
+    safe = top.masked_fill(top == -math.inf, 0.0)
+    e = torch.exp(x - safe)
+    o, l = e @ v, e.sum(3, keepdim=True)
+    if sp:
+        w = torch.exp(my - safe)
+        o, l = o + w * oy, l + w * ly
+    o = torch.where(l > 0, o / l, torch.zeros((), device=DEV))
+    lse = (safe + torch.log(l)).reshape(R, Hkv, n, G).permute(0, 2, 1, 3).reshape(R, n, H)
+    o = o.reshape(R, Hkv, n, G, D).permute(0, 2, 1, 3, 4).reshape(R, n, H, D)
+    jj = row_j.clamp(0, n - 1)
+    s["out"].copy_(torch.where(row_ok[:, None, None], o[row_r, jj].to(s["out"].dtype), s["out"]))
+    s["lse"].copy_(torch.where(row_ok[:, None], lse[row_r, jj], s["lse"]))
+    return {"out": s["out"], "lse": s["lse"]}
+
+
+def _append(s):
+    row_r, row_j, ok, _, _ = _rows_of(s)
+    ln = s["len"].long()
+    page = s["case"]["page"]
+    t = (ok & (ln[row_r] >= 0)).nonzero()[:, 0]
+    r = row_r[t]
+    p = ln[r] + row_j[t]
+    ids = s["table"][r, p // page].long()
+    blk, slot = p % page // 16, p % 16
+    Hkv, D = s["k"].shape[2], s["v"].shape[4]
+    s["k"][0][ids, :, blk, :, slot] = s["k_new"][t].unflatten(2, (D // 8, 8))
+    s["v"][0][ids, :, blk, :, slot] = s["v_new"][t]
+    return {"k": s["k"], "v": s["v"]}
+
+
+def _add(ref, ids, takes, by):
+    ref.scatter_add_(0, ids.clamp(min=0).long().flatten(), (takes.int() * by).flatten())
+
+
+def _trim(s, rows, keep):
+    page = s["case"]["page"]
+    old = s["table"] if rows is None else s["table"][rows]
+    have = torch.arange(old.shape[1], device=DEV)
+    drop = (have >= ((keep.clamp(min=0) + page - 1) // page)[:, None]) & (old >= 0)
+    _add(s["ref"], old, drop, -1)
+    new = old.masked_fill(drop, -1)
+    ln = s["len"] if rows is None else s["len"][rows]
+    ln = torch.where(keep < 0, -1, torch.minimum(ln, keep))
+    if rows is None:
+        s["table"].copy_(new)
+        s["len"].copy_(ln)
+    else:
+        s["table"][rows] = new
+        s["len"][rows] = ln
+
+
+def _lowest_free(ref):
+    return torch.argsort((ref != 0).to(torch.uint8), stable=True), (ref == 0).sum()
+
+
+def _turnover(s):
+    page = s["case"]["page"]
+    _trim(s, None, s["keep"])
+    ln, off = s["len"].long(), s["offsets"].long()
+    n = off[1:] - off[:-1] + s["lead"]
+    have = (s["table"] >= 0).sum(1)
+    need = torch.where(ln < 0, 0, ((ln + n + page - 1) // page - have).clamp(min=0))
+    before = need.cumsum(0) - need
+    order, n_free = _lowest_free(s["ref"])
+    ok = (ln >= 0) & ((need == 0) | (before + need <= n_free))
+    place = torch.arange(s["table"].shape[1], device=DEV) - have[:, None]
+    takes = (place >= 0) & (place < need[:, None]) & ok[:, None]
+    ids = order[(before[:, None] + place).clamp(0, order.shape[0] - 1)].int()
+    s["table"].copy_(torch.where(takes, ids, s["table"]))
+    _add(s["ref"], ids, takes, 1)
+    s["granted"].copy_(ok.int())
+    return {"table": s["table"], "len": s["len"], "ref": s["ref"], "granted": s["granted"]}
+
+
+def _fork(s):
+    page = s["case"]["page"]
+    dst, src = s["dst"].long(), s["src"].long()
+    _trim(s, dst, s["zero"])
+    ln = s["len"][src].long()
+    whole = torch.zeros_like(ln) if s["deep"] else ln // page
+    total = (ln + page - 1) // page
+    need = total - whole
+    before = need.cumsum(0) - need
+    order, n_free = _lowest_free(s["ref"])
+    ok = before + need <= n_free
+    at = torch.arange(s["table"].shape[1], device=DEV)
+    from_ = s["table"][src]
+    shares = (at < whole[:, None]) & ok[:, None]
+    copies = (at >= whole[:, None]) & (at < total[:, None]) & ok[:, None]
+    ids = order[(before[:, None] + at - whole[:, None]).clamp(0, order.shape[0] - 1)].int()
+    s["table"][dst] = torch.where(shares, from_, torch.where(copies, ids, -1))
+    s["len"][dst] = torch.where(ok, ln, 0).int()
+    _add(s["ref"], from_, shares, 1)
+    _add(s["ref"], ids, copies, 1)
+    a, b = from_[copies].long(), ids[copies].long()
+    s["k"][:, b] = s["k"][:, a]
+    s["v"][:, b] = s["v"][:, a]
+    s["forked"].copy_(ok.int())
+    return {"table": s["table"], "len": s["len"], "ref": s["ref"], "forked": s["forked"], "k": s["k"], "v": s["v"]}
+
+
+def _compact(s):
+    s["table"].copy_(s["table0"])
+    s["ref"].copy_(s["ref0"])
+    ref = s["ref"]
+    n = ref.shape[0]
+    live = ref > 0
+    n_live = live.sum()
+    at = torch.arange(n, device=DEV)
+    a, b = (live & (at >= n_live)).nonzero()[:, 0], (~live & (at < n_live)).nonzero()[:, 0]
+    page_map = torch.where(live, at, -1)
+    page_map[a] = b
+    s["k"][:, b] = s["k"][:, a]
+    s["v"][:, b] = s["v"][:, a]
+    ref[b] = ref[a]
+    ref[a] = 0
+    t = s["table"].long()
+    s["table"].copy_(torch.where(t >= 0, page_map[t.clamp(min=0)], -1))
+    s["page_map"].copy_(page_map)
+    s["n_live"].copy_(n_live)
+    return {"table": s["table"], "ref": s["ref"], "page_map": s["page_map"], "n_live": s["n_live"], "k": s["k"], "v": s["v"]}
+
+
+def run(s):
+    if own:
+        return _own(s)
+    return {"attend": _attend, "append": _append, "turnover": _turnover, "fork": _fork, "compact": _compact}[s["op"]](s)
+
+
+def _own(s):
+    from confidence_scheduled_verification_amd import binding as B
+    h, op = s["cache"], s["op"]
+    if op == "attend":
+        shared = (s["group_off"], s["shared_table"], s["shared_pages"]) if "sp" in s else None
+        B.dspark_cache_attend(h, 0, s["q"], s["offsets"], s["lead"], s["max_new"], s["scale"], s["out"], lse=s["lse"],
+                              shared=shared, ws=s["ws"])
+        return {"out": s["out"], "lse": s["lse"]}
+    if op == "append":
+        B.dspark_cache_append(h, 0, s["k_new"], s["v_new"], s["offsets"], s["lead"], s["max_new"])
+        return {"k": s["k"], "v": s["v"]}
+    if op == "turnover":
+        B.dspark_pages_trim(h, None, s["keep"])
+        B.dspark_pages_reserve(h, s["offsets"], s["lead"], s["granted"], ws=s["ws"])
+        return {"table": s["table"], "len": s["len"], "ref": s["ref"], "granted": s["granted"]}
+    if op == "fork":
+        B.dspark_pages_trim(h, s["dst"], s["zero"])
+        B.dspark_pages_fork(h, s["src"], s["dst"], s["forked"], deep=s["deep"], ws=s["ws"])
+        return {"table": s["table"], "len": s["len"], "ref": s["ref"], "forked": s["forked"], "k": s["k"], "v": s["v"]}
+    s["table"].copy_(s["table0"])
+    s["ref"].copy_(s["ref0"])
+    B.dspark_pages_compact(h, s["page_map"], s["n_live"], ws=s["ws"])
+    return {"table": s["table"], "ref": s["ref"], "page_map": s["page_map"], "n_live": s["n_live"], "k": s["k"], "v": s["v"]}
+
+
+# ---- the definitions, in 64 bits --------------------------------------------------------------------------------------------
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    f = {"attend": _exact_attend, "append": _exact_append, "turnover": _exact_turnover, "fork": _exact_fork,
+         "compact": _exact_compact}[s["op"]]
+    return f(s, case)
+
+
+def _token(c, p):
+    """Where position p of a row lies: page in the row, block and slot in the page."""
+    return p // c["page"], p % c["page"] // 16, p % 16
+
+
+def _exact_attend(s, c):
+    out, lse = s["out"].double(), s["lse"].double()
+    off, ln, table = s["offsets"].tolist(), s["len"].tolist(), s["table"].long()
+    H, Hkv, D, page = c["H"], c["Hkv"], c["D"], c["page"]
+    for r in range(c["R"]):
+        a, b = off[r] + c["lead"] * r, off[r + 1] + c["lead"] * (r + 1)
+        if a == b:
+            continue
+        if ln[r] < 0:
+            out[a:b], lse[a:b] = 0.0, -math.inf
+            continue
+        T = ln[r] + b - a
+        ids = table[r, :-(-T // page)]
+        for h in range(Hkv):  # K [T, D] and V [D, T] of one head
+            K = s["k"][0, ids, h].double().movedim(3, 2).flatten(3).flatten(0, 2)[:T]
+            V = s["v"][0, ids, h].double().movedim(2, 0).flatten(1)[:, :T]
+            hs = slice(h * (H // Hkv), (h + 1) * (H // Hkv))
+            z = torch.tensordot(s["q"][a:b, hs].double(), K, dims=([2], [1])) * (1.0 / math.sqrt(D))
+            late = torch.arange(T, device=DEV)[None, None] > ln[r] + torch.arange(b - a, device=DEV)[:, None, None]
+            z[late.expand_as(z)] = -math.inf
+            ls = torch.logsumexp(z, 2)
+            lse[a:b, hs] = ls
+            out[a:b, hs] = torch.tensordot(torch.exp(z - ls[:, :, None]), V, dims=([2], [1]))
+    return {"out": out, "lse": lse}
+
+
+def _exact_append(s, c):
+    k, v = s["k"].cpu(), s["v"].cpu()
+    off, ln, table = s["offsets"].tolist(), s["len"].tolist(), s["table"].tolist()
+    kn, vn = s["k_new"].cpu(), s["v_new"].cpu()
+    for r in range(c["R"]):
+        a, b = off[r] + c["lead"] * r, off[r + 1] + c["lead"] * (r + 1)
+        for t in range(a, b if ln[r] >= 0 else a):
+            i, blk, slot = _token(c, ln[r] + t - a)
+            k[0, table[r][i], :, blk, :, slot, :] = kn[t].reshape(c["Hkv"], -1, 8)
+            v[0, table[r][i], :, blk, :, slot] = vn[t]
+    return {"k": k, "v": v}
+
+
+def _held(row):
+    return [p for p in row if p >= 0]
+
+
+def _exact_turnover(s, c):
+    table, ln, ref = s["table"].tolist(), s["len"].tolist(), s["ref"].tolist()
+    off, keep, width = s["offsets"].tolist(), s["keep"].tolist(), s["table"].shape[1]
+    rows = [_held(x) for x in table]
+    for r, row in enumerate(rows):
+        while len(row) > -(-max(keep[r], 0) // c["page"]):
+            ref[row.pop()] -= 1
+        ln[r] = min(ln[r], keep[r])
+    free = [p for p, n in enumerate(ref) if n == 0]
+    told, granted = 0, []
+    for r, row in enumerate(rows):
+        need = 0 if ln[r] < 0 else max(0, -(-(ln[r] + off[r + 1] - off[r] + c["lead"]) // c["page"]) - len(row))
+        granted.append(int(ln[r] >= 0 and (need == 0 or told + need <= len(free))))
+        if granted[-1]:
+            for p in free[told:told + need]:
+                row.append(p)
+                ref[p] = 1
+        told += need
+    table = [row + [-1] * (width - len(row)) for row in rows]
+    return {"table": _i32(table), "len": _i32(ln), "ref": _i32(ref), "granted": _i32(granted)}
+
+
+def _exact_fork(s, c):
+    table, ln, ref, width = [_held(x) for x in s["table"].tolist()], s["len"].tolist(), s["ref"].tolist(), s["table"].shape[1]
+    src, dst = s["src"].tolist(), s["dst"].tolist()
+    for d in dst:
+        for p in table[d]:
+            ref[p] -= 1
+        table[d], ln[d] = [], 0
+    free = [p for p, n in enumerate(ref) if n == 0]
+    told, forked, pairs = 0, [], []
+    for a, d in zip(src, dst):
+        fresh = len(table[a]) if c["deep"] else (1 if ln[a] % c["page"] else 0)
+        forked.append(int(told + fresh <= len(free)))
+        if forked[-1]:
+            kept = table[a][:len(table[a]) - fresh]
+            new = free[told:told + fresh]
+            pairs += list(zip(table[a][len(kept):], new))
+            for p in kept + new:
+                ref[p] += 1
+            table[d], ln[d] = kept + new, ln[a]
+        told += fresh
+    k, v = s["k"].clone(), s["v"].clone()
+    for a, b in pairs:
+        k[:, b], v[:, b] = k[:, a], v[:, a]
+    table = [row + [-1] * (width - len(row)) for row in table]
+    return {"table": _i32(table), "len": _i32(ln), "ref": _i32(ref), "forked": _i32(forked), "k": k, "v": v}
+
+
+def _exact_compact(s, c):
+    ref = s["ref"].tolist()
+    live = [p for p, n in enumerate(ref) if n > 0]
+    holes = [p for p in range(len(live)) if ref[p] == 0]
+    page_map = {p: p for p in live}
+    for a, b in zip([p for p in live if p >= len(live)], holes):
+        page_map[a] = b
+    k, v = s["k"].clone(), s["v"].clone()
+    new_ref = [0] * len(ref)
+    for a, b in page_map.items():
+        new_ref[b] = ref[a]
+        if a != b:
+            k[:, b], v[:, b] = k[:, a], v[:, a]
+    table = [[page_map.get(p, -1) for p in row] for row in s["table"].tolist()]
+    return {"table": _i32(table), "ref": _i32(new_ref), "page_map": _i32([page_map.get(p, -1) for p in range(len(ref))]),
+            "n_live": _i32([len(live)]), "k": k, "v": v}
