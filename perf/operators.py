@@ -179,7 +179,7 @@ def _handle(s, layers, n_pages, c, width):
     from confidence_scheduled_verification_amd import binding as B
     return B.PagedCache(layers, n_pages, c["page"], c.get("Hkv", 1), c.get("D", 64),
                         B.DSPARK_F16 if c.get("dtype") == "fp16" else B.DSPARK_BF16, s["table"].shape[0], width,
-                        k=s.get("k"), v=s.get("v"), table=s["table"], len=s["len"], ref=s["ref"])
+                        k=s.get("k"), v=s.get("v"), table=s["table"], len=s["len"], ref=s["ref"], data="k" in s)
 
 
 def _place(order, pages_of, rows, width, n_pages):
