@@ -19,11 +19,15 @@ LIB_PATH = os.path.join(PKG, "libdspark.so")
 
 DSPARK_F32 = 0
 DSPARK_BF16 = 1
+DSPARK_F16 = 2  # the paged cache alone
 STATUS_PREV_CLAMPED = 1
 STATUS_CONF_SANITIZED = 2
 STATUS_COST_INVALID = 4
 STATUS_SYNC_TIMEOUT = 8
 STATUS_BAD_ALLOCATION = 16
+STATUS_BAD_PAGE = 32
+STATUS_BAD_ROW = 64
+STATUS_NO_PAGES = 128
 LAUNCH_RESIDENT = 0
 LAUNCH_COOPERATIVE = 1
 MAX_SLOTS = 16384
@@ -39,7 +43,9 @@ EXPORTS = ["dspark_last_error", "dspark_version", "dspark_workspace_bytes", "dsp
            "dspark_chain", "dspark_chain_sample", "dspark_survival", "dspark_topb_select", "dspark_choose_budget", "dspark_allocate",
            "dspark_step", "dspark_step_sized", "dspark_step_static", "dspark_schedule", "dspark_accept_greedy", "dspark_set_timing_events",
            "dspark_force_monotone", "dspark_profile_shapes", "dspark_build_cost_table", "dspark_set_launch_mode",
-           "dspark_get_launch_mode"]
+           "dspark_get_launch_mode", "dspark_pages_workspace_bytes", "dspark_pages_reserve", "dspark_pages_trim",
+           "dspark_pages_commit", "dspark_pages_fork", "dspark_pages_compact", "dspark_cache_append",
+           "dspark_cache_attend_workspace_bytes", "dspark_cache_attend"]
 
 # int fn(int shape, void* user, void* stream)
 SHAPE_FN = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p)
@@ -50,6 +56,13 @@ class dspark_markov_t(ctypes.Structure):
     _fields_ = [("magic", ctypes.c_uint64), ("A", ctypes.c_void_p), ("Bmat", ctypes.c_void_p),
                 ("state", ctypes.c_void_p), ("state_bytes", ctypes.c_size_t), ("V", ctypes.c_int32),
                 ("rank", ctypes.c_int32), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class dspark_cache_t(ctypes.Structure):
+    """The C description of a paged cache (include/dspark.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p), ("len", ctypes.c_void_p),
+                ("ref", ctypes.c_void_p)] + [(n, ctypes.c_int32) for n in (
+                    "layers", "n_pages", "page_size", "n_kv_heads", "head_dim", "dtype", "rows", "width")]
 
 
 class DSparkError(RuntimeError):
@@ -102,9 +115,23 @@ def lib():
         L.dspark_force_monotone.argtypes = [p, i]
         L.dspark_profile_shapes.argtypes = [SHAPE_FN, p, p, i, i, i, p, p]
         L.dspark_build_cost_table.argtypes = [p, i, p, i, i, p, i]
+        i64 = ctypes.c_int64
+        L.dspark_pages_workspace_bytes.restype = sz
+        L.dspark_pages_workspace_bytes.argtypes = [i, i]
+        L.dspark_pages_reserve.argtypes = [p, p, i, i, p, p, p, sz, p]
+        L.dspark_pages_trim.argtypes = [p, p, i, p, p, p]
+        L.dspark_pages_commit.argtypes = [p, p, i, i, p, p]
+        L.dspark_pages_fork.argtypes = [p, p, p, i, i, p, p, p, sz, p]
+        L.dspark_pages_compact.argtypes = [p, p, p, p, p, sz, p]
+        L.dspark_cache_append.argtypes = [p, i, p, i64, p, i64, i, p, i, i, i, p, p]
+        L.dspark_cache_attend_workspace_bytes.restype = sz
+        L.dspark_cache_attend_workspace_bytes.argtypes = [i, i, i, i, i]
+        L.dspark_cache_attend.argtypes = [p, i, p, i64, i, i, p, i, i, i, ctypes.c_float, i, p, p, i, p, p, i64, p, p, p,
+                                          sz, p]
         for name in EXPORTS:
             if name not in ("dspark_last_error", "dspark_version", "dspark_workspace_bytes",
-                            "dspark_markov_state_bytes"):
+                            "dspark_markov_state_bytes", "dspark_pages_workspace_bytes",
+                            "dspark_cache_attend_workspace_bytes"):
                 getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -431,6 +458,180 @@ def dspark_accept_greedy(ver_tokens, offsets, target, R: int, K: int, accept_len
         raise ValueError("dspark_accept_greedy: inconsistent sizes")
     _check(lib().dspark_accept_greedy(_p(ver_tokens), _p(offsets), _p(target), R, K, _p(accept_len),
                                       _p(next_prev0), _p(out_tokens), _p(status), _stream(stream)))
+
+
+class PagedCache:
+    """A paged cache of keys and values (include/dspark.h, dspark_cache_t): `k` and `v` (every
+    layer's pages), `table` [rows, width] (page ids, -1 for none), `len` [rows] (tokens kept, -1
+    for a vacant row) and `ref` [n_pages] (table rows that hold each page).  Buffers that are
+    not given are allocated, empty: no pages held, every row vacant.  With data=False the cache
+    is the bookkeeping alone (reserve, commit and trim).  The buffers are referenced here; the
+    caller reads and writes `len` and `table` as tensors."""
+
+    def __init__(self, layers: int, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, dtype: int,
+                 rows: int, width: int, k=None, v=None, table=None, len=None, ref=None, device="cuda", data: bool = True):
+        torch = _torch()
+        if dtype not in (DSPARK_BF16, DSPARK_F16):
+            raise ValueError("PagedCache: dtype must be DSPARK_BF16 or DSPARK_F16")
+        if min(layers, n_pages, page_size, n_kv_heads, head_dim, width) < 1 or rows < 0 or page_size % 16 or head_dim % 8:
+            raise ValueError("PagedCache: sizes must be positive, page_size a multiple of 16, head_dim of 8")
+        for t in (k, v, table, len, ref):
+            if t is not None:
+                device = t.device
+        device = torch.device(device)
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        self.torch_dtype = torch.bfloat16 if dtype == DSPARK_BF16 else torch.float16
+        shapes = dict(k=(layers, n_pages, n_kv_heads, page_size // 16, head_dim // 8, 16, 8),
+                      v=(layers, n_pages, n_kv_heads, page_size // 16, head_dim, 16),
+                      table=(rows, width), len=(rows,), ref=(n_pages,))
+        given = dict(k=k, v=v, table=table, len=len, ref=ref)
+        for name, want in shapes.items():
+            dt = self.torch_dtype if name in "kv" else torch.int32
+            t = given[name]
+            if t is None and (data or name not in "kv"):
+                t = torch.zeros(want, dtype=dt, device=device) if name in ("k", "v", "ref") else \
+                    torch.full(want, -1, dtype=dt, device=device)
+            if t is not None:
+                if tuple(t.shape) != want or t.dtype != dt or not t.is_contiguous() or t.device != device:
+                    raise ValueError(f"PagedCache: {name} must be contiguous {dt} {list(want)} on {device}, "
+                                     f"got {t.dtype} {list(t.shape)} on {t.device}")
+            setattr(self, name, t)
+        self.layers, self.n_pages, self.page_size, self.n_kv_heads, self.head_dim, self.dtype = (
+            layers, n_pages, page_size, n_kv_heads, head_dim, dtype)
+        self.rows, self.width, self.device = rows, width, self.table.device
+        self.handle = dspark_cache_t(_p(self.k), _p(self.v), _p(self.table), _p(self.len), _p(self.ref), layers, n_pages,
+                                     page_size, n_kv_heads, head_dim, dtype, rows, width)
+        self._ref = ctypes.byref(self.handle)
+
+
+def _on(cache: PagedCache, what: str, ints=(), others=()):
+    """The cache's device is the current one, and every tensor of the call lies there; `ints` are
+    int32 and densely packed."""
+    torch = _torch()
+    for t in ints:
+        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
+            raise ValueError(f"{what}: index tensors must be contiguous int32")
+    for t in (*ints, *others):
+        if t is not None and t.device != cache.device:
+            raise ValueError(f"{what}: a tensor on {t.device}, the cache is on {cache.device}")
+    if cache.device.type != "cuda" or cache.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: the cache is on {cache.device}, which is not the current GPU")
+
+
+def pages_workspace(cache: PagedCache, n: int):
+    """Workspace of reserve, fork (up to n requests or forks) and compact."""
+    nbytes = int(lib().dspark_pages_workspace_bytes(cache.n_pages, n))
+    return _torch().empty(nbytes // 4, dtype=_torch().int32, device=cache.device)
+
+
+def cache_workspace(cache: PagedCache, R: int, H: int, max_new: int, n_groups: int = 0):
+    """Workspace of dspark_cache_attend for up to R requests of up to max_new rows."""
+    nbytes = int(lib().dspark_cache_attend_workspace_bytes(R, H, cache.head_dim, max_new, n_groups))
+    return _torch().empty((nbytes + 15) // 16 * 4, dtype=_torch().int32, device=cache.device)
+
+
+def _offsets_rows(cache: PagedCache, offsets, what: str) -> int:
+    if offsets.dim() != 1 or not 1 <= offsets.shape[0] <= cache.rows + 1:
+        raise ValueError(f"{what}: offsets must be [R+1] with R at most the cache's {cache.rows} rows")
+    return offsets.shape[0] - 1
+
+
+def dspark_pages_reserve(cache: PagedCache, offsets, lead: int, granted, ws, status=None, stream=None):
+    """Pages for a step's rows, the lowest free ones in the order of the requests."""
+    R = _offsets_rows(cache, offsets, "dspark_pages_reserve")
+    _shape(granted, (R,), "dspark_pages_reserve: granted")
+    _on(cache, "dspark_pages_reserve", (offsets, granted), (ws, status))
+    _check(lib().dspark_pages_reserve(cache._ref, _p(offsets), lead, R, _p(granted), _p(status), _p(ws), _ws_bytes(ws),
+                                      _stream(stream)))
+
+
+def dspark_pages_trim(cache: PagedCache, rows=None, keep=None, status=None, stream=None):
+    """Table rows (all of them where `rows` is None) cut back to `keep` tokens each (None: freed;
+    negative: freed and vacant)."""
+    n = cache.rows if rows is None else rows.numel()
+    if keep is not None:
+        _shape(keep, (n,), "dspark_pages_trim: keep")
+    _on(cache, "dspark_pages_trim", (rows, keep), (status,))
+    _check(lib().dspark_pages_trim(cache._ref, _p(rows), n, _p(keep), _p(status), _stream(stream)))
+
+
+def dspark_pages_commit(cache: PagedCache, accept_len, lead: int, status=None, stream=None):
+    """After dspark_accept_greedy: the accepted rows stay, the pages past them are let go."""
+    if accept_len.dim() != 1 or accept_len.shape[0] > cache.rows:
+        raise ValueError(f"dspark_pages_commit: accept_len must be [R] with R at most {cache.rows}")
+    _on(cache, "dspark_pages_commit", (accept_len,), (status,))
+    _check(lib().dspark_pages_commit(cache._ref, _p(accept_len), lead, accept_len.shape[0], _p(status), _stream(stream)))
+
+
+def dspark_pages_fork(cache: PagedCache, src, dst, forked, ws, deep: bool = False, status=None, stream=None):
+    """Rows dst continue rows src: whole pages shared and the last one copied (deep: all copied)."""
+    _shape(dst, (src.numel(),), "dspark_pages_fork: dst")
+    _shape(forked, (src.numel(),), "dspark_pages_fork: forked")
+    _on(cache, "dspark_pages_fork", (src, dst, forked), (ws, status))
+    _check(lib().dspark_pages_fork(cache._ref, _p(src), _p(dst), src.numel(), int(deep), _p(forked), _p(status), _p(ws),
+                                   _ws_bytes(ws), _stream(stream)))
+
+
+def dspark_pages_compact(cache: PagedCache, page_map, n_live, ws, status=None, stream=None):
+    """Live pages to the front; page_map [n_pages] receives each page's new place (-1: free)."""
+    _shape(page_map, (cache.n_pages,), "dspark_pages_compact: page_map")
+    _shape(n_live, (1,), "dspark_pages_compact: n_live")
+    _on(cache, "dspark_pages_compact", (page_map, n_live), (ws, status))
+    _check(lib().dspark_pages_compact(cache._ref, _p(page_map), _p(n_live), _p(status), _p(ws), _ws_bytes(ws),
+                                      _stream(stream)))
+
+
+def _packed(cache: PagedCache, t, heads, what: str):
+    """Rows of [heads, head_dim] whose heads are densely packed; the stride between rows."""
+    if t.dim() != 3 or t.shape[1:] != (heads, cache.head_dim) or t.dtype != cache.torch_dtype:
+        raise ValueError(f"{what} must be {cache.torch_dtype} [rows, {heads}, {cache.head_dim}], "
+                         f"got {t.dtype} {list(t.shape)}")
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != cache.head_dim)):
+        raise ValueError(f"{what}: each row's heads must be densely packed")
+    return t.stride(0) if t.shape[0] > 1 else heads * cache.head_dim
+
+
+def dspark_cache_append(cache: PagedCache, layer: int, k_new, v_new, offsets, lead: int, max_new: int, status=None,
+                        stream=None):
+    """One layer's K and V of a step's rows into the reserved pages."""
+    R = _offsets_rows(cache, offsets, "dspark_cache_append")
+    ks = _packed(cache, k_new, cache.n_kv_heads, "dspark_cache_append: k_new")
+    vs = _packed(cache, v_new, cache.n_kv_heads, "dspark_cache_append: v_new")
+    if v_new.shape[0] != k_new.shape[0]:
+        raise ValueError("dspark_cache_append: k_new and v_new must have as many rows")
+    _on(cache, "dspark_cache_append", (offsets,), (k_new, v_new, status))
+    _check(lib().dspark_cache_append(cache._ref, layer, _p(k_new), ks, _p(v_new), vs, k_new.shape[0], _p(offsets), lead,
+                                     R, max_new, _p(status), _stream(stream)))
+
+
+def dspark_cache_attend(cache: PagedCache, layer: int, q, offsets, lead: int, max_new: int, scale: float, out, lse=None,
+                        shared=None, ws=None, status=None, stream=None):
+    """One layer's attention of a step's rows.  `shared`: (group_off [n+1], shared_table [n, w],
+    shared_pages [n]) of prefixes that requests share, whose keys are read once for all of them."""
+    what = "dspark_cache_attend"
+    R = _offsets_rows(cache, offsets, what)
+    H = q.shape[1] if q.dim() == 3 else 0
+    qs = _packed(cache, q, H, f"{what}: q")
+    os_ = _packed(cache, out, H, f"{what}: out")
+    if out.shape[0] != q.shape[0]:
+        raise ValueError(f"{what}: q and out must have as many rows")
+    if lse is not None and (tuple(lse.shape) != (q.shape[0], H) or lse.dtype != _torch().float32 or
+                            not lse.is_contiguous()):
+        raise ValueError(f"{what}: lse must be contiguous float32 [{q.shape[0]}, {H}]")
+    n_groups = width = 0
+    off = table = pages = None
+    if shared is not None:
+        off, table, pages = shared
+        if table.dim() != 2:
+            raise ValueError(f"{what}: shared_table must be [groups, width]")
+        n_groups, width = table.shape
+        _shape(off, (n_groups + 1,), f"{what}: group_off")
+        _shape(pages, (n_groups,), f"{what}: shared_pages")
+    _on(cache, what, (offsets, off, table, pages), (q, out, lse, ws, status))
+    _check(lib().dspark_cache_attend(cache._ref, layer, _p(q), qs, q.shape[0], H, _p(offsets), lead, R, max_new,
+                                     float(scale), n_groups, _p(off), _p(table), width, _p(pages), _p(out), os_, _p(lse),
+                                     _p(status), _p(ws), _ws_bytes(ws), _stream(stream)))
 
 
 def dspark_set_launch_mode(mode: int):

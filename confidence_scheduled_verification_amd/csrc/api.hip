@@ -11,18 +11,15 @@
 #include <mutex>
 #include <vector>
 
+#include "cache.h"
 #include "dspark.h"
 #include "kernels.h"
 
 static_assert(dspark::kMaxSlotsWs == DSPARK_MAX_SLOTS, "the step counters are sized for the slot limit");
 
-namespace {
+namespace dspark {
 
 thread_local char g_err[512] = "";
-std::atomic<int> g_launch_mode{DSPARK_LAUNCH_RESIDENT};
-std::atomic<int> g_chain_form{DSPARK_CHAIN_PRUNED};
-thread_local hipEvent_t g_ev_before_chain = nullptr;
-thread_local hipEvent_t g_ev_after_chain = nullptr;
 
 int fail(int code, const char* fmt, ...) {
     va_list ap;
@@ -48,6 +45,19 @@ int num_cu() {
     }
     return cache[dev];
 }
+
+}  // namespace dspark
+
+using dspark::fail;
+using dspark::hip_fail;
+using dspark::num_cu;
+
+namespace {
+
+std::atomic<int> g_launch_mode{DSPARK_LAUNCH_RESIDENT};
+std::atomic<int> g_chain_form{DSPARK_CHAIN_PRUNED};
+thread_local hipEvent_t g_ev_before_chain = nullptr;
+thread_local hipEvent_t g_ev_after_chain = nullptr;
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -161,7 +171,7 @@ int check_sched_scalars(int n, int n_sampling, int T, int num_reqs, const float*
 
 extern "C" {
 
-const char* dspark_last_error(void) { return g_err; }
+const char* dspark_last_error(void) { return dspark::g_err; }
 
 const char* dspark_version(void) { return "dspark-gfx950 0.1"; }
 

@@ -1,0 +1,93 @@
+// Internal launchers of the paged cache (pages.hip, append.hip, attend.hip) and the
+// host helpers that the C entry points share.  Argument checks happen in cache_api.hip.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "dspark.h"
+
+namespace dspark {
+
+// Error text of this thread and the current device's compute units (api.hip).
+int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+int hip_fail(hipError_t e, const char* where);
+int num_cu();
+
+constexpr uint32_t kStatusBadPage = 32u;
+constexpr uint32_t kStatusBadRow = 64u;
+constexpr uint32_t kStatusNoPages = 128u;
+
+constexpr int kBlockTokens = 16;    // tokens of one block of a page
+constexpr int kPageSlice = 4096;    // reference counts that one workgroup counts
+
+inline int page_slices(int n_pages) { return (n_pages + kPageSlice - 1) / kPageSlice; }
+
+// Workspace of reserve, fork and compact, in 32-bit words: each slice's count, then two
+// words per request or fork, then two per page (the copies' sources and destinations).
+inline size_t pages_ws_words(int n_pages, int n) {
+    return (size_t)page_slices(n_pages) + 2 * (size_t)n + 2 * (size_t)n_pages + 8;
+}
+
+hipError_t launch_reserve(const dspark_cache_t& c, const int32_t* offsets, int lead, int R, int32_t* granted,
+                          uint32_t* status, int32_t* ws, hipStream_t s);
+hipError_t launch_trim(const dspark_cache_t& c, const int32_t* rows, int n, const int32_t* keep, uint32_t* status,
+                       hipStream_t s);
+hipError_t launch_commit(const dspark_cache_t& c, const int32_t* accept_len, int lead, int R, uint32_t* status,
+                         hipStream_t s);
+hipError_t launch_fork(const dspark_cache_t& c, const int32_t* src, const int32_t* dst, int n, int deep,
+                       int32_t* forked, uint32_t* status, int32_t* ws, int num_cu, hipStream_t s);
+hipError_t launch_compact(const dspark_cache_t& c, int32_t* page_map, int32_t* n_live, uint32_t* status, int32_t* ws,
+                          int num_cu, hipStream_t s);
+
+struct AppendArgs {
+    const uint16_t* k_new;
+    const uint16_t* v_new;
+    int64_t k_stride, v_stride;  // elements between rows
+    uint16_t* k;                 // the layer's pages
+    uint16_t* v;
+    const int32_t* table;
+    const int32_t* len;
+    const int32_t* offsets;
+    int lead, R, rows, max_new, Hkv, D, page, n_pages, width;
+    uint32_t* status;
+};
+hipError_t launch_append(const AppendArgs& a, hipStream_t s);
+
+// Attention: a launch's workers share its units of keys evenly, so a segment (the rows of
+// one request or group, a tile of them, with one key head) is split over consecutive
+// workers where it has to be.  A worker leaves a split segment's part in one of its two
+// slots: slot 0 for the segment that an earlier worker began, slot 1 for the one that it
+// begins and does not end.
+constexpr int kAttendUnit = 128;        // keys of one unit
+constexpr int kAttendTile = 32;         // query rows (row, head of the group) of one tile
+constexpr int kAttendMaxWorkers = 512;  // workgroups of one launch
+
+struct AttendArgs {
+    const uint16_t* q;
+    int64_t q_stride, out_stride;  // elements between rows
+    const uint16_t* k;             // the layer's pages
+    const uint16_t* v;
+    const int32_t* table;
+    const int32_t* len;
+    const int32_t* offsets;
+    int lead, R, rows, max_new, H, Hkv, G, D, dtype, page, n_pages, width;
+    float scale_log2;  // the scores' scale times log2(e)
+    int n_groups, shared_width;
+    const int32_t* group_off;
+    const int32_t* shared_table;
+    const int32_t* shared_pages;
+    uint16_t* out;
+    float* lse;
+    uint32_t* status;
+    int workers;
+    float* slots[2];   // parts of split segments: of the requests' own keys, of the shared ones
+    float* dense;      // shared keys: whole segments' parts, [Hkv][rows G][D], then maxima and sums
+    uint32_t* cum[2];  // running units (of one key head) of the requests, of the groups
+};
+size_t attend_ws_bytes(int R, int H, int D, int max_new, int n_groups);
+void attend_ws_layout(AttendArgs& a, void* ws);
+hipError_t launch_attend(AttendArgs a, int num_cu, hipStream_t s);
+
+}  // namespace dspark

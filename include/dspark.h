@@ -59,7 +59,7 @@ typedef enum {
     DSPARK_EHIP = -5          /* HIP runtime error (text in dspark_last_error)    */
 } dspark_status_t;
 
-typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1 } dspark_dtype_t;
+typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_F16 = 2 /* the paged cache alone */ } dspark_dtype_t;
 
 /* Device-side conditions, OR-ed into *status. */
 #define DSPARK_STATUS_PREV_CLAMPED 1u   /* a prev0 entry was outside [0,V); it was clamped into range      */
@@ -71,6 +71,13 @@ typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1 } dspark_dtype_t;
                                            tokens are then unreliable                                       */
 #define DSPARK_STATUS_BAD_ALLOCATION 16u /* dspark_accept_greedy met an inconsistent offsets row; that request
                                            accepted nothing and its next prev0 is -1                        */
+#define DSPARK_STATUS_BAD_PAGE 32u      /* paged cache: a page id outside [0, n_pages) where a page was needed (its
+                                           tokens are left out), a page released more often than it was held, or
+                                           a request whose table does not begin with its group's pages      */
+#define DSPARK_STATUS_BAD_ROW 64u       /* paged cache: a request, table row or group whose offsets, length or
+                                           index do not fit (see each call for what becomes of it)          */
+#define DSPARK_STATUS_NO_PAGES 128u     /* paged cache: too few free pages, or no room in the table; the request or
+                                           fork was not served                                              */
 
 /* Admission rules of stage 4. */
 #define DSPARK_RULE_ARGMAX 0      /* the smallest B with the largest f(B) (vLLM blog, "Scheduling the budget")  */
@@ -420,6 +427,173 @@ int dspark_step_sized(const void* base, const void* A, const void* Bmat, int dty
 int dspark_accept_greedy(const int32_t* ver_tokens, const int32_t* offsets, const int32_t* target, int R, int K,
                          int32_t* accept_len, int32_t* next_prev0, int32_t* out_tokens, uint32_t* status,
                          void* stream);
+
+/*
+ * The paged cache of the verification pass.
+ *
+ * Between the schedule (dspark_step's offsets) and the acceptance (dspark_accept_greedy)
+ * the target runs each request's rows: the last accepted token and its drafts, row j of
+ * request r at row offsets[r] + lead * r + j of the packed tensors, n_r = offsets[r+1] -
+ * offsets[r] + lead rows (the layout of dspark_accept_greedy's target for lead = 1; lead =
+ * 0 packs offsets' rows alone, e.g. pieces of prompts).  These calls keep the keys and
+ * values that such rows write and read, in pages of a cache:
+ *   dspark_pages_reserve   pages for the step's rows;
+ *   dspark_cache_append    one layer's K and V of the rows into them;
+ *   dspark_cache_attend    one layer's attention of the rows;
+ *   dspark_pages_commit    after the acceptance: the accepted rows stay, the pages past
+ *                          them are let go;
+ *   dspark_pages_trim      rows cut back or freed;
+ *   dspark_pages_fork      a request's cache continued by another one;
+ *   dspark_pages_compact   the live pages moved to the front.
+ *
+ * dspark_cache_t describes buffers that the caller owns (device memory):
+ *   k      [layers, n_pages, n_kv_heads, page_size/16, head_dim/8, 16, 8]
+ *   v      [layers, n_pages, n_kv_heads, page_size/16, head_dim, 16]
+ *          (bf16 or fp16) a page holds page_size tokens in blocks of 16: token t and
+ *          dim d of a block are K's [d/8][t][d%8] and V's [d][t], the order in which the
+ *          matrix instructions take them; 16-byte aligned
+ *   table  [rows, width] int32: row r's pages in the order of its tokens, then -1.  The
+ *          step's request r has table row r
+ *   len    [rows] int32: tokens that row r keeps; below 0 for a vacant row, whose request
+ *          takes part in nothing
+ *   ref    [n_pages] int32: table rows that hold the page; 0 for a free page
+ * Start with table all -1, len -1 or 0 and ref 0.  The calls keep these two in step with
+ * each other; a page that a caller holds besides (a group's pages that no row holds) has a
+ * count of the caller's.  reserve, commit and trim need no k and v (they may be NULL).
+ * Limits: n_pages <= DSPARK_CACHE_MAX_PAGES; page_size a power of two from 16 to 256;
+ * rows * width < 2^31; head_dim 64, 128 or 256; n_kv_heads <= 1024; at most
+ * DSPARK_CACHE_MAX_REQUESTS requests or forks in a call.  The sizes of the whole cache
+ * pass 32 bits without harm.  Calls that share a cache or a workspace must not overlap;
+ * nothing in a workspace has to be cleared or is kept between calls.
+ */
+#define DSPARK_CACHE_MAX_PAGES (1 << 24)
+#define DSPARK_CACHE_MAX_REQUESTS 8192
+#define DSPARK_CACHE_MAX_GROUPS 1024
+typedef struct dspark_cache {
+    void* k;
+    void* v;
+    int32_t* table;
+    int32_t* len;
+    int32_t* ref;
+    int32_t layers, n_pages, page_size, n_kv_heads, head_dim, dtype, rows, width;
+} dspark_cache_t;
+
+/* Bytes of workspace (16-byte aligned) for reserve and fork of up to n requests or forks,
+ * and for compact (n = 0 will do). */
+size_t dspark_pages_workspace_bytes(int n_pages, int n);
+
+/*
+ * Pages for a step's rows: request r of the first R table rows needs
+ *   need_r = max(0, ceil((len[r] + n_r) / page_size) - pages that its row holds)
+ * more.  Requests are served in order, r if need_0 + ... + need_r free pages exist (or
+ * need_r = 0), and each takes the lowest free pages that are left; they join its row and
+ * get a count of 1.  len stays.
+ *   offsets  [R+1] int32, lead: the step's rows (see above)
+ *   granted  [R]   int32 output: 1 served, 0 not (vacant; DSPARK_STATUS_NO_PAGES where
+ *                  pages or table entries ran out; DSPARK_STATUS_BAD_ROW for n_r < 0 or a
+ *                  row that does not hold the pages of its len tokens; nothing of such a
+ *                  request changes)
+ */
+int dspark_pages_reserve(const dspark_cache_t* cache, const int32_t* offsets, int lead, int R, int32_t* granted,
+                         uint32_t* status, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Table rows cut back: row rows[i] (row i where rows is NULL) keeps the pages of keep[i]
+ * tokens (0 where keep is NULL) and len = min(len, keep[i]); the pages behind leave it, and
+ * one that no row holds any more is free.  keep[i] < 0 makes the row vacant (len = -1).  A
+ * row may be named more than once (it keeps the least).  A rows[i] outside the table is
+ * left out (DSPARK_STATUS_BAD_ROW).
+ */
+int dspark_pages_trim(const dspark_cache_t* cache, const int32_t* rows, int n, const int32_t* keep, uint32_t* status,
+                      void* stream);
+
+/*
+ * After the acceptance: request r keeps its first lead + accept_len[r] rows of the step
+ * (accept_len from dspark_accept_greedy), len[r] += lead + accept_len[r], and the pages
+ * past them leave its row as in dspark_pages_trim.  Vacant rows stay as they are; so does
+ * one whose accept_len is negative or reaches past its pages (DSPARK_STATUS_BAD_ROW).
+ */
+int dspark_pages_commit(const dspark_cache_t* cache, const int32_t* accept_len, int lead, int R, uint32_t* status,
+                        void* stream);
+
+/*
+ * Forks: table row dst[i], which holds no pages (len <= 0), continues row src[i]: it
+ * shares the whole pages of its len tokens (their counts grow by one) and gets a copy of
+ * the last, partly filled one, every layer's K and V, in a page of its own; with deep != 0
+ * it gets copies of all of them.  New pages are the lowest free ones, in the order of the
+ * forks; fork i is served if the pages that forks 0..i need exist.  All rows are read as
+ * they were before the call.
+ *   forked  [n] int32 output: 1 served, 0 not (DSPARK_STATUS_NO_PAGES; or
+ *           DSPARK_STATUS_BAD_ROW for rows outside the table, a vacant src, src = dst, a
+ *           dst that holds pages or that an earlier fork of the call names; nothing of
+ *           such a fork changes, and it counts for no pages)
+ */
+int dspark_pages_fork(const dspark_cache_t* cache, const int32_t* src, const int32_t* dst, int n, int deep,
+                      int32_t* forked, uint32_t* status, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Compaction: with n_live pages that have a count, the k-th lowest of those at or above
+ * n_live moves to the k-th lowest free page below it, every layer's K and V, and ref and
+ * the whole table follow.  Afterwards pages [0, n_live) are live and the others free (what
+ * was in them stays).
+ *   page_map  [n_pages] int32 output: each page's new place, -1 for one that was free;
+ *             for page lists that the caller keeps beside the table
+ *   n_live    [1] int32 output
+ * A table entry without a live page becomes -1 (DSPARK_STATUS_BAD_PAGE).
+ */
+int dspark_pages_compact(const dspark_cache_t* cache, int32_t* page_map, int32_t* n_live, uint32_t* status, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/*
+ * One layer's K and V of a step's rows into the pages: row j of request r goes to position
+ * len[r] + j, in pages that dspark_pages_reserve has put there.  Positions outside the rows
+ * stay as they are.
+ *   k_new, v_new  [n_rows] rows of [n_kv_heads, head_dim], k_stride and v_stride elements
+ *                 apart (multiples of 8; 16-byte aligned), in the cache's dtype
+ *   offsets       [R+1], lead: the step's rows; max_new >= every n_r
+ * A request with n_r < 0 or > max_new, rows outside the tensors or tokens past its table
+ * is left out (DSPARK_STATUS_BAD_ROW); so are tokens whose page id is none
+ * (DSPARK_STATUS_BAD_PAGE).
+ */
+int dspark_cache_append(const dspark_cache_t* cache, int layer, const void* k_new, int64_t k_stride, const void* v_new,
+                        int64_t v_stride, int n_rows, const int32_t* offsets, int lead, int R, int max_new,
+                        uint32_t* status, void* stream);
+
+/*
+ * One layer's attention of a step's rows over the cache, which holds the rows' own K and V
+ * already.  Row j of request r sees the positions 0..len[r] + j of its table row:
+ *   out[row, head] = sum_p softmax_p(scale * q[row, head] . K[p, g]) V[p, g]
+ *   lse[row, head] = ln sum_p exp(scale * q[row, head] . K[p, g])        g = head / (H / n_kv_heads)
+ * Scores, the softmax and the sums are held in fp32; the weights (at most 1, relative to
+ * the row's largest) are rounded to the cache's dtype for the second product, and out once.
+ * A position that a row does not see has no influence on it, whatever its K and V hold.
+ *   q, out   [n_rows] rows of [H, head_dim], q_stride and out_stride elements apart
+ *            (multiples of 8; 16-byte aligned), in the cache's dtype; they must not alias
+ *   lse      [n_rows, H] fp32 output, or NULL
+ *   offsets  [R+1], lead: the step's rows; max_new >= every n_r
+ *   scale    positive and finite
+ * Shared prefixes: requests group_off[g] .. group_off[g+1] - 1 of group g share their first
+ * shared_pages[g] pages, whose ids are shared_table[g, 0 ..]: those keys are read once for
+ * all of the group's rows instead of once a request.  Each such request has len >=
+ * shared_pages[g] * page_size and a table that begins with these pages (as fork leaves it;
+ * DSPARK_STATUS_BAD_PAGE where it does not, and the group's pages count).  Requests outside
+ * every group read all of their own.
+ *   n_groups (0: none), group_off [n_groups+1] int32 not decreasing, shared_table
+ *   [n_groups, shared_width] int32, shared_pages [n_groups] int32
+ * Rows that see nothing (vacant requests) get zeros and lse -inf; so do those of a request
+ * whose length fits neither its table nor its group (DSPARK_STATUS_BAD_ROW).  A request
+ * with n_r < 0 or > max_new or rows outside the tensors is left out with the same status,
+ * and rows that belong to no request stay as they are.  Page ids outside the cache are not
+ * read: their tokens are left out (DSPARK_STATUS_BAD_PAGE).  Results are the same in every
+ * run.  More rows, heads and tokens than 32-bit numbers of work units hold return
+ * DSPARK_EUNSUPPORTED.
+ */
+size_t dspark_cache_attend_workspace_bytes(int R, int H, int head_dim, int max_new, int n_groups);
+int dspark_cache_attend(const dspark_cache_t* cache, int layer, const void* q, int64_t q_stride, int n_rows, int H,
+                        const int32_t* offsets, int lead, int R, int max_new, float scale, int n_groups,
+                        const int32_t* group_off, const int32_t* shared_table, int shared_width,
+                        const int32_t* shared_pages, void* out, int64_t out_stride, float* lse, uint32_t* status,
+                        void* ws, size_t ws_bytes, void* stream);
 
 /*
  * How the persistent kernels are launched.  The single-launch step (dspark_step,
