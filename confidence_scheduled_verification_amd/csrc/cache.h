@@ -60,8 +60,9 @@ hipError_t launch_append(const AppendArgs& a, hipStream_t s);
 // workers where it has to be.  A worker leaves a split segment's part in one of its two
 // slots: slot 0 for the segment that an earlier worker began, slot 1 for the one that it
 // begins and does not end.
-constexpr int kAttendUnit = 128;        // keys of one unit
-constexpr int kAttendTile = 32;         // query rows (row, head of the group) of one tile
+constexpr int kAttendMinTile = 32;      // columns (row, head of the group) of one tile, at least
+constexpr int kAttendMaxTile = 64;      // and at most
+constexpr int kAttendMinUnit = 64;      // keys of one unit, at least
 constexpr int kAttendMaxWorkers = 512;  // workgroups of one launch
 
 struct AttendArgs {
@@ -72,7 +73,7 @@ struct AttendArgs {
     const int32_t* table;
     const int32_t* len;
     const int32_t* offsets;
-    int lead, R, rows, max_new, H, Hkv, G, D, dtype, page, n_pages, width;
+    int lead, R, rows, max_new, H, Hkv, G, D, dtype, page, page_shift, n_pages, width;
     float scale_log2;  // the scores' scale times log2(e)
     int n_groups, shared_width;
     const int32_t* group_off;
@@ -81,7 +82,7 @@ struct AttendArgs {
     uint16_t* out;
     float* lse;
     uint32_t* status;
-    int workers;
+    int tile[2], unit[2], workers[2];  // the launches' forms: [0] the requests' own keys, [1] the shared ones
     float* slots[2];   // parts of split segments: of the requests' own keys, of the shared ones
     float* dense;      // shared keys: whole segments' parts, [Hkv][rows G][D], then maxima and sums
     uint32_t* cum[2];  // running units (of one key head) of the requests, of the groups

@@ -195,10 +195,10 @@ int dspark_cache_attend(const dspark_cache_t* c, int layer, const void* q, int64
     const int G = H / c->n_kv_heads;
     // rows past R * max_new belong to no request; the work is numbered with 32 bits
     const int rows = (int)std::min<long long>(n_rows, (long long)R * max_new);
-    const long long tiles = ((long long)max_new * G + dspark::kAttendTile - 1) / dspark::kAttendTile;
-    const long long row_tiles = ((long long)rows * H + dspark::kAttendTile - 1) / dspark::kAttendTile;
-    const long long units = (long long)c->width * c->page_size / dspark::kAttendUnit + 1;
-    const long long shared_units = (long long)shared_width * c->page_size / dspark::kAttendUnit + 1;
+    const long long tiles = ((long long)max_new * G + dspark::kAttendMinTile - 1) / dspark::kAttendMinTile;
+    const long long row_tiles = ((long long)rows * H + dspark::kAttendMinTile - 1) / dspark::kAttendMinTile;
+    const long long units = (long long)c->width * c->page_size / dspark::kAttendMinUnit + 1;
+    const long long shared_units = (long long)shared_width * c->page_size / dspark::kAttendMinUnit + 1;
     if ((long long)rows * H > INT32_MAX || tiles > 65535 ||
         std::min(tiles * R, row_tiles / c->n_kv_heads + R) * c->n_kv_heads * units > INT32_MAX ||
         (long long)c->width * c->page_size > INT32_MAX ||
@@ -229,6 +229,7 @@ int dspark_cache_attend(const dspark_cache_t* c, int layer, const void* q, int64
     a.D = c->head_dim;
     a.dtype = c->dtype;
     a.page = c->page_size;
+    a.page_shift = __builtin_ctz(c->page_size);
     a.n_pages = c->n_pages;
     a.width = c->width;
     a.scale_log2 = (float)((double)scale * 1.4426950408889634);
