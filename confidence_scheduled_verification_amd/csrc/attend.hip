@@ -39,10 +39,11 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kT = 256;
+constexpr int kWideFrom = 64;  // columns of a request or group beyond which the many-rows form runs
 constexpr float kInf = __builtin_huge_valf();
 
 struct Bf16 {
-    static constexpr uint32_t kExp = 0x7F80u, kMant = 0x007Fu, kOne = 0x3F80u;
+    static constexpr uint32_t kExp = 0x7F80u, kMant = 0x007Fu, kOne = 0x3F80u, k64 = 0x4280u, k4096 = 0x4580u;
     static __device__ __forceinline__ f32x16 mfma(s16x8 a, s16x8 b, f32x16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
                                                        c, 0, 0, 0);
@@ -50,13 +51,15 @@ struct Bf16 {
     static __device__ __forceinline__ uint16_t bits(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
 };
 struct F16 {
-    static constexpr uint32_t kExp = 0x7C00u, kMant = 0x03FFu, kOne = 0x3C00u;
+    static constexpr uint32_t kExp = 0x7C00u, kMant = 0x03FFu, kOne = 0x3C00u, k64 = 0x5400u, k4096 = 0x6C00u;
     static __device__ __forceinline__ f32x16 mfma(s16x8 a, s16x8 b, f32x16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
                                                       0, 0);
     }
     static __device__ __forceinline__ uint16_t bits(float x) { return __builtin_bit_cast(uint16_t, (_Float16)x); }
 };
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 // One request's rows and keys: 1 rows that see keys [kb, ln + n) of its own; 0 rows that
 // see nothing (vacant, or its length does not fit its table or prefix); -1 its rows do not
@@ -130,35 +133,6 @@ __device__ Group shared_of(const AttendArgs& a, int g, uint32_t& bad) {
     return q;
 }
 
-// What one item (request or group) brings: its rows, the keys [kb, ke) that this launch
-// gives them and the table that these lie in.  The last key that row j sees is ln + j.
-struct Work {
-    int start, n, kb, ke, ln, group;
-    const int32_t* table;
-};
-
-template <int kSet>
-__device__ Work work_of(const AttendArgs& a, int i) {
-    uint32_t bad = 0;
-    Work w;
-    if (kSet) {
-        const Group g = shared_of(a, i, bad);
-        w = Work{g.start, g.n, 0, g.ke, 0, -1, a.shared_table + (size_t)i * a.shared_width};
-    } else {
-        Request q;
-        request_of(a, i, q, bad);
-        w = Work{q.start, q.n, q.kb, q.ln + q.n, q.ln, q.group, a.table + (size_t)i * a.width};
-    }
-    // the same in every lane: held in scalar registers
-    w.start = __builtin_amdgcn_readfirstlane(w.start);
-    w.n = __builtin_amdgcn_readfirstlane(w.n);
-    w.kb = __builtin_amdgcn_readfirstlane(w.kb);
-    w.ke = __builtin_amdgcn_readfirstlane(w.ke);
-    w.ln = __builtin_amdgcn_readfirstlane(w.ln);
-    w.group = __builtin_amdgcn_readfirstlane(w.group);
-    return w;
-}
-
 template <int kTile>
 __device__ __forceinline__ int tiles_of(const AttendArgs& a, int n) {
     return (n * a.G + kTile - 1) / kTile;
@@ -169,35 +143,70 @@ __device__ __forceinline__ int units_of(int keys) {
 }
 // The same for launch `set`, whose form the host has chosen.
 __device__ __forceinline__ int tiles_in(const AttendArgs& a, int set, int n) {
-    return (n * a.G + a.tile[set] - 1) / a.tile[set];
+    return (n * a.G + a.tile[set] - 1) >> a.tile_shift[set];
 }
 __device__ __forceinline__ int units_in(const AttendArgs& a, int set, int keys) {
-    return (keys + a.unit[set] - 1) / a.unit[set];
+    return (keys + a.unit[set] - 1) >> a.unit_shift[set];
 }
 
-// Workers that have a unit at all, so that no part between two others is missing.
-__device__ __forceinline__ int workers_of(const AttendArgs& a, int set, uint32_t total) {
-    return total < (uint32_t)a.workers[set] ? (int)total : a.workers[set];
-}
-// Worker w's first unit, and the worker of unit u, when `workers` share `total` units.
-__device__ __forceinline__ uint32_t first_unit(uint32_t total, int workers, int w) {
-    return (uint32_t)((uint64_t)total * (uint32_t)w / (uint32_t)workers);
-}
-__device__ __forceinline__ int worker_of(uint32_t total, int workers, uint32_t u) {
-    return (int)((((uint64_t)u + 1) * (uint32_t)workers - 1) / total);
-}
+// How `total` units are dealt to the workers: each takes `each` consecutive ones, the first
+// `more` one more than that.  Where there are fewer units than workers the others have none.
+struct Split {
+    uint32_t each, more;
+    int workers;
+    __device__ __forceinline__ Split(uint32_t total, int most) {
+        workers = total < (uint32_t)most ? (int)total : most;
+        each = workers ? total / (uint32_t)workers : 0;
+        more = workers ? total % (uint32_t)workers : 0;
+    }
+    __device__ __forceinline__ uint32_t first(uint32_t w) const { return w * each + min(w, more); }
+    __device__ __forceinline__ int worker_of(uint32_t u) const {
+        const uint32_t big = more * (each + 1);
+        return (int)(u < big ? u / (each + 1) : more + (u - big) / each);
+    }
+};
 
 __device__ __forceinline__ float* slot_of(const AttendArgs& a, int set, int worker, int which) {
     return a.slots[set] + (size_t)(worker * 2 + which) * ((size_t)a.tile[set] * (a.D + 2));
 }
 
-// Running units (of one key head) of the items in LDS, kept for the second kernel too;
-// returns the units of all heads.  One workgroup of 256 threads.
-template <int kSet>
+// Running units (of one key head) of the items in LDS, and what each of the first kCached
+// brings, so that a workgroup looks at the requests once; the groups' running units are kept
+// for the next launch too.  Returns the units of all heads.
+constexpr int kCached = 384;  // items: LDS for two workgroups a compute unit at head_dim 128
+
+// Rows that see nothing get zeros: those of the requests without units.  Request i is looked
+// at by enough workgroups, from number i on, to give each wave about four of its rows.
+template <int kThreads>
+__device__ void clear_unseen(const AttendArgs& a, int n, const uint32_t* s_cum) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, grid = gridDim.x;
+    constexpr int kWaves = kThreads / 64;
+    const int takes = min(grid, (a.max_new + 4 * kWaves - 1) / (4 * kWaves));
+    for (int i0 = 0; i0 < n; i0 += 64) {
+        const int at = i0 + lane;
+        const bool mine = at < n && s_cum[at] == s_cum[at + 1] && (blockIdx.x + grid - at % grid) % grid < takes;
+        for (uint64_t left = __ballot(mine); left; left &= left - 1) {
+            const int i = i0 + (int)__ffsll((unsigned long long)left) - 1;
+            Request q;
+            uint32_t none = 0;
+            if (request_of(a, i, q, none) != 0) continue;
+            const int turn = (blockIdx.x + grid - i % grid) % grid;
+            for (int j = turn * kWaves + wave; j < q.n; j += takes * kWaves) {
+                uint16_t* row = a.out + (size_t)(q.start + j) * a.out_stride;
+                for (int e = lane; e < a.H * (a.D / 8); e += 64) *(uint4*)(row + e * 8) = make_uint4(0, 0, 0, 0);
+                if (a.lse)
+                    for (int e = lane; e < a.H; e += 64) a.lse[(size_t)(q.start + j) * a.H + e] = -kInf;
+            }
+        }
+    }
+}
+
+template <int kSet, int kThreads>
 __device__ uint32_t plan(const AttendArgs& a, int n, uint32_t* s_cum, uint32_t* s_base) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    Request* s_info = (Request*)(s_cum + n + 1);
     uint32_t base = 0, bad = 0;
-    for (int i0 = 0; i0 < n; i0 += kT) {
+    for (int i0 = 0; i0 < n; i0 += kThreads) {
         const int i = i0 + tid;
         uint32_t x = 0;
         if (i < n) {
@@ -206,7 +215,9 @@ __device__ uint32_t plan(const AttendArgs& a, int n, uint32_t* s_cum, uint32_t* 
                 x = (uint32_t)tiles_in(a, 1, g.n) * units_in(a, 1, g.ke);
             } else {
                 Request q;
-                if (request_of(a, i, q, bad) == 1) x = (uint32_t)tiles_in(a, 0, q.n) * units_in(a, 0, q.ln + q.n - q.kb);
+                const int state = request_of(a, i, q, bad);
+                if (state == 1) x = (uint32_t)tiles_in(a, 0, q.n) * units_in(a, 0, q.ln + q.n - q.kb);
+                if (i < kCached) s_info[i] = q;
             }
         }
         uint32_t y = x;
@@ -220,14 +231,17 @@ __device__ uint32_t plan(const AttendArgs& a, int n, uint32_t* s_cum, uint32_t* 
         __syncthreads();
         for (int w = 0; w < wave; ++w) y += s_base[w];
         if (i < n) s_cum[i] = base + y - x;
-        base += s_base[0] + s_base[1] + s_base[2] + s_base[3];
+#pragma unroll
+        for (int w = 0; w < kThreads / 64; ++w) base += s_base[w];
     }
     if (tid == 0) s_cum[n] = base;
     __syncthreads();
     if (blockIdx.x == 0) {
-        for (int i = tid; i <= n; i += kT) a.cum[kSet][i] = s_cum[i];
+        if (kSet)
+            for (int i = tid; i <= n; i += kThreads) a.cum[i] = s_cum[i];
         if (bad) raise_status(a.status, bad);
     }
+    if (kSet == 0) clear_unseen<kThreads>(a, n, s_cum);
     return __builtin_amdgcn_readfirstlane(base) * a.Hkv;
 }
 
@@ -241,53 +255,133 @@ __device__ __forceinline__ int item_of(const AttendArgs& a, const uint32_t* s_cu
     return i;
 }
 
+// The units of a group in its launch, as the requests' launch needs them to find the parts:
+// those of its tile t with key head h are [u0 + (h tiles + t) units, + units).
+struct Shared {
+    int start, n;  // the group's rows; n = 0 for none
+    uint32_t u0, units, tiles;
+};
+
+// What one item (request or group) brings: its rows, the keys [kb, ke) that this launch
+// gives them and the table that these lie in.  The last key that row j sees is ln + j.
+struct Work {
+    int start, n, kb, ke, ln, group;
+    const int32_t* table;
+    Shared shared;
+};
+
+template <int kSet>
+__device__ Work work_of(const AttendArgs& a, int i, int n, const uint32_t* s_cum) {
+    uint32_t bad = 0;
+    Work w{};
+    if (kSet) {
+        const Group g = shared_of(a, i, bad);
+        w.start = uniform(g.start);
+        w.n = uniform(g.n);
+        w.ke = uniform(g.ke);
+        w.group = -1;
+        w.table = a.shared_table + (size_t)i * a.shared_width;
+        return w;
+    }
+    Request q;
+    if (i < kCached) q = ((const Request*)(s_cum + n + 1))[i];
+    else request_of(a, i, q, bad);
+    // the same in every lane: held in scalar registers
+    w.start = uniform(q.start);
+    w.n = uniform(q.n);
+    w.kb = uniform(q.kb);
+    w.ln = uniform(q.ln);
+    w.ke = w.ln + w.n;
+    w.group = uniform(q.group);
+    w.table = a.table + (size_t)i * a.width;
+    if (w.kb > 0) {
+        const Group g = shared_of(a, w.group, bad);
+        // (rows outside the group's, as offsets that fall would have it, have no part there)
+        if (uniform(g.ke) > 0 && w.start >= uniform(g.start) && w.start + w.n <= uniform(g.start + g.n)) {
+            w.shared.start = uniform(g.start);
+            w.shared.n = uniform(g.n);
+            w.shared.units = units_in(a, 1, uniform(g.ke));
+            w.shared.tiles = tiles_in(a, 1, w.shared.n);
+            w.shared.u0 = uniform(a.cum[w.group]) * a.Hkv;
+        }
+    }
+    return w;
+}
+
 // A request's table has to begin with its group's pages.
 __device__ void check_prefix(const AttendArgs& a, const Work& q) {
     bool differs = false;
     const int32_t* shared = a.shared_table + (size_t)q.group * a.shared_width;
-    for (int p = threadIdx.x; p < q.kb >> a.page_shift; p += kT) differs |= q.table[p] != shared[p];
+    for (int p = threadIdx.x; p < q.kb >> a.page_shift; p += blockDim.x) differs |= q.table[p] != shared[p];
     if (differs) raise_status(a.status, kStatusBadPage);
 }
 
-// Adds a part (maximum pm and sum pl of one column, o its values) to a running one.
-__device__ __forceinline__ void join(float& m, float& l, float (&acc)[8], float pm, float pl, const float* o) {
+// Adds a part (maximum pm and sum pl of one column, x and y eight of its values) to a running one.
+__device__ __forceinline__ void join(float& m, float& l, float (&acc)[8], float pm, float pl, float4 x, float4 y) {
     if (pm == -kInf) return;
     const float mx = fmaxf(m, pm);
     const float s0 = __builtin_amdgcn_exp2f(m - mx), s1 = __builtin_amdgcn_exp2f(pm - mx);
     m = mx;
     l = l * s0 + pl * s1;
-    const float4 x = *(const float4*)o, y = *(const float4*)(o + 4);
     const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = acc[i] * s0 + v[i] * s1;
 }
 
-// Adds the parts of the segment whose units are [u0, u0 + units): column `col` of its tile.
-__device__ __forceinline__ void join_parts(const AttendArgs& a, int set, uint32_t total, uint32_t u0, uint32_t units,
-                                           int col, int c8, float& m, float& l, float (&acc)[8]) {
-    const int workers = workers_of(a, set, total), tile = a.tile[set];
-    const int wa = worker_of(total, workers, u0), wb = worker_of(total, workers, u0 + units - 1);
-    for (int w = wa; w <= wb; ++w) {
-        const float* s = slot_of(a, set, w, w == wa);
-        join(m, l, acc, s[(size_t)tile * a.D + col], s[(size_t)tile * (a.D + 1) + col], s + (size_t)col * a.D + c8 * 8);
+// Adds the parts that workers wa..wb have left of a segment: column `col` of its tile.  Four
+// parts are requested at a time, so that a long segment's parts do not wait for each other.
+__device__ __forceinline__ void join_parts(const AttendArgs& a, int set, int wa, int wb, int col, int c8, float& m,
+                                           float& l, float (&acc)[8]) {
+    const size_t tile = a.tile[set];
+    for (int w0 = wa; w0 <= wb; w0 += 4) {
+        float pm[4], pl[4];
+        float4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int w = min(w0 + i, wb);
+            const float* s = slot_of(a, set, w, w == wa);
+            pm[i] = s[tile * a.D + col];
+            pl[i] = s[tile * (a.D + 1) + col];
+            x[i] = *(const float4*)(s + (size_t)col * a.D + c8 * 8);
+            y[i] = *(const float4*)(s + (size_t)col * a.D + c8 * 8 + 4);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (w0 + i <= wb) join(m, l, acc, pm[i], pl[i], x[i], y[i]);
     }
 }
 
-// Adds the shared keys' part of query row f (row G + head of the group) of key head h.
-__device__ void join_shared(const AttendArgs& a, int group, int f, int h, int c8, float& m, float& l, float (&acc)[8]) {
-    uint32_t bad = 0;
-    const Group g = shared_of(a, group, bad);
-    const int at = f - g.start * a.G;
-    if (g.ke <= 0 || at < 0 || at >= g.n * a.G) return;
-    const uint32_t* cum = a.cum[1];
-    const uint32_t total = cum[a.n_groups] * a.Hkv, units = units_in(a, 1, g.ke), tiles = tiles_in(a, 1, g.n);
-    const uint32_t u0 = cum[group] * a.Hkv + (h * tiles + at / a.tile[1]) * units;
-    const int workers = workers_of(a, 1, total);
-    if (worker_of(total, workers, u0) == worker_of(total, workers, u0 + units - 1)) {
-        const size_t n = (size_t)a.Hkv * a.rows * a.G, i = (size_t)h * a.rows * a.G + f;
-        join(m, l, acc, a.dense[n * a.D + i], a.dense[n * (a.D + 1) + i], a.dense + i * a.D + c8 * 8);
+// The shared keys' parts for the columns from f0 on: they lie in one tile of the group's
+// launch, or from column `edge` on in the next one (a tile there is at least as wide).
+struct SharedParts {
+    int edge, col0;        // the first column of the second tile; f0's column in the first one
+    int first[2], last[2];  // the workers that hold parts of the two
+};
+
+__device__ SharedParts shared_parts(const AttendArgs& a, const Split& split, const Shared& g, int f0, int h) {
+    SharedParts p{};
+    const int at = f0 - g.start * a.G, tile = at >> a.tile_shift[1];
+    p.col0 = at - (tile << a.tile_shift[1]);
+    p.edge = a.tile[1] - p.col0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t u0 = g.u0 + (h * g.tiles + min(tile + i, (int)g.tiles - 1)) * g.units;
+        p.first[i] = uniform(split.worker_of(u0));
+        p.last[i] = uniform(split.worker_of(u0 + g.units - 1));
+    }
+    return p;
+}
+
+// Adds them for column c of f0's tile, key head h.
+__device__ __forceinline__ void join_shared(const AttendArgs& a, const SharedParts& p, int f0, int c, int h, int c8, float& m,
+                                            float& l, float (&acc)[8]) {
+    const int i = c >= p.edge;
+    if (p.first[i] == p.last[i]) {
+        const size_t n = (size_t)a.Hkv * a.rows * a.G, f = (size_t)h * a.rows * a.G + f0 + c;
+        const float* o = a.dense + f * a.D + c8 * 8;
+        join(m, l, acc, a.dense[n * a.D + f], a.dense[n * (a.D + 1) + f], *(const float4*)o, *(const float4*)(o + 4));
     } else {
-        join_parts(a, 1, total, u0, units, at % a.tile[1], c8, m, l, acc);
+        join_parts(a, 1, p.first[i], p.last[i], i ? c - p.edge : p.col0 + c, c8, m, l, acc);
     }
 }
 
@@ -316,8 +410,8 @@ template <class E>
 __device__ __forceinline__ void add_special(f32x16& o, s16x8 v0, s16x8 v1, s16x8 sees0, s16x8 sees1) {
     const auto weight = [](short v) -> short {
         const uint32_t y = (uint16_t)v;
-        if ((y & E::kExp) != E::kExp) return 0;
-        return (short)E::bits(y & E::kMant ? 4096.f : y & 0x8000u ? 1.f : 64.f);
+        const uint32_t inf = y & 0x8000u ? E::kOne : E::k64, w = y & E::kMant ? E::k4096 : inf;
+        return (short)((y & E::kExp) == E::kExp ? w : 0u);
     };
     s16x8 x0, x1;
 #pragma unroll
@@ -329,9 +423,8 @@ __device__ __forceinline__ void add_special(f32x16& o, s16x8 v0, s16x8 v1, s16x8
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const uint32_t c = (uint32_t)n[i], neg = c & 63u, pos = (c >> 6) & 63u;
-        if (c >= 4096u || (neg && pos)) o[i] = __builtin_nanf("");
-        else if (pos) o[i] += kInf;
-        else if (neg) o[i] -= kInf;
+        const float add = pos ? kInf : neg ? -kInf : 0.f;
+        o[i] = c >= 4096u || (neg && pos) ? __builtin_nanf("") : o[i] + add;
     }
 }
 
@@ -357,10 +450,10 @@ __device__ __forceinline__ uint32_t clear_masked(s16x8& v, int valid) {
 // 8 c8 on.  The result, where the segment ends here and its keys were the requests' own;
 // else the part, for whoever joins it.
 template <class E, int kSet>
-__device__ __forceinline__ void finish(const AttendArgs& a, const Work& q, bool whole, bool begins, int f0, int c, int h,
-                                       int c8, float m, float l, float (&acc)[8]) {
+__device__ __forceinline__ void finish(const AttendArgs& a, const SharedParts& parts, bool shared, bool whole,
+                                       bool begins, int f0, int c, int h, int c8, float m, float l, float (&acc)[8]) {
     if (whole && kSet == 0) {
-        if (q.kb > 0) join_shared(a, q.group, f0 + c, h, c8, m, l, acc);
+        if (shared) join_shared(a, parts, f0, c, h, c8, m, l, acc);
         store_row<E>(a, f0 + c, h, c8, m, l, acc);
         return;
     }
@@ -432,11 +525,13 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
     const int col = lane & 31, half = lane >> 5;
     const int key_wave = wave / kTiles, sub = wave % kTiles;
     const int n = kSet ? a.n_groups : a.R;
-    const uint32_t total = plan<kSet>(a, n, s_cum, s_base);
-    const int workers = workers_of(a, kSet, total);
-    if ((int)blockIdx.x >= workers) return;
-    uint32_t u = first_unit(total, workers, blockIdx.x);
-    const uint32_t u_end = first_unit(total, workers, blockIdx.x + 1);
+    const uint32_t total = plan<kSet, kT>(a, n, s_cum, s_base);
+    const Split split(total, a.workers[kSet]);
+    if (kSet == 0 && tid == 0) a.ends[blockIdx.x].units = 0;
+    if ((int)blockIdx.x >= split.workers) return;
+    const Split split1(kSet == 0 && a.n_groups ? uniform(a.cum[a.n_groups]) * a.Hkv : 0, a.workers[1]);
+    uint32_t u = split.first(blockIdx.x);
+    const uint32_t u_end = split.first(blockIdx.x + 1);
     const int shift = a.page_shift - 4, in_page = (1 << shift) - 1;  // blocks of 16 in a page
     const int head_shift = __builtin_ctz(D) + a.page_shift;  // a head's elements in a page
 
@@ -447,7 +542,7 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
             const int i = item_of(a, s_cum, n, u);
             item_u0 = __builtin_amdgcn_readfirstlane(s_cum[i]) * a.Hkv;
             item_u1 = __builtin_amdgcn_readfirstlane(s_cum[i + 1]) * a.Hkv;
-            q = work_of<kSet>(a, i);
+            q = work_of<kSet>(a, i, n, s_cum);
         }
         const uint32_t units = units_of<kUnit>(q.ke - q.kb), tiles = tiles_of<32 * kTiles>(a, q.n);
         const uint32_t in = u - item_u0, seg = in / units, unit0 = in % units;
@@ -456,6 +551,9 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
         const int f0 = q.start * a.G + tile * (32 * kTiles);
         const int nf = min(32 * kTiles, q.n * a.G - tile * (32 * kTiles));
         if (kSet == 0 && q.kb > 0 && seg == 0 && unit0 == 0) check_prefix(a, q);
+        if (kSet == 0 && unit0 > 0 && tid == 0)  // begun by an earlier worker: for the joining kernel
+            a.ends[blockIdx.x] = AttendEnd{units, split.worker_of(u - unit0), split.worker_of(u - unit0 + units - 1), f0,
+                                           nf, h, q.shared.start, q.shared.n, q.shared.u0, q.shared.units, q.shared.tiles};
 
         // Q^T as the first product's second operand: this lane's column, dims 16 c + 8 half + 0..7.
         const int f = f0 + min(sub * 32 + col, nf - 1);
@@ -590,6 +688,8 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
 
         // The waves' parts joined, column by column, eight dims to a thread.
         const bool whole = unit0 == 0 && unit1 == units;
+        SharedParts parts{};
+        if (kSet == 0 && whole && q.shared.n > 0) parts = shared_parts(a, split1, q.shared, f0, h);
 #pragma unroll
         for (int d0 = 0; d0 < D; d0 += kDims) {
             __syncthreads();
@@ -612,46 +712,275 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
 #pragma unroll
                 for (int w = 0; w < kKeyWaves; ++w) {
                     const int from = w * kTiles + c / 32;
-                    join(jm, jl, acc, s_m[from][c % 32], s_l[from][c % 32], &s_o[from][c % 32][c8 * 8]);
+                    join(jm, jl, acc, s_m[from][c % 32], s_l[from][c % 32], *(const float4*)&s_o[from][c % 32][c8 * 8],
+                         *(const float4*)&s_o[from][c % 32][c8 * 8 + 4]);
                 }
-                finish<E, kSet>(a, q, whole, unit0 == 0, f0, c, h, d0 / 8 + c8, jm, jl, acc);
+                finish<E, kSet>(a, parts, q.shared.n > 0, whole, unit0 == 0, f0, c, h, d0 / 8 + c8, jm, jl, acc);
             }
         }
         u += unit1 - unit0;
     }
 }
 
-// Joins the parts of the segments that were split, and gives zeros to rows that see nothing.
+// The many-rows form, for groups and prompts: a wave takes 32 columns, the workgroup eight
+// (at head_dim 64 and 256: four) times as many, and all waves read the same 64 keys from LDS, which
+// the next 64 are brought to meanwhile (global_load_lds: memory to LDS with no registers
+// between).  The lanes of such a load pick their 16 bytes so that what a wave reads later,
+// an operand of a matrix instruction, lies in LDS lane after lane.  The running maximum of
+// a column follows only when it grows by more than 8 in the exponent of two; until then the
+// weights are taken relative to the older one, at most 2^8, and nothing has to be rescaled.
+template <int D>
+struct Wide {
+    static constexpr int kWaves = D == 128 ? 8 : 4;
+    static constexpr int kThreads = kWaves * 64, kTile = kWaves * 32, kUnit = 64;
+    static constexpr int kPerCu = D == 64 ? 3 : 1;  // workgroups: as many as the registers allow
+    static constexpr int kBlock = 16 * D;           // elements of a block's K or V
+};
+
+template <class E, int D, int kSet>
+__global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::kPerCu) void attend_wide_kernel(AttendArgs a) {
+    typedef Wide<D> W;
+    constexpr int NT = D / 32, NC = D / 16, kPitch = 36;
+    constexpr int kStage = 8 * W::kBlock * 2, kJoin = W::kWaves * 32 * kPitch * 4;  // bytes
+    __shared__ __attribute__((aligned(16))) char s_mem[2 * kStage > kJoin ? 2 * kStage : kJoin];
+    __shared__ int s_have[2][4];
+    __shared__ uint32_t s_base[8];
+    extern __shared__ uint32_t s_cum[];  // running units, n + 1, then the requests
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int col = lane & 31, half = lane >> 5;
+    const int n = kSet ? a.n_groups : a.R;
+    const uint32_t total = plan<kSet, W::kThreads>(a, n, s_cum, s_base);
+    const Split split(total, a.workers[kSet]);
+    if (kSet == 0 && tid == 0) a.ends[blockIdx.x].units = 0;
+    if ((int)blockIdx.x >= split.workers) return;
+    const Split split1(kSet == 0 && a.n_groups ? uniform(a.cum[a.n_groups]) * a.Hkv : 0, a.workers[1]);
+    uint32_t u = split.first(blockIdx.x);
+    const uint32_t u_end = split.first(blockIdx.x + 1);
+    const int shift = a.page_shift - 4, in_page = (1 << shift) - 1;  // blocks of 16 in a page
+    const int head_shift = __builtin_ctz(D) + a.page_shift;          // a head's elements in a page
+    // where this lane's 16 bytes of each 1 KB of a block come from: K's keys with bits 2 and 3 of
+    // their number swapped, V's halves of 16 tokens one after the other
+    const int key = lane & 15, k_from = (lane >> 4) * 128 + ((key & 3) | ((key & 4) << 1) | ((key & 8) >> 1)) * 8;
+    const int v_from = col * 16 + half * 8;
+
+    uint32_t item_u0 = 0, item_u1 = 0;  // units of the item at hand
+    Work q{};
+    while (u < u_end) {
+        if (u >= item_u1) {
+            const int i = item_of(a, s_cum, n, u);
+            item_u0 = uniform(s_cum[i]) * a.Hkv;
+            item_u1 = uniform(s_cum[i + 1]) * a.Hkv;
+            q = work_of<kSet>(a, i, n, s_cum);
+        }
+        const uint32_t units = units_of<W::kUnit>(q.ke - q.kb), tiles = tiles_of<W::kTile>(a, q.n);
+        const uint32_t in = u - item_u0, seg = in / units, unit0 = in % units;
+        const int h = seg / tiles, tile = seg % tiles;
+        const uint32_t unit1 = min(units, unit0 + (u_end - u));
+        const int f0 = q.start * a.G + tile * W::kTile;
+        const int nf = min(W::kTile, q.n * a.G - tile * W::kTile);
+        if (kSet == 0 && q.kb > 0 && seg == 0 && unit0 == 0) check_prefix(a, q);
+        if (kSet == 0 && unit0 > 0 && tid == 0)  // begun by an earlier worker: for the joining kernel
+            a.ends[blockIdx.x] = AttendEnd{units, split.worker_of(u - unit0), split.worker_of(u - unit0 + units - 1), f0,
+                                           nf, h, q.shared.start, q.shared.n, q.shared.u0, q.shared.units, q.shared.tiles};
+
+        const int f = f0 + min(wave * 32 + col, nf - 1);
+        const uint16_t* qp = a.q + (size_t)(f / a.G) * a.q_stride + (size_t)(h * a.G + f % a.G) * D + half * 8;
+        s16x8 qf[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) qf[c] = *(const s16x8*)(qp + c * 16);
+        // The column's last key; the wave's earliest and latest of them, and the tile's latest.
+        const int last = kSet ? q.ke - 1 : q.ln + f / a.G - q.start;
+        const int first_last = kSet ? q.ke - 1 : q.ln + (f0 + min(wave * 32, nf - 1)) / a.G - q.start;
+        const int wave_end = wave * 32 >= nf ? 0 : kSet ? q.ke : q.ln + (f0 + min(wave * 32 + 31, nf - 1)) / a.G - q.start + 1;
+        const int tile_end = kSet ? q.ke : q.ln + (f0 + nf - 1) / a.G - q.start + 1;
+
+        f32x16 o[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) o[t] = f32x16{};
+        float m = -kInf, l = 0.f;  // m of the raw scores; l this half's share of the sum
+        int pos = q.kb + (int)(unit0 * W::kUnit);
+        const int pos_end = min(tile_end, q.kb + (int)(unit1 * W::kUnit));
+        int special_from = -1;
+        bool bad_page = false;
+        PageIds pages;
+        if (pos < pos_end)
+            pages.start(q.table, (q.ke + (1 << a.page_shift) - 1) >> a.page_shift,
+                        min(pos + (wave & 3) * 16, q.ke - 1) >> a.page_shift, lane);
+
+        // Block b of the 64 keys at p: whether it is there, and its first element of K and V.
+        const auto locate = [&](int p, int b, size_t& at) {
+            const int blk = (p >> 4) + b;
+            bool there = p + b * 16 < q.ke;
+            int page = there ? pages.at(blk >> shift, lane) : 0;
+            if ((unsigned)page >= (unsigned)a.n_pages) {
+                page = 0;
+                there = false;
+                bad_page = true;
+            }
+            at = (((size_t)(unsigned)page * (unsigned)a.Hkv + h) << head_shift) + (size_t)(blk & in_page) * W::kBlock;
+            return there;
+        };
+        const auto bring = [&](int p, int buf) {
+            const int b = wave & 3;
+            size_t at;
+            const bool there = locate(p, b, at);
+            if (wave < 4 && lane == 0) s_have[buf][b] = there;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                if (W::kWaves == 8 && kv != wave >> 2) continue;  // waves 0-3 bring K, 4-7 V; or each both
+                const uint16_t* from = kv ? a.v + at + v_from : a.k + at + k_from;
+                char* to = s_mem + buf * kStage + (kv * 4 + b) * (W::kBlock * 2);
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j)
+                    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from + j * 512),
+                                                     (__attribute__((address_space(3))) void*)(to + j * 1024), 16, 0, 0);
+            }
+        };
+
+        __syncthreads();  // LDS is free
+        if (pos < pos_end) bring(pos, 0);
+        for (int buf = 0; pos < pos_end; buf ^= 1, pos += W::kUnit) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's share of the 64 keys has landed
+            __syncthreads();                                  // everyone's has, and the other buffer is free
+            if (pos + W::kUnit < pos_end) bring(pos + W::kUnit, buf ^ 1);
+            if (pos >= wave_end) continue;  // the wave's columns see none of these
+            const char* mem = s_mem + buf * kStage;
+            f32x16 s[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                s[b] = f32x16{};
+                const char* kl = mem + (2 * b + (col >> 4)) * (W::kBlock * 2) + (half * 16 + (col & 15)) * 16;
+#pragma unroll
+                for (int c = 0; c < NC; ++c) s[b] = E::mfma(*(const s16x8*)(kl + c * 512), qf[c], s[b]);
+            }
+            const int4 have = *(const int4*)s_have[buf];
+            const bool all = uniform(have.x & have.y & have.z & have.w);
+            const bool masked = pos + 63 > first_last || !all;
+            if (masked) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const int there = j < 8 ? have.x : j < 16 ? have.y : j < 24 ? have.z : have.w;
+                    if (pos + (j / 8) * 16 + half * 8 + j % 8 > last || !there) s[j / 16][j % 16] = -kInf;
+                }
+            }
+            float mx = s[0][0];
+#pragma unroll
+            for (int j = 1; j < 32; ++j) mx = fmaxf(mx, s[j / 16][j % 16]);
+            mx = fmaxf(mx, other_half(mx));
+            if (__ballot((mx - m) * a.scale_log2 > 8.f)) {
+                const float m_new = fmaxf(m, mx);
+                const float alpha = __builtin_amdgcn_exp2f((m - (m_new == -kInf ? 0.f : m_new)) * a.scale_log2);
+                m = m_new;
+                l *= alpha;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) o[t][j] *= alpha;
+            }
+            const float mc = m == -kInf ? 0.f : m * a.scale_log2;
+            s16x8 pf[4];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j / 16][j % 16], a.scale_log2, -mc));
+                l += p;
+                pf[j / 8][j % 8] = (short)E::bits(p);  // the weights, rounded for the matrix instruction
+            }
+            const char* vl = mem + 4 * (W::kBlock * 2) + lane * 16;
+            if (!masked) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        o[t] = E::mfma(*(const s16x8*)(vl + b * (W::kBlock * 2) + t * 1024), pf[b], o[t]);
+            } else {
+                uint32_t special = 0;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        s16x8 v = *(const s16x8*)(vl + b * (W::kBlock * 2) + t * 1024);
+                        const int there = b == 0 ? have.x : b == 1 ? have.y : b == 2 ? have.z : have.w;
+                        special |= clear_masked<E>(v, there ? q.ke - (pos + b * 16 + half * 8) : 0);
+                        o[t] = E::mfma(v, pf[b], o[t]);
+                    }
+                if (special_from < 0 && __ballot(special != 0)) special_from = pos;
+            }
+        }
+        l += other_half(l);
+        if (bad_page && lane == 0) raise_status(a.status, kStatusBadPage);
+        if (special_from >= 0) {
+            pages.fetch(special_from >> a.page_shift, lane);
+            for (pos = special_from; pos < min(pos_end, wave_end); pos += 32) {
+                size_t at[2];
+                const bool have[2] = {locate(pos, 0, at[0]), locate(pos, 1, at[1])};
+                s16x8 sees[2];
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    sees[j / 8][j % 8] =
+                        pos + (j / 8) * 16 + half * 8 + j % 8 <= last && have[j / 8] ? (short)E::kOne : (short)0;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    add_special<E>(o[t], *(const s16x8*)(a.v + at[0] + t * 512 + v_from),
+                                   *(const s16x8*)(a.v + at[1] + t * 512 + v_from), sees[0], sees[1]);
+            }
+        }
+        const float ms = m == -kInf ? -kInf : m * a.scale_log2;
+
+        // The wave's columns, 32 dims at a time through LDS, eight dims of a column to a lane.
+        const bool whole = unit0 == 0 && unit1 == units;
+        SharedParts parts{};
+        if (kSet == 0 && whole && q.shared.n > 0) parts = shared_parts(a, split1, q.shared, f0, h);
+        __syncthreads();
+        float* s_o = (float*)s_mem + wave * (32 * kPitch);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *(float4*)&s_o[col * kPitch + 8 * j + 4 * half] =
+                    make_float4(o[t][4 * j], o[t][4 * j + 1], o[t][4 * j + 2], o[t][4 * j + 3]);
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int e = lane; e < 128; e += 64) {
+                const int c = e >> 2, c8 = e & 3;
+                const float jm = __shfl(ms, c, 64), jl = __shfl(l, c, 64);
+                const float4 x = *(const float4*)&s_o[c * kPitch + c8 * 8], y = *(const float4*)&s_o[c * kPitch + c8 * 8 + 4];
+                float acc[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                if (wave * 32 + c < nf)
+                    finish<E, kSet>(a, parts, q.shared.n > 0, whole, unit0 == 0, f0, wave * 32 + c, h, t * 4 + c8, jm, jl, acc);
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
+        u += unit1 - unit0;
+    }
+}
+
+// Joins the parts of the segments that were split.  Where worker w goes on with a segment that
+// worker w - 1 began, workgroup (w, .) joins it, eight dims of a column to a thread.
 template <class E>
 __global__ __launch_bounds__(kT) void attend_join_kernel(AttendArgs a) {
-    const int r = blockIdx.x, h = blockIdx.y, tile = blockIdx.z, width = a.tile[0];
-    Request q;
-    uint32_t bad = 0;
-    const int state = request_of(a, r, q, bad);
-    if (state < 0 || tile * width >= q.n * a.G) return;
-    const int f0 = q.start * a.G + tile * width, nf = min(width, q.n * a.G - tile * width);
-    const uint32_t *cum = a.cum[0], total = cum[a.R] * a.Hkv;
-    const uint32_t units = state ? units_in(a, 0, q.ln + q.n - q.kb) : 0;
-    const uint32_t u0 = state ? cum[r] * a.Hkv + (h * tiles_in(a, 0, q.n) + tile) * units : 0;
-    const int workers = workers_of(a, 0, total);
-    if (state && worker_of(total, workers, u0) == worker_of(total, workers, u0 + units - 1)) return;
-    for (int e = threadIdx.x; e < nf * (a.D / 8); e += kT) {
-        const int c = e / (a.D / 8), c8 = e % (a.D / 8);
-        float m = -kInf, l = 0.f, acc[8] = {};
-        if (state) {
-            join_parts(a, 0, total, u0, units, c, c8, m, l, acc);
-            if (q.kb > 0) join_shared(a, q.group, f0 + c, h, c8, m, l, acc);
-        }
-        store_row<E>(a, f0 + c, h, c8, m, l, acc);
+    const AttendEnd e = a.ends[blockIdx.x];
+    if (e.units == 0 || e.first != (int)blockIdx.x - 1) return;
+    const int chunks = a.D / 8, c = blockIdx.y * (kT / chunks) + threadIdx.x / chunks, c8 = threadIdx.x % chunks;
+    if (c >= e.nf) return;
+    float m = -kInf, l = 0.f, acc[8] = {};
+    join_parts(a, 0, e.first, e.last, c, c8, m, l, acc);
+    if (e.shared_n > 0) {
+        const Split split1(a.cum[a.n_groups] * a.Hkv, a.workers[1]);
+        const Shared g{e.shared_start, e.shared_n, e.shared_u0, e.shared_units, e.shared_tiles};
+        join_shared(a, shared_parts(a, split1, g, e.f0, e.h), e.f0, c, e.h, c8, m, l, acc);
     }
+    store_row<E>(a, e.f0 + c, e.h, c8, m, l, acc);
 }
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 template <class E, int D, int kSet>
 hipError_t run_set(const AttendArgs& a, hipStream_t s) {
-    const size_t lds = ((kSet ? a.n_groups : a.R) + 1) * sizeof(uint32_t);
-    if (a.tile[kSet] == 64)
+    const size_t lds = kSet ? (a.n_groups + 1) * sizeof(uint32_t)
+                            : (a.R + 1) * sizeof(uint32_t) + std::min(a.R, kCached) * sizeof(Request);
+    if (a.tile[kSet] == Wide<D>::kTile)
+        hipLaunchKernelGGL((attend_wide_kernel<E, D, kSet>), dim3(a.workers[kSet]), dim3(Wide<D>::kThreads), lds, s, a);
+    else if (a.tile[kSet] == 64)
         hipLaunchKernelGGL((attend_kernel<E, D, kSet, 2>), dim3(a.workers[kSet]), dim3(kT), lds, s, a);
     else
         hipLaunchKernelGGL((attend_kernel<E, D, kSet, 1>), dim3(a.workers[kSet]), dim3(kT), lds, s, a);
@@ -663,8 +992,7 @@ hipError_t run(const AttendArgs& a, hipStream_t s) {
     hipError_t e = a.n_groups ? run_set<E, D, 1>(a, s) : hipSuccess;
     if (e == hipSuccess) e = run_set<E, D, 0>(a, s);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(attend_join_kernel<E>, dim3(a.R, a.Hkv, (a.max_new * a.G + a.tile[0] - 1) / a.tile[0]), dim3(kT),
-                       0, s, a);
+    hipLaunchKernelGGL(attend_join_kernel<E>, dim3(a.workers[0], a.tile[0] / (kT / (D / 8))), dim3(kT), 0, s, a);
     return hipGetLastError();
 }
 
@@ -681,7 +1009,7 @@ size_t dense_bytes(int R, int H, int D, int max_new) {
 }  // namespace
 
 size_t attend_ws_bytes(int R, int H, int D, int max_new, int n_groups) {
-    size_t n = slots_bytes(D) + round256((size_t)(R + 1) * 4);
+    size_t n = slots_bytes(D) + round256(kAttendMaxWorkers * sizeof(AttendEnd));
     if (n_groups) n += slots_bytes(D) + round256((size_t)(n_groups + 1) * 4) + dense_bytes(R, H, D, max_new);
     return n;
 }
@@ -690,24 +1018,28 @@ void attend_ws_layout(AttendArgs& a, void* ws) {
     char* p = (char*)ws;
     a.slots[0] = (float*)p;
     p += slots_bytes(a.D);
-    a.cum[0] = (uint32_t*)p;
-    p += round256((size_t)(a.R + 1) * 4);
+    a.ends = (AttendEnd*)p;
+    p += round256(kAttendMaxWorkers * sizeof(AttendEnd));
     if (!a.n_groups) return;
     a.slots[1] = (float*)p;
     p += slots_bytes(a.D);
-    a.cum[1] = (uint32_t*)p;
+    a.cum = (uint32_t*)p;
     p += round256((size_t)(a.n_groups + 1) * 4);
     a.dense = (float*)p;
 }
 
 hipError_t launch_attend(AttendArgs a, int cus, hipStream_t s) {
-    const int w = std::min(cus * (a.D <= 128 ? 2 : 1), kAttendMaxWorkers);
-    // 64 columns to a workgroup where a request (a group) may have more than 32 of them
+    // The many-rows form where a request (a group) may have more columns than the other form
+    // takes at once; else 64 columns to a workgroup where it may have more than 32.
+    const int wide = a.D == 64 ? Wide<64>::kTile : a.D == 128 ? Wide<128>::kTile : Wide<256>::kTile;
     for (int set = 0; set < 2; ++set) {
         const long long columns = (long long)(set ? a.rows : a.max_new) * a.G;
-        a.tile[set] = columns > 32 ? 64 : 32;
-        a.unit[set] = a.tile[set] == 64 ? 64 : 128;
-        a.workers[set] = w;
+        a.tile[set] = columns > kWideFrom ? wide : columns > 32 ? 64 : 32;
+        a.unit[set] = a.tile[set] == 32 ? 128 : 64;
+        const int per_cu = a.tile[set] == wide ? (a.D == 64 ? Wide<64>::kPerCu : 1) : a.D <= 128 ? 2 : 1;
+        a.workers[set] = std::min(cus * per_cu, kAttendMaxWorkers);
+        a.tile_shift[set] = __builtin_ctz(a.tile[set]);
+        a.unit_shift[set] = __builtin_ctz(a.unit[set]);
     }
     return a.dtype == DSPARK_F16 ? run_dim<F16>(a, s) : run_dim<Bf16>(a, s);
 }

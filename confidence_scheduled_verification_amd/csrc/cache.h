@@ -61,9 +61,17 @@ hipError_t launch_append(const AppendArgs& a, hipStream_t s);
 // slots: slot 0 for the segment that an earlier worker began, slot 1 for the one that it
 // begins and does not end.
 constexpr int kAttendMinTile = 32;      // columns (row, head of the group) of one tile, at least
-constexpr int kAttendMaxTile = 64;      // and at most
+constexpr int kAttendMaxTile = 256;     // and at most
 constexpr int kAttendMinUnit = 64;      // keys of one unit, at least
-constexpr int kAttendMaxWorkers = 512;  // workgroups of one launch
+constexpr int kAttendMaxWorkers = 768;  // workgroups of one launch
+
+// A worker's first segment, where an earlier worker began it (units = 0: it did not): the
+// workers that have parts of it, its columns, and its group's units.
+struct AttendEnd {
+    uint32_t units;
+    int first, last, f0, nf, h, shared_start, shared_n;
+    uint32_t shared_u0, shared_units, shared_tiles;
+};
 
 struct AttendArgs {
     const uint16_t* q;
@@ -82,10 +90,11 @@ struct AttendArgs {
     uint16_t* out;
     float* lse;
     uint32_t* status;
-    int tile[2], unit[2], workers[2];  // the launches' forms: [0] the requests' own keys, [1] the shared ones
+    int tile[2], unit[2], tile_shift[2], unit_shift[2], workers[2];  // the launches' forms: [0] the requests' own keys, [1] the shared ones
     float* slots[2];   // parts of split segments: of the requests' own keys, of the shared ones
     float* dense;      // shared keys: whole segments' parts, [Hkv][rows G][D], then maxima and sums
-    uint32_t* cum[2];  // running units (of one key head) of the requests, of the groups
+    AttendEnd* ends;   // [workers[0]]
+    uint32_t* cum;     // running units (of one key head) of the groups
 };
 size_t attend_ws_bytes(int R, int H, int D, int max_new, int n_groups);
 void attend_ws_layout(AttendArgs& a, void* ws);
