@@ -39,8 +39,23 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kT = 256;
-constexpr int kWideFrom = 64;  // columns of a request or group beyond which the many-rows form runs
+#ifndef WF
+#define WF 128
+#endif
+#ifndef WL
+#define WL 8
+#endif
+constexpr int kWideFrom = WF;  // columns of a request or group beyond which the many-rows form runs
+#ifndef FL
+#define FL 2
+#endif
+constexpr int kFewLeast = FL;    // units of the other
+constexpr int kWideLeast = WL;  // units of that form that are worth a workgroup
 constexpr float kInf = __builtin_huge_valf();
+// The running maximum follows only when it grows by more than this exponent of two; until
+// then the weights are taken relative to the older one, at most 2^8, and nothing that has
+// been summed has to be rescaled.
+constexpr float kLag = 8.f;
 
 struct Bf16 {
     static constexpr uint32_t kExp = 0x7F80u, kMant = 0x007Fu, kOne = 0x3F80u, k64 = 0x4280u, k4096 = 0x4580u;
@@ -149,13 +164,13 @@ __device__ __forceinline__ int units_in(const AttendArgs& a, int set, int keys) 
     return (keys + a.unit[set] - 1) >> a.unit_shift[set];
 }
 
-// How `total` units are dealt to the workers: each takes `each` consecutive ones, the first
-// `more` one more than that.  Where there are fewer units than workers the others have none.
+// How a launch's units are dealt to its workers: each takes `each` consecutive ones, the first
+// `more` one more than that.  Workers beyond one for every `least` units have none.
 struct Split {
     uint32_t each, more;
     int workers;
-    __device__ __forceinline__ Split(uint32_t total, int most) {
-        workers = total < (uint32_t)most ? (int)total : most;
+    __device__ __forceinline__ Split(const AttendArgs& a, int set, uint32_t total) {
+        workers = min((uint32_t)a.workers[set], (total + a.least[set] - 1) / a.least[set]);
         each = workers ? total / (uint32_t)workers : 0;
         more = workers ? total % (uint32_t)workers : 0;
     }
@@ -171,8 +186,8 @@ __device__ __forceinline__ float* slot_of(const AttendArgs& a, int set, int work
 }
 
 // Running units (of one key head) of the items in LDS, and what each of the first kCached
-// brings, so that a workgroup looks at the requests once; the groups' running units are kept
-// for the next launch too.  Returns the units of all heads.
+// brings, so that a workgroup looks at the requests once; with shared prefixes the running
+// units are kept for the kernel that joins the parts.  Returns the units of all heads.
 constexpr int kCached = 384;  // items: LDS for two workgroups a compute unit at head_dim 128
 
 // Rows that see nothing get zeros: those of the requests without units.  Request i is looked
@@ -237,8 +252,8 @@ __device__ uint32_t plan(const AttendArgs& a, int n, uint32_t* s_cum, uint32_t* 
     if (tid == 0) s_cum[n] = base;
     __syncthreads();
     if (blockIdx.x == 0) {
-        if (kSet)
-            for (int i = tid; i <= n; i += kThreads) a.cum[i] = s_cum[i];
+        if (a.n_groups)
+            for (int i = tid; i <= n; i += kThreads) a.cum[kSet][i] = s_cum[i];
         if (bad) raise_status(a.status, bad);
     }
     if (kSet == 0) clear_unseen<kThreads>(a, n, s_cum);
@@ -255,33 +270,23 @@ __device__ __forceinline__ int item_of(const AttendArgs& a, const uint32_t* s_cu
     return i;
 }
 
-// The units of a group in its launch, as the requests' launch needs them to find the parts:
-// those of its tile t with key head h are [u0 + (h tiles + t) units, + units).
-struct Shared {
-    int start, n;  // the group's rows; n = 0 for none
-    uint32_t u0, units, tiles;
-};
-
 // What one item (request or group) brings: its rows, the keys [kb, ke) that this launch
 // gives them and the table that these lie in.  The last key that row j sees is ln + j.
 struct Work {
     int start, n, kb, ke, ln, group;
     const int32_t* table;
-    Shared shared;
 };
 
 template <int kSet>
-__device__ Work work_of(const AttendArgs& a, int i, int n, const uint32_t* s_cum) {
+__device__ __forceinline__ void work_of(const AttendArgs& a, int i, int n, const uint32_t* s_cum, Work& w) {
     uint32_t bad = 0;
-    Work w{};
     if (kSet) {
         const Group g = shared_of(a, i, bad);
         w.start = uniform(g.start);
         w.n = uniform(g.n);
         w.ke = uniform(g.ke);
-        w.group = -1;
         w.table = a.shared_table + (size_t)i * a.shared_width;
-        return w;
+        return;
     }
     Request q;
     if (i < kCached) q = ((const Request*)(s_cum + n + 1))[i];
@@ -294,25 +299,13 @@ __device__ Work work_of(const AttendArgs& a, int i, int n, const uint32_t* s_cum
     w.ke = w.ln + w.n;
     w.group = uniform(q.group);
     w.table = a.table + (size_t)i * a.width;
-    if (w.kb > 0) {
-        const Group g = shared_of(a, w.group, bad);
-        // (rows outside the group's, as offsets that fall would have it, have no part there)
-        if (uniform(g.ke) > 0 && w.start >= uniform(g.start) && w.start + w.n <= uniform(g.start + g.n)) {
-            w.shared.start = uniform(g.start);
-            w.shared.n = uniform(g.n);
-            w.shared.units = units_in(a, 1, uniform(g.ke));
-            w.shared.tiles = tiles_in(a, 1, w.shared.n);
-            w.shared.u0 = uniform(a.cum[w.group]) * a.Hkv;
-        }
-    }
-    return w;
 }
 
-// A request's table has to begin with its group's pages.
+// A request's table has to begin with its group's pages.  One wave.
 __device__ void check_prefix(const AttendArgs& a, const Work& q) {
     bool differs = false;
     const int32_t* shared = a.shared_table + (size_t)q.group * a.shared_width;
-    for (int p = threadIdx.x; p < q.kb >> a.page_shift; p += blockDim.x) differs |= q.table[p] != shared[p];
+    for (int p = threadIdx.x & 63; p < q.kb >> a.page_shift; p += 64) differs |= q.table[p] != shared[p];
     if (differs) raise_status(a.status, kStatusBadPage);
 }
 
@@ -351,37 +344,28 @@ __device__ __forceinline__ void join_parts(const AttendArgs& a, int set, int wa,
     }
 }
 
-// The shared keys' parts for the columns from f0 on: they lie in one tile of the group's
-// launch, or from column `edge` on in the next one (a tile there is at least as wide).
-struct SharedParts {
-    int edge, col0;        // the first column of the second tile; f0's column in the first one
-    int first[2], last[2];  // the workers that hold parts of the two
+// Where a launch leaves the part of a column of a segment that it did not split: set 0 where
+// the requests' shared keys are still to be joined, set 1 always.
+struct Dense {
+    float *o, *m, *l;
 };
-
-__device__ SharedParts shared_parts(const AttendArgs& a, const Split& split, const Shared& g, int f0, int h) {
-    SharedParts p{};
-    const int at = f0 - g.start * a.G, tile = at >> a.tile_shift[1];
-    p.col0 = at - (tile << a.tile_shift[1]);
-    p.edge = a.tile[1] - p.col0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t u0 = g.u0 + (h * g.tiles + min(tile + i, (int)g.tiles - 1)) * g.units;
-        p.first[i] = uniform(split.worker_of(u0));
-        p.last[i] = uniform(split.worker_of(u0 + g.units - 1));
-    }
-    return p;
+__device__ __forceinline__ Dense dense_of(const AttendArgs& a, int set, int f, int h) {
+    const size_t all = (size_t)a.Hkv * a.rows * a.G, at = (size_t)h * a.rows * a.G + f;
+    float* p = a.dense[set];
+    return Dense{p + at * a.D, p + all * a.D + at, p + all * (a.D + 1) + at};
 }
 
-// Adds them for column c of f0's tile, key head h.
-__device__ __forceinline__ void join_shared(const AttendArgs& a, const SharedParts& p, int f0, int c, int h, int c8, float& m,
-                                            float& l, float (&acc)[8]) {
-    const int i = c >= p.edge;
-    if (p.first[i] == p.last[i]) {
-        const size_t n = (size_t)a.Hkv * a.rows * a.G, f = (size_t)h * a.rows * a.G + f0 + c;
-        const float* o = a.dense + f * a.D + c8 * 8;
-        join(m, l, acc, a.dense[n * a.D + f], a.dense[n * (a.D + 1) + f], *(const float4*)o, *(const float4*)(o + 4));
+// Adds what launch `set` has of query row f (row G + head of the group) of key head h: column c
+// of its item, whose first unit is u0 and whose key heads have `tiles` tiles of `units`.
+__device__ __forceinline__ void join_item(const AttendArgs& a, int set, const Split& split, uint32_t u0, int tiles,
+                                          uint32_t units, int f, int c, int h, int c8, float& m, float& l, float (&acc)[8]) {
+    const uint32_t u = u0 + (h * tiles + (c >> a.tile_shift[set])) * units;
+    const int wa = split.worker_of(u), wb = split.worker_of(u + units - 1);
+    if (wa == wb) {
+        const Dense d = dense_of(a, set, f, h);
+        join(m, l, acc, *d.m, *d.l, *(const float4*)(d.o + c8 * 8), *(const float4*)(d.o + c8 * 8 + 4));
     } else {
-        join_parts(a, 1, p.first[i], p.last[i], i ? c - p.edge : p.col0 + c, c8, m, l, acc);
+        join_parts(a, set, wa, wb, c & (a.tile[set] - 1), c8, m, l, acc);
     }
 }
 
@@ -446,39 +430,69 @@ __device__ __forceinline__ uint32_t clear_masked(s16x8& v, int valid) {
     return any;
 }
 
-// Column c of the tile at f0 is done as far as this workgroup goes: eight dims of it, from
-// 8 c8 on.  The result, where the segment ends here and its keys were the requests' own;
-// else the part, for whoever joins it.
+// Column c of the tile at f0 is done as far as this worker goes: eight dims of it, from 8 c8
+// on.  The result, where the segment ends here and has all of its keys (final); else the
+// part, for whoever joins it.
 template <class E, int kSet>
-__device__ __forceinline__ void finish(const AttendArgs& a, const SharedParts& parts, bool shared, bool whole,
-                                       bool begins, int f0, int c, int h, int c8, float m, float l, float (&acc)[8]) {
-    if (whole && kSet == 0) {
-        if (shared) join_shared(a, parts, f0, c, h, c8, m, l, acc);
+__device__ __forceinline__ void finish(const AttendArgs& a, int worker, bool final, bool whole, bool begins, int f0, int c,
+                                       int h, int c8, float m, float l, const float (&acc)[8]) {
+    if (kSet == 0 && final) {
         store_row<E>(a, f0 + c, h, c8, m, l, acc);
         return;
     }
-    float *po, *pm, *pl;
+    Dense d;
     if (whole) {
-        const size_t all = (size_t)a.Hkv * a.rows * a.G, at = (size_t)h * a.rows * a.G + f0 + c;
-        po = a.dense + at * a.D;
-        pm = a.dense + all * a.D + at;
-        pl = a.dense + all * (a.D + 1) + at;
+        d = dense_of(a, kSet, f0 + c, h);
     } else {
         const size_t tile = a.tile[kSet];
-        float* slot = slot_of(a, kSet, blockIdx.x, begins);
-        po = slot + (size_t)c * a.D;
-        pm = slot + tile * a.D + c;
-        pl = slot + tile * (a.D + 1) + c;
+        float* slot = slot_of(a, kSet, worker, begins);
+        d = Dense{slot + (size_t)c * a.D, slot + tile * a.D + c, slot + tile * (a.D + 1) + c};
     }
-    *(float4*)(po + c8 * 8) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    *(float4*)(po + c8 * 8 + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    *(float4*)(d.o + c8 * 8) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    *(float4*)(d.o + c8 * 8 + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
     if (c8 == 0) {
-        *pm = m;
-        *pl = l;
+        *d.m = m;
+        *d.l = l;
     }
 }
 
-__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32, 64); }
+// A wave's 32 columns done, from c0 of the tile at f0 on: 32 dims at a time through LDS (pitch
+// 36: the lanes' 16-byte stores and loads meet no bank twice), eight dims of a column to a
+// lane.  m and l are the lanes' columns'.
+constexpr int kPitch = 36;
+
+template <class E, int kSet, int NT>
+__device__ __forceinline__ void finish_wave(const AttendArgs& a, float* s_o, int worker, bool final, bool whole,
+                                            bool begins, int f0, int c0, int nf, int h, float m, float l, const f32x16 (&o)[NT]) {
+    const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            *(float4*)&s_o[col * kPitch + 8 * j + 4 * half] =
+                make_float4(o[t][4 * j], o[t][4 * j + 1], o[t][4 * j + 2], o[t][4 * j + 3]);
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int e = lane; e < 128; e += 64) {
+            const int c = e >> 2, c8 = e & 3;
+            const float jm = __shfl(m, c, 64), jl = __shfl(l, c, 64);
+            const float4 x = *(const float4*)&s_o[c * kPitch + c8 * 8], y = *(const float4*)&s_o[c * kPitch + c8 * 8 + 4];
+            const float acc[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+            if (c0 + c < nf) finish<E, kSet>(a, worker, final, whole, begins, f0, c0 + c, h, t * 4 + c8, jm, jl, acc);
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// The larger of a lane's value and that of the lane 32 on; and their sum.
+__device__ __forceinline__ float max_halves(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float add_halves(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
 
 // Page ids of a table row, 64 entries at a time in the lanes of a wave: entry i is read
 // with readlane, so that the next block's address does not wait for memory.
@@ -496,239 +510,317 @@ struct PageIds {
         base = first;
         const int i = first + lane;
         ids = table[i < n ? i : n - 1];
-        asm volatile("" : "+v"(ids));  // waited for here, so that readers need not wait for what else is under way
     }
+    // Waits for the ids here, so that readers need not wait for what else is under way.
+    __device__ __forceinline__ void settle() { asm volatile("" : "+v"(ids)); }
     __device__ __forceinline__ int at(int i, int lane) {
-        if (i - base >= 64) fetch(i, lane);
+        if (i - base >= 64) {
+            fetch(i, lane);
+            settle();
+        }
         return __builtin_amdgcn_readlane(ids, i - base);
     }
 };
+
+// A worker's way through its units: the segment at hand, and the item it belongs to.
+template <int kSet, int kTile, int kUnit>
+struct Cursor {
+    uint32_t u, u_end;
+    uint32_t item_u0 = 0, item_u1 = 0;  // units of the item
+    Work q{};
+    uint32_t units, unit0, unit1;  // the segment's units; those [unit0, unit1) are the worker's
+    int h, f0, nf;                 // its key head and columns
+
+    int worker;
+    bool leads;  // this lane speaks for the worker
+
+    __device__ __forceinline__ Cursor(const Split& split, int w, bool lead)
+        : u(split.first(w)), u_end(split.first(w + 1)), worker(w), leads(lead) {}
+    // The segment of unit u.
+    __device__ __forceinline__ void look(const AttendArgs& a, const Split& split, int n, const uint32_t* s_cum) {
+        if (u >= item_u1) {
+            const int i = item_of(a, s_cum, n, u);
+            item_u0 = uniform(s_cum[i]) * a.Hkv;
+            item_u1 = uniform(s_cum[i + 1]) * a.Hkv;
+            work_of<kSet>(a, i, n, s_cum, q);
+        }
+        units = units_of<kUnit>(q.ke - q.kb);
+        const uint32_t tiles = tiles_of<kTile>(a, q.n), in = u - item_u0, seg = in / units;
+        unit0 = in % units;
+        unit1 = min(units, unit0 + (u_end - u));
+        h = seg / tiles;
+        const int tile = seg % tiles;
+        f0 = q.start * a.G + tile * kTile;
+        nf = min(kTile, q.n * a.G - tile * kTile);
+        if (kSet == 0 && q.kb > 0 && seg == 0 && unit0 == 0) check_prefix(a, q);
+        if (kSet == 0 && unit0 > 0 && leads)  // begun by an earlier worker: for the joining kernel
+            a.ends[worker] = AttendEnd{units, split.worker_of(u - unit0), split.worker_of(u - unit0 + units - 1), f0,
+                                           nf, h};
+    }
+    __device__ __forceinline__ bool whole() const { return unit0 == 0 && unit1 == units; }
+    // On to the next segment; false where there is none.
+    __device__ __forceinline__ bool step() {
+        u += unit1 - unit0;
+        return u < u_end;
+    }
+    // The last key that the columns of query row f / G see.
+    __device__ __forceinline__ int last_of(const AttendArgs& a, int f) const {
+        return kSet ? q.ke - 1 : q.ln + f / a.G - q.start;
+    }
+};
+
+// Q^T as the first product's second operand: column f's dims 16 c + 8 half + 0..7.
+template <int D>
+__device__ __forceinline__ void load_q(const AttendArgs& a, s16x8 (&qf)[D / 16], int f, int h, int half) {
+    const uint16_t* qp = a.q + (size_t)(f / a.G) * a.q_stride + (size_t)(h * a.G + f % a.G) * D + half * 8;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) qf[c] = *(const s16x8*)(qp + c * 16);
+}
 
 // The few-rows form.  A workgroup takes kTiles tiles of the segment's columns: its four
 // waves are 4 / kTiles groups of keys by kTiles tiles, so that up to 64 columns read the
 // keys once.  Each wave streams: the next block's K is requested as soon as the first
 // product has used this one's, the next V after the second product, so about 16 KB a wave
-// are under way while it computes (kSet 0: the requests' own keys; 1: the groups' shared
-// ones).
+// are under way while it computes; and the next segment's rows, page ids and first keys
+// are requested before this one's waves are joined (kSet 0: the requests' own keys; 1: the
+// groups' shared ones).
 template <class E, int D, int kSet, int kTiles>
 __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs a) {
     constexpr int NT = D / 32, NC = D / 16;
     constexpr int kKeyWaves = 4 / kTiles;
     constexpr int kUnit = 32 * kKeyWaves;
     constexpr int kDims = D <= 128 ? D : 128;  // dims joined over the waves at a time
-    constexpr int kPitch = kDims + 4;
-    __shared__ float s_o[4][32][kPitch];
+    constexpr int kRow = kDims + 4;
+    __shared__ float s_o[4][32][kRow];
     __shared__ float s_m[4][32], s_l[4][32];
     __shared__ uint32_t s_base[8];
-    extern __shared__ uint32_t s_cum[];  // running units, n + 1
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    extern __shared__ uint32_t s_cum[];  // running units, n + 1, then the requests
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int col = lane & 31, half = lane >> 5;
     const int key_wave = wave / kTiles, sub = wave % kTiles;
     const int n = kSet ? a.n_groups : a.R;
     const uint32_t total = plan<kSet, kT>(a, n, s_cum, s_base);
-    const Split split(total, a.workers[kSet]);
+    const Split split(a, kSet, total);
     if (kSet == 0 && tid == 0) a.ends[blockIdx.x].units = 0;
     if ((int)blockIdx.x >= split.workers) return;
-    const Split split1(kSet == 0 && a.n_groups ? uniform(a.cum[a.n_groups]) * a.Hkv : 0, a.workers[1]);
-    uint32_t u = split.first(blockIdx.x);
-    const uint32_t u_end = split.first(blockIdx.x + 1);
     const int shift = a.page_shift - 4, in_page = (1 << shift) - 1;  // blocks of 16 in a page
-    const int head_shift = __builtin_ctz(D) + a.page_shift;  // a head's elements in a page
+    const int head_shift = __builtin_ctz(D) + a.page_shift;          // a head's elements in a page
+    const int swapped = (col & 3) | ((col & 4) << 1) | ((col & 8) >> 1);  // key of this lane in its block of 16
 
-    uint32_t item_u0 = 0, item_u1 = 0;  // units of the item at hand
-    Work q{};
-    while (u < u_end) {
-        if (u >= item_u1) {
-            const int i = item_of(a, s_cum, n, u);
-            item_u0 = __builtin_amdgcn_readfirstlane(s_cum[i]) * a.Hkv;
-            item_u1 = __builtin_amdgcn_readfirstlane(s_cum[i + 1]) * a.Hkv;
-            q = work_of<kSet>(a, i, n, s_cum);
-        }
-        const uint32_t units = units_of<kUnit>(q.ke - q.kb), tiles = tiles_of<32 * kTiles>(a, q.n);
-        const uint32_t in = u - item_u0, seg = in / units, unit0 = in % units;
-        const int h = seg / tiles, tile = seg % tiles;
-        const uint32_t unit1 = min(units, unit0 + (u_end - u));
-        const int f0 = q.start * a.G + tile * (32 * kTiles);
-        const int nf = min(32 * kTiles, q.n * a.G - tile * (32 * kTiles));
-        if (kSet == 0 && q.kb > 0 && seg == 0 && unit0 == 0) check_prefix(a, q);
-        if (kSet == 0 && unit0 > 0 && tid == 0)  // begun by an earlier worker: for the joining kernel
-            a.ends[blockIdx.x] = AttendEnd{units, split.worker_of(u - unit0), split.worker_of(u - unit0 + units - 1), f0,
-                                           nf, h, q.shared.start, q.shared.n, q.shared.u0, q.shared.units, q.shared.tiles};
+    Cursor<kSet, 32 * kTiles, kUnit> cur(split, blockIdx.x, tid == 0);
+    s16x8 qf[NC], kf[NC], vf[NT][2];
+    f32x16 o[NT];
+    PageIds pages;
+    const uint16_t *kp[2], *vp[2];
+    bool have[2], bad_page = false;
+    int pos, pos_end, last, first_last;
 
-        // Q^T as the first product's second operand: this lane's column, dims 16 c + 8 half + 0..7.
-        const int f = f0 + min(sub * 32 + col, nf - 1);
-        const uint16_t* qp = a.q + (size_t)(f / a.G) * a.q_stride + (size_t)(h * a.G + f % a.G) * D + half * 8;
-        s16x8 qf[NC];
+    // The two blocks of 16 keys at position p: where K and V lie, and whether they are there.
+    const auto locate = [&](int p, bool(&there)[2]) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) qf[c] = *(const s16x8*)(qp + c * 16);
-        const int last = kSet ? q.ke - 1 : q.ln + f / a.G - q.start;            // the column's last key
-        const int first_last = kSet ? q.ke - 1 : q.ln + f0 / a.G - q.start;  // the earliest of them
+        for (int b = 0; b < 2; ++b) {
+            const int blk = (p >> 4) + b;
+            there[b] = p + b * 16 < cur.q.ke;
+            int page = there[b] ? pages.at(blk >> shift, lane) : 0;
+            if ((unsigned)page >= (unsigned)a.n_pages) {
+                page = 0;
+                there[b] = false;
+                bad_page = true;
+            }
+            const size_t at =
+                (((size_t)(unsigned)page * (unsigned)a.Hkv + cur.h) << head_shift) + (size_t)(blk & in_page) * (16 * D);
+            kp[b] = a.k + at;
+            vp[b] = a.v + at;
+        }
+    };
+    const auto load_k = [&]() {
+        const uint16_t* kl = (col < 16 ? kp[0] : kp[1]) + half * 128 + swapped * 8;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) kf[c] = *(const s16x8*)(kl + c * 256);
+    };
+    const auto load_v = [&]() {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) vf[t][b] = *(const s16x8*)(vp[b] + (t * 32 + col) * 16 + half * 8);
+    };
+    // A segment's beginning, in two steps: its columns and page ids, then its first keys.
+    const auto enter = [&]() {
+        const int f = cur.f0 + min(sub * 32 + col, cur.nf - 1);
+        load_q<D>(a, qf, f, cur.h, half);
+        last = cur.last_of(a, f);               // the column's last key
+        first_last = cur.last_of(a, cur.f0);  // the earliest of them
+        pos = cur.q.kb + (int)(cur.unit0 * kUnit) + key_wave * 32;
+        pos_end = sub * 32 < cur.nf ? min(cur.q.ke, cur.q.kb + (int)(cur.unit1 * kUnit)) : 0;
+        if (pos < pos_end)
+            pages.start(cur.q.table, (cur.q.ke + (1 << a.page_shift) - 1) >> a.page_shift, pos >> a.page_shift, lane);
+    };
+    const auto first_keys = [&]() {
+        if (pos >= pos_end) return;
+        pages.settle();
+        locate(pos, have);
+        load_k();
+        __builtin_amdgcn_sched_barrier(0);  // K first, as in the loop: its waits count on this order
+        load_v();
+    };
 
-        f32x16 o[NT];
+    // What joining a finished segment's waves needs, while the next segment is at hand.
+    float ms = -kInf, l = 0.f;
+    bool final = false, whole = false, begins = false;
+    int f0 = 0, nf = 0, h = 0;
+    // The waves' parts joined, column by column, eight dims to a thread, kDims dims at a time.
+    const auto put = [&](int d0) {
+        __syncthreads();
+        if (half == 0) {
+            s_m[wave][col] = ms;
+            s_l[wave][col] = l;
+        }
+#pragma unroll
+        for (int t = 0; t < kDims / 32; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const f32x16& x = o[d0 / 32 + t];
+                *(float4*)&s_o[wave][col][t * 32 + 8 * j + 4 * half] =
+                    make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+            }
+        __syncthreads();
+    };
+    const auto take = [&](int d0) {
+        for (int e = tid; e < nf * (kDims / 8); e += kT) {
+            const int c = e / (kDims / 8), c8 = e % (kDims / 8);
+            float jm = -kInf, jl = 0.f, acc[8] = {};
+#pragma unroll
+            for (int w = 0; w < kKeyWaves; ++w) {
+                const int from = w * kTiles + c / 32;
+                join(jm, jl, acc, s_m[from][c % 32], s_l[from][c % 32], *(const float4*)&s_o[from][c % 32][c8 * 8],
+                     *(const float4*)&s_o[from][c % 32][c8 * 8 + 4]);
+            }
+            finish<E, kSet>(a, blockIdx.x, final, whole, begins, f0, c, h, d0 / 8 + c8, jm, jl, acc);
+        }
+    };
+
+    bool more = true;
+    for (bool first = true;; first = false) {
+        if (more) {
+            cur.look(a, split, n, s_cum);
+            enter();
+        }
+        if (D <= kDims) {
+            if (!first) put(0);
+            if (more) first_keys();  // on their way while the last segment is joined
+            if (!first) take(0);
+        } else {  // (no registers for both)
+            if (!first) {
+#pragma unroll
+                for (int d0 = 0; d0 < D; d0 += kDims) {
+                    put(d0);
+                    take(d0);
+                }
+            }
+            if (more) first_keys();
+        }
+        if (!more) break;
 #pragma unroll
         for (int t = 0; t < NT; ++t) o[t] = f32x16{};
-        float m = -kInf, l = 0.f;  // m of the raw scores; l this half's share of the sum
-
-        const int swapped = (col & 3) | ((col & 4) << 1) | ((col & 8) >> 1);  // key of this lane in its block of 16
-        int pos = q.kb + (int)(unit0 * kUnit) + key_wave * 32;
-        const int pos_end = min(q.ke, q.kb + (int)(unit1 * kUnit));
-        if (pos < pos_end && sub * 32 < nf) {
-            PageIds pages;
-            pages.start(q.table, (q.ke + (1 << a.page_shift) - 1) >> a.page_shift, pos >> a.page_shift, lane);
-            const uint16_t *kp[2], *vp[2];
-            bool have[2], next_have[2], bad_page = false;
-            s16x8 kf[NC], vf[NT][2];
-            // The two blocks of 16 keys at position p: where K and V lie, and whether they are there.
-            const auto locate = [&](int p, bool(&there)[2]) {
+        float m = -kInf;  // of the raw scores; l is this half's share of the sum
+        l = 0.f;
+        int special_from = -1;     // the first block with values that add_special has to add
+        // K is waited for here, where other loads and stores may be under way as well; inside the
+        // loop its waits then count on the order of the loop's own loads.
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const int blk = (p >> 4) + b;
-                    there[b] = p + b * 16 < q.ke;
-                    int page = there[b] ? pages.at(blk >> shift, lane) : 0;
-                    if ((unsigned)page >= (unsigned)a.n_pages) {
-                        page = 0;
-                        there[b] = false;
-                        bad_page = true;
-                    }
-                    const size_t at =
-                        (((size_t)(unsigned)page * (unsigned)a.Hkv + h) << head_shift) + (size_t)(blk & in_page) * (16 * D);
-                    kp[b] = a.k + at;
-                    vp[b] = a.v + at;
-                }
-            };
-            const auto load_k = [&]() {
-                const uint16_t* kl = (col < 16 ? kp[0] : kp[1]) + half * 128 + swapped * 8;
+        for (int c = 0; c < NC; ++c) asm volatile("" : "+v"(kf[c]));
 #pragma unroll
-                for (int c = 0; c < NC; ++c) kf[c] = *(const s16x8*)(kl + c * 256);
-            };
-            const auto load_v = [&]() {
+        for (int t = 0; t < NT; ++t) asm volatile("" : "+v"(vf[t][0]), "+v"(vf[t][1]));
+        if (pos < pos_end) do {
+            f32x16 s = {};
+#pragma unroll
+            for (int c = 0; c < NC; ++c) s = E::mfma(kf[c], qf[c], s);
+            // (after the last keys these once more, unused: a load that may be left out would have
+            // every later wait count on its absence)
+            const int next = pos + kUnit;
+            bool next_have[2];
+            locate(next < pos_end ? next : pos, next_have);
+            load_k();
+            const bool masked = pos + 31 > first_last || !have[0] || !have[1];
+            if (masked) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (pos + (j / 8) * 16 + half * 8 + j % 8 > last || !have[j / 8]) s[j] = -kInf;
+            }
+            float mx = s[0];
+#pragma unroll
+            for (int j = 1; j < 16; ++j) mx = fmaxf(mx, s[j]);
+            mx = max_halves(mx);
+            if (__ballot((mx - m) * a.scale_log2 > kLag)) {
+                const float m_new = fmaxf(m, mx);
+                const float alpha = __builtin_amdgcn_exp2f((m - (m_new == -kInf ? 0.f : m_new)) * a.scale_log2);
+                m = m_new;
+                l *= alpha;
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) vf[t][b] = *(const s16x8*)(vp[b] + (t * 32 + col) * 16 + half * 8);
-            };
-            int special_from = -1;  // the first block with values that add_special has to add
-            locate(pos, have);
-            load_k();
+                    for (int j = 0; j < 16; ++j) o[t][j] *= alpha;
+            }
+            const float mc = m == -kInf ? 0.f : m * a.scale_log2;
+            s16x8 pf[2];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], a.scale_log2, -mc));
+                l += p;
+                pf[j / 8][j % 8] = (short)E::bits(p);  // weights of at most 1, rounded for the matrix instruction
+            }
+            if (masked) {
+                uint32_t special = 0;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        special |= clear_masked<E>(vf[t][b], have[b] ? cur.q.ke - (pos + b * 16 + half * 8) : 0);
+                        __builtin_amdgcn_sched_barrier(0);  // one after the other, in few registers
+                    }
+                if (special_from < 0 && __ballot(special != 0)) special_from = pos;
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) o[t] = E::mfma(vf[t][1], pf[1], E::mfma(vf[t][0], pf[0], o[t]));
             load_v();
-            for (;;) {
-                f32x16 s = {};
+            pos = next;
+            have[0] = next_have[0];
+            have[1] = next_have[1];
+        } while (pos < pos_end);
+        l = add_halves(l);
+        if (special_from >= 0) {
+            pages.fetch(special_from >> a.page_shift, lane);
+            pages.settle();
+            for (pos = special_from; pos < pos_end; pos += kUnit) {
+                locate(pos, have);
+                s16x8 sees[2];
 #pragma unroll
-                for (int c = 0; c < NC; ++c) s = E::mfma(kf[c], qf[c], s);
-                const int next = pos + kUnit;
-                const bool more = next < pos_end;
-                if (more) {
-                    locate(next, next_have);
-                    load_k();
-                }
-                const bool masked = pos + 31 > first_last || !have[0] || !have[1];
-                if (masked) {
+                for (int j = 0; j < 16; ++j)
+                    sees[j / 8][j % 8] =
+                        pos + (j / 8) * 16 + half * 8 + j % 8 <= last && have[j / 8] ? (short)E::kOne : (short)0;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (pos + (j / 8) * 16 + half * 8 + j % 8 > last || !have[j / 8]) s[j] = -kInf;
-                }
-                float mx = s[0];
-#pragma unroll
-                for (int j = 1; j < 16; ++j) mx = fmaxf(mx, s[j]);
-                mx = fmaxf(mx, other_half(mx));
-                if (__ballot(mx > m)) {  // a larger maximum: what has been summed so far shrinks
-                    const float m_new = fmaxf(m, mx);
-                    const float alpha = __builtin_amdgcn_exp2f((m - (m_new == -kInf ? 0.f : m_new)) * a.scale_log2);
-                    m = m_new;
-                    l *= alpha;
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) o[t][j] *= alpha;
-                }
-                const float mc = m == -kInf ? 0.f : m * a.scale_log2;
-                s16x8 pf[2];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], a.scale_log2, -mc));
-                    l += p;
-                    pf[j / 8][j % 8] = (short)E::bits(p);  // weights of at most 1, rounded for the matrix instruction
-                }
-                if (masked) {
-                    uint32_t special = 0;
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int t = 0; t < NT; ++t)
-                            special |= clear_masked<E>(vf[t][b], have[b] ? q.ke - (pos + b * 16 + half * 8) : 0);
-                    if (special_from < 0 && __ballot(special != 0)) special_from = pos;
-                }
-#pragma unroll
-                for (int t = 0; t < NT; ++t) o[t] = E::mfma(vf[t][1], pf[1], E::mfma(vf[t][0], pf[0], o[t]));
-                if (!more) break;
-                load_v();
-                pos = next;
-                have[0] = next_have[0];
-                have[1] = next_have[1];
-            }
-            l += other_half(l);
-            if (bad_page && lane == 0) raise_status(a.status, kStatusBadPage);
-            if (special_from >= 0) {
-                pages.fetch(special_from >> a.page_shift, lane);
-                for (pos = special_from; pos < pos_end; pos += kUnit) {
-                    locate(pos, have);
-                    s16x8 sees[2];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        sees[j / 8][j % 8] =
-                            pos + (j / 8) * 16 + half * 8 + j % 8 <= last && have[j / 8] ? (short)E::kOne : (short)0;
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        add_special<E>(o[t], *(const s16x8*)(vp[0] + (t * 32 + col) * 16 + half * 8),
-                                       *(const s16x8*)(vp[1] + (t * 32 + col) * 16 + half * 8), sees[0], sees[1]);
-                }
+                for (int t = 0; t < NT; ++t)
+                    add_special<E>(o[t], *(const s16x8*)(vp[0] + (t * 32 + col) * 16 + half * 8),
+                                   *(const s16x8*)(vp[1] + (t * 32 + col) * 16 + half * 8), sees[0], sees[1]);
             }
         }
-        const float ms = m == -kInf ? -kInf : m * a.scale_log2;
-
-        // The waves' parts joined, column by column, eight dims to a thread.
-        const bool whole = unit0 == 0 && unit1 == units;
-        SharedParts parts{};
-        if (kSet == 0 && whole && q.shared.n > 0) parts = shared_parts(a, split1, q.shared, f0, h);
-#pragma unroll
-        for (int d0 = 0; d0 < D; d0 += kDims) {
-            __syncthreads();
-            if (half == 0) {
-                s_m[wave][col] = ms;
-                s_l[wave][col] = l;
-            }
-#pragma unroll
-            for (int t = 0; t < kDims / 32; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const f32x16& x = o[d0 / 32 + t];
-                    *(float4*)&s_o[wave][col][t * 32 + 8 * j + 4 * half] =
-                        make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-                }
-            __syncthreads();
-            for (int e = tid; e < nf * (kDims / 8); e += kT) {
-                const int c = e / (kDims / 8), c8 = e % (kDims / 8);
-                float jm = -kInf, jl = 0.f, acc[8] = {};
-#pragma unroll
-                for (int w = 0; w < kKeyWaves; ++w) {
-                    const int from = w * kTiles + c / 32;
-                    join(jm, jl, acc, s_m[from][c % 32], s_l[from][c % 32], *(const float4*)&s_o[from][c % 32][c8 * 8],
-                         *(const float4*)&s_o[from][c % 32][c8 * 8 + 4]);
-                }
-                finish<E, kSet>(a, parts, q.shared.n > 0, whole, unit0 == 0, f0, c, h, d0 / 8 + c8, jm, jl, acc);
-            }
-        }
-        u += unit1 - unit0;
+        ms = m == -kInf ? -kInf : m * a.scale_log2;
+        whole = cur.whole();
+        begins = cur.unit0 == 0;
+        f0 = cur.f0;
+        nf = cur.nf;
+        h = cur.h;
+        final = whole && cur.q.kb == 0;
+        more = cur.step();
     }
+    if (bad_page && lane == 0) raise_status(a.status, kStatusBadPage);
 }
 
 // The many-rows form, for groups and prompts: a wave takes 32 columns, the workgroup eight
 // (at head_dim 64 and 256: four) times as many, and all waves read the same 64 keys from LDS, which
 // the next 64 are brought to meanwhile (global_load_lds: memory to LDS with no registers
 // between).  The lanes of such a load pick their 16 bytes so that what a wave reads later,
-// an operand of a matrix instruction, lies in LDS lane after lane.  The running maximum of
-// a column follows only when it grows by more than 8 in the exponent of two; until then the
-// weights are taken relative to the older one, at most 2^8, and nothing has to be rescaled.
+// an operand of a matrix instruction, lies in LDS lane after lane.
 template <int D>
 struct Wide {
     static constexpr int kWaves = D == 128 ? 8 : 4;
@@ -740,7 +832,7 @@ struct Wide {
 template <class E, int D, int kSet>
 __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::kPerCu) void attend_wide_kernel(AttendArgs a) {
     typedef Wide<D> W;
-    constexpr int NT = D / 32, NC = D / 16, kPitch = 36;
+    constexpr int NT = D / 32, NC = D / 16;
     constexpr int kStage = 8 * W::kBlock * 2, kJoin = W::kWaves * 32 * kPitch * 4;  // bytes
     __shared__ __attribute__((aligned(16))) char s_mem[2 * kStage > kJoin ? 2 * kStage : kJoin];
     __shared__ int s_have[2][4];
@@ -750,12 +842,9 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
     const int col = lane & 31, half = lane >> 5;
     const int n = kSet ? a.n_groups : a.R;
     const uint32_t total = plan<kSet, W::kThreads>(a, n, s_cum, s_base);
-    const Split split(total, a.workers[kSet]);
+    const Split split(a, kSet, total);
     if (kSet == 0 && tid == 0) a.ends[blockIdx.x].units = 0;
     if ((int)blockIdx.x >= split.workers) return;
-    const Split split1(kSet == 0 && a.n_groups ? uniform(a.cum[a.n_groups]) * a.Hkv : 0, a.workers[1]);
-    uint32_t u = split.first(blockIdx.x);
-    const uint32_t u_end = split.first(blockIdx.x + 1);
     const int shift = a.page_shift - 4, in_page = (1 << shift) - 1;  // blocks of 16 in a page
     const int head_shift = __builtin_ctz(D) + a.page_shift;          // a head's elements in a page
     // where this lane's 16 bytes of each 1 KB of a block come from: K's keys with bits 2 and 3 of
@@ -763,43 +852,25 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
     const int key = lane & 15, k_from = (lane >> 4) * 128 + ((key & 3) | ((key & 4) << 1) | ((key & 8) >> 1)) * 8;
     const int v_from = col * 16 + half * 8;
 
-    uint32_t item_u0 = 0, item_u1 = 0;  // units of the item at hand
-    Work q{};
-    while (u < u_end) {
-        if (u >= item_u1) {
-            const int i = item_of(a, s_cum, n, u);
-            item_u0 = uniform(s_cum[i]) * a.Hkv;
-            item_u1 = uniform(s_cum[i + 1]) * a.Hkv;
-            q = work_of<kSet>(a, i, n, s_cum);
-        }
-        const uint32_t units = units_of<W::kUnit>(q.ke - q.kb), tiles = tiles_of<W::kTile>(a, q.n);
-        const uint32_t in = u - item_u0, seg = in / units, unit0 = in % units;
-        const int h = seg / tiles, tile = seg % tiles;
-        const uint32_t unit1 = min(units, unit0 + (u_end - u));
-        const int f0 = q.start * a.G + tile * W::kTile;
-        const int nf = min(W::kTile, q.n * a.G - tile * W::kTile);
-        if (kSet == 0 && q.kb > 0 && seg == 0 && unit0 == 0) check_prefix(a, q);
-        if (kSet == 0 && unit0 > 0 && tid == 0)  // begun by an earlier worker: for the joining kernel
-            a.ends[blockIdx.x] = AttendEnd{units, split.worker_of(u - unit0), split.worker_of(u - unit0 + units - 1), f0,
-                                           nf, h, q.shared.start, q.shared.n, q.shared.u0, q.shared.units, q.shared.tiles};
-
+    Cursor<kSet, W::kTile, W::kUnit> cur(split, blockIdx.x, tid == 0);
+    do {
+        cur.look(a, split, n, s_cum);
+        const Work& q = cur.q;
+        const int f0 = cur.f0, nf = cur.nf, h = cur.h;
         const int f = f0 + min(wave * 32 + col, nf - 1);
-        const uint16_t* qp = a.q + (size_t)(f / a.G) * a.q_stride + (size_t)(h * a.G + f % a.G) * D + half * 8;
         s16x8 qf[NC];
-#pragma unroll
-        for (int c = 0; c < NC; ++c) qf[c] = *(const s16x8*)(qp + c * 16);
+        load_q<D>(a, qf, f, h, half);
         // The column's last key; the wave's earliest and latest of them, and the tile's latest.
-        const int last = kSet ? q.ke - 1 : q.ln + f / a.G - q.start;
-        const int first_last = kSet ? q.ke - 1 : q.ln + (f0 + min(wave * 32, nf - 1)) / a.G - q.start;
-        const int wave_end = wave * 32 >= nf ? 0 : kSet ? q.ke : q.ln + (f0 + min(wave * 32 + 31, nf - 1)) / a.G - q.start + 1;
-        const int tile_end = kSet ? q.ke : q.ln + (f0 + nf - 1) / a.G - q.start + 1;
+        const int last = cur.last_of(a, f), first_last = cur.last_of(a, f0 + min(wave * 32, nf - 1));
+        const int wave_end = wave * 32 >= nf ? 0 : cur.last_of(a, f0 + min(wave * 32 + 31, nf - 1)) + 1;
+        const int tile_end = cur.last_of(a, f0 + nf - 1) + 1;
 
         f32x16 o[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) o[t] = f32x16{};
         float m = -kInf, l = 0.f;  // m of the raw scores; l this half's share of the sum
-        int pos = q.kb + (int)(unit0 * W::kUnit);
-        const int pos_end = min(tile_end, q.kb + (int)(unit1 * W::kUnit));
+        int pos = q.kb + (int)(cur.unit0 * W::kUnit);
+        const int pos_end = min(tile_end, q.kb + (int)(cur.unit1 * W::kUnit));
         int special_from = -1;
         bool bad_page = false;
         PageIds pages;
@@ -838,7 +909,10 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
         };
 
         __syncthreads();  // LDS is free
-        if (pos < pos_end) bring(pos, 0);
+        if (pos < pos_end) {
+            pages.settle();
+            bring(pos, 0);
+        }
         for (int buf = 0; pos < pos_end; buf ^= 1, pos += W::kUnit) {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's share of the 64 keys has landed
             __syncthreads();                                  // everyone's has, and the other buffer is free
@@ -866,8 +940,8 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
             float mx = s[0][0];
 #pragma unroll
             for (int j = 1; j < 32; ++j) mx = fmaxf(mx, s[j / 16][j % 16]);
-            mx = fmaxf(mx, other_half(mx));
-            if (__ballot((mx - m) * a.scale_log2 > 8.f)) {
+            mx = max_halves(mx);
+            if (__ballot((mx - m) * a.scale_log2 > kLag)) {
                 const float m_new = fmaxf(m, mx);
                 const float alpha = __builtin_amdgcn_exp2f((m - (m_new == -kInf ? 0.f : m_new)) * a.scale_log2);
                 m = m_new;
@@ -902,14 +976,16 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
                         const int there = b == 0 ? have.x : b == 1 ? have.y : b == 2 ? have.z : have.w;
                         special |= clear_masked<E>(v, there ? q.ke - (pos + b * 16 + half * 8) : 0);
                         o[t] = E::mfma(v, pf[b], o[t]);
+                        __builtin_amdgcn_sched_barrier(0);  // one after the other, in few registers
                     }
                 if (special_from < 0 && __ballot(special != 0)) special_from = pos;
             }
         }
-        l += other_half(l);
+        l = add_halves(l);
         if (bad_page && lane == 0) raise_status(a.status, kStatusBadPage);
         if (special_from >= 0) {
             pages.fetch(special_from >> a.page_shift, lane);
+            pages.settle();
             for (pos = special_from; pos < min(pos_end, wave_end); pos += 32) {
                 size_t at[2];
                 const bool have[2] = {locate(pos, 0, at[0]), locate(pos, 1, at[1])};
@@ -924,38 +1000,18 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
                                    *(const s16x8*)(a.v + at[1] + t * 512 + v_from), sees[0], sees[1]);
             }
         }
-        const float ms = m == -kInf ? -kInf : m * a.scale_log2;
+        m = m == -kInf ? -kInf : m * a.scale_log2;
 
-        // The wave's columns, 32 dims at a time through LDS, eight dims of a column to a lane.
-        const bool whole = unit0 == 0 && unit1 == units;
-        SharedParts parts{};
-        if (kSet == 0 && whole && q.shared.n > 0) parts = shared_parts(a, split1, q.shared, f0, h);
-        __syncthreads();
-        float* s_o = (float*)s_mem + wave * (32 * kPitch);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                *(float4*)&s_o[col * kPitch + 8 * j + 4 * half] =
-                    make_float4(o[t][4 * j], o[t][4 * j + 1], o[t][4 * j + 2], o[t][4 * j + 3]);
-            __builtin_amdgcn_wave_barrier();
-#pragma unroll
-            for (int e = lane; e < 128; e += 64) {
-                const int c = e >> 2, c8 = e & 3;
-                const float jm = __shfl(ms, c, 64), jl = __shfl(l, c, 64);
-                const float4 x = *(const float4*)&s_o[c * kPitch + c8 * 8], y = *(const float4*)&s_o[c * kPitch + c8 * 8 + 4];
-                float acc[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-                if (wave * 32 + c < nf)
-                    finish<E, kSet>(a, parts, q.shared.n > 0, whole, unit0 == 0, f0, wave * 32 + c, h, t * 4 + c8, jm, jl, acc);
-            }
-            __builtin_amdgcn_wave_barrier();
-        }
-        u += unit1 - unit0;
-    }
+        const bool whole = cur.whole();
+        __syncthreads();  // LDS is free
+        finish_wave<E, kSet, NT>(a, (float*)s_mem + wave * (32 * kPitch), blockIdx.x, whole && q.kb == 0, whole, cur.unit0 == 0, f0, wave * 32, nf,
+                                 h, m, l, o);
+    } while (cur.step());
 }
 
-// Joins the parts of the segments that were split.  Where worker w goes on with a segment that
-// worker w - 1 began, workgroup (w, .) joins it, eight dims of a column to a thread.
+// Joins the parts of the segments that were split, where no prefix is shared.  Where worker w
+// goes on with a segment that worker w - 1 began, workgroup (w, .) joins it, eight dims of a
+// column to a thread.
 template <class E>
 __global__ __launch_bounds__(kT) void attend_join_kernel(AttendArgs a) {
     const AttendEnd e = a.ends[blockIdx.x];
@@ -964,12 +1020,44 @@ __global__ __launch_bounds__(kT) void attend_join_kernel(AttendArgs a) {
     if (c >= e.nf) return;
     float m = -kInf, l = 0.f, acc[8] = {};
     join_parts(a, 0, e.first, e.last, c, c8, m, l, acc);
-    if (e.shared_n > 0) {
-        const Split split1(a.cum[a.n_groups] * a.Hkv, a.workers[1]);
-        const Shared g{e.shared_start, e.shared_n, e.shared_u0, e.shared_units, e.shared_tiles};
-        join_shared(a, shared_parts(a, split1, g, e.f0, e.h), e.f0, c, e.h, c8, m, l, acc);
-    }
     store_row<E>(a, e.f0 + c, e.h, c8, m, l, acc);
+}
+
+// Joins everything where prefixes are shared: a workgroup the columns of a request with one
+// key head (up to kJoinItems of eight dims), from its own launch and its group's.
+constexpr int kJoinItems = 4 * kT;
+template <class E>
+__global__ __launch_bounds__(kT) void attend_join_shared_kernel(AttendArgs a) {
+    const int r = blockIdx.x, h = blockIdx.y, chunks = a.D / 8;
+    Request q;
+    uint32_t bad = 0;
+    if (request_of(a, r, q, bad) != 1) return;
+    const Split own(a, 0, a.cum[0][a.R] * a.Hkv), common(a, 1, a.cum[1][a.n_groups] * a.Hkv);
+    const uint32_t u0 = a.cum[0][r] * a.Hkv, units = units_in(a, 0, q.ln + q.n - q.kb);
+    const int tiles = tiles_in(a, 0, q.n), f0 = q.start * a.G;
+    if (q.kb == 0 && own.worker_of(u0) == own.worker_of(u0 + a.Hkv * tiles * units - 1)) return;  // all done already
+    Group g{};
+    uint32_t g_u0 = 0;
+    if (q.kb > 0) {
+        g = shared_of(a, q.group, bad);
+        g_u0 = a.cum[1][q.group] * a.Hkv;
+        // (rows outside the group's, as offsets that fall would have it, have no part there)
+        if (q.start < g.start || q.start + q.n > g.start + g.n) g.ke = 0;
+    }
+    const int end = min((blockIdx.z + 1) * kJoinItems, (uint32_t)(q.n * a.G * chunks));
+    for (int e = blockIdx.z * kJoinItems + threadIdx.x; e < end; e += kT) {
+        const int c = e / chunks, c8 = e % chunks;
+        float m = -kInf, l = 0.f, acc[8] = {};
+        if (q.kb == 0) {  // its whole tiles are done already
+            const uint32_t u = u0 + (h * tiles + (c >> a.tile_shift[0])) * units;
+            if (own.worker_of(u) == own.worker_of(u + units - 1)) continue;
+        }
+        join_item(a, 0, own, u0, tiles, units, f0 + c, c, h, c8, m, l, acc);
+        if (g.ke > 0)
+            join_item(a, 1, common, g_u0, tiles_in(a, 1, g.n), units_in(a, 1, g.ke), f0 + c, f0 + c - g.start * a.G, h, c8, m,
+                      l, acc);
+        store_row<E>(a, f0 + c, h, c8, m, l, acc);
+    }
 }
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
@@ -992,7 +1080,12 @@ hipError_t run(const AttendArgs& a, hipStream_t s) {
     hipError_t e = a.n_groups ? run_set<E, D, 1>(a, s) : hipSuccess;
     if (e == hipSuccess) e = run_set<E, D, 0>(a, s);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(attend_join_kernel<E>, dim3(a.workers[0], a.tile[0] / (kT / (D / 8))), dim3(kT), 0, s, a);
+    if (a.n_groups)
+        hipLaunchKernelGGL(attend_join_shared_kernel<E>,
+                           dim3(a.R, a.Hkv, ((size_t)a.max_new * a.G * (D / 8) + kJoinItems - 1) / kJoinItems), dim3(kT), 0,
+                           s, a);
+    else
+        hipLaunchKernelGGL(attend_join_kernel<E>, dim3(a.workers[0], a.tile[0] / (kT / (D / 8))), dim3(kT), 0, s, a);
     return hipGetLastError();
 }
 
@@ -1001,7 +1094,13 @@ hipError_t run_dim(const AttendArgs& a, hipStream_t s) {
     return a.D == 64 ? run<E, 64>(a, s) : a.D == 128 ? run<E, 128>(a, s) : run<E, 256>(a, s);
 }
 
-size_t slots_bytes(int D) { return round256((size_t)kAttendMaxWorkers * 2 * kAttendMaxTile * (D + 2) * sizeof(float)); }
+// Two parts a worker, of as many columns a compute unit as the forms have.
+size_t slots_bytes(int D) {
+    const int columns = std::max(D <= 128 ? 128 : 64, D == 64 ? Wide<64>::kPerCu * Wide<64>::kTile
+                                                       : D == 128 ? Wide<128>::kTile : Wide<256>::kTile);
+    return round256((size_t)kAttendMaxCus * columns * 2 * (D + 2) * sizeof(float));
+}
+constexpr int kMaxWorkers = kAttendMaxCus * 3;  // of any form
 size_t dense_bytes(int R, int H, int D, int max_new) {
     return round256((size_t)R * max_new * H * (D + 2) * sizeof(float));
 }
@@ -1009,35 +1108,42 @@ size_t dense_bytes(int R, int H, int D, int max_new) {
 }  // namespace
 
 size_t attend_ws_bytes(int R, int H, int D, int max_new, int n_groups) {
-    size_t n = slots_bytes(D) + round256(kAttendMaxWorkers * sizeof(AttendEnd));
-    if (n_groups) n += slots_bytes(D) + round256((size_t)(n_groups + 1) * 4) + dense_bytes(R, H, D, max_new);
+    size_t n = slots_bytes(D) + round256(kMaxWorkers * sizeof(AttendEnd));
+    if (n_groups)
+        n += slots_bytes(D) + round256((size_t)(R + 1) * 4) + round256((size_t)(n_groups + 1) * 4) +
+             2 * dense_bytes(R, H, D, max_new);
     return n;
 }
 
 void attend_ws_layout(AttendArgs& a, void* ws) {
     char* p = (char*)ws;
-    a.slots[0] = (float*)p;
-    p += slots_bytes(a.D);
-    a.ends = (AttendEnd*)p;
-    p += round256(kAttendMaxWorkers * sizeof(AttendEnd));
+    const auto take = [&](size_t bytes) {
+        char* at = p;
+        p += bytes;
+        return at;
+    };
+    a.slots[0] = (float*)take(slots_bytes(a.D));
+    a.ends = (AttendEnd*)take(round256(kMaxWorkers * sizeof(AttendEnd)));
     if (!a.n_groups) return;
-    a.slots[1] = (float*)p;
-    p += slots_bytes(a.D);
-    a.cum = (uint32_t*)p;
-    p += round256((size_t)(a.n_groups + 1) * 4);
-    a.dense = (float*)p;
+    a.slots[1] = (float*)take(slots_bytes(a.D));
+    a.cum[0] = (uint32_t*)take(round256((size_t)(a.R + 1) * 4));
+    a.cum[1] = (uint32_t*)take(round256((size_t)(a.n_groups + 1) * 4));
+    a.dense[0] = (float*)take(dense_bytes(a.R, a.H, a.D, a.max_new));
+    a.dense[1] = (float*)take(dense_bytes(a.R, a.H, a.D, a.max_new));
 }
 
 hipError_t launch_attend(AttendArgs a, int cus, hipStream_t s) {
-    // The many-rows form where a request (a group) may have more columns than the other form
-    // takes at once; else 64 columns to a workgroup where it may have more than 32.
+    // The many-rows form where a request (a group) may have more columns than kWideFrom; else
+    // workers of two waves where it may have more than the 32 of one.
     const int wide = a.D == 64 ? Wide<64>::kTile : a.D == 128 ? Wide<128>::kTile : Wide<256>::kTile;
+    const int wide_per_cu = a.D == 64 ? Wide<64>::kPerCu : 1;
+    cus = std::min(cus, kAttendMaxCus);
     for (int set = 0; set < 2; ++set) {
         const long long columns = (long long)(set ? a.rows : a.max_new) * a.G;
         a.tile[set] = columns > kWideFrom ? wide : columns > 32 ? 64 : 32;
-        a.unit[set] = a.tile[set] == 32 ? 128 : 64;
-        const int per_cu = a.tile[set] == wide ? (a.D == 64 ? Wide<64>::kPerCu : 1) : a.D <= 128 ? 2 : 1;
-        a.workers[set] = std::min(cus * per_cu, kAttendMaxWorkers);
+        a.unit[set] = columns > 32 ? 64 : 128;
+        a.workers[set] = cus * (columns > kWideFrom ? wide_per_cu : a.D <= 128 ? 2 : 1);
+        a.least[set] = columns > kWideFrom ? kWideLeast : kFewLeast;
         a.tile_shift[set] = __builtin_ctz(a.tile[set]);
         a.unit_shift[set] = __builtin_ctz(a.unit[set]);
     }

@@ -60,17 +60,15 @@ hipError_t launch_append(const AppendArgs& a, hipStream_t s);
 // workers where it has to be.  A worker leaves a split segment's part in one of its two
 // slots: slot 0 for the segment that an earlier worker began, slot 1 for the one that it
 // begins and does not end.
-constexpr int kAttendMinTile = 32;      // columns (row, head of the group) of one tile, at least
-constexpr int kAttendMaxTile = 256;     // and at most
-constexpr int kAttendMinUnit = 64;      // keys of one unit, at least
-constexpr int kAttendMaxWorkers = 768;  // workgroups of one launch
+constexpr int kAttendMinTile = 32;  // columns (row, head of the group) of one tile, at least
+constexpr int kAttendMinUnit = 64;  // keys of one unit, at least
+constexpr int kAttendMaxCus = 256;  // compute units that a launch uses
 
 // A worker's first segment, where an earlier worker began it (units = 0: it did not): the
-// workers that have parts of it, its columns, and its group's units.
+// workers that have parts of it, and its columns.
 struct AttendEnd {
     uint32_t units;
-    int first, last, f0, nf, h, shared_start, shared_n;
-    uint32_t shared_u0, shared_units, shared_tiles;
+    int first, last, f0, nf, h;
 };
 
 struct AttendArgs {
@@ -90,11 +88,11 @@ struct AttendArgs {
     uint16_t* out;
     float* lse;
     uint32_t* status;
-    int tile[2], unit[2], tile_shift[2], unit_shift[2], workers[2];  // the launches' forms: [0] the requests' own keys, [1] the shared ones
+    int tile[2], unit[2], tile_shift[2], unit_shift[2], workers[2], least[2];  // the launches' forms: [0] the requests' own keys, [1] the shared ones
     float* slots[2];   // parts of split segments: of the requests' own keys, of the shared ones
-    float* dense;      // shared keys: whole segments' parts, [Hkv][rows G][D], then maxima and sums
+    float* dense[2];   // with shared prefixes: the parts of whole segments, [Hkv][rows G][D], then maxima and sums
     AttendEnd* ends;   // [workers[0]]
-    uint32_t* cum;     // running units (of one key head) of the groups
+    uint32_t* cum[2];  // with shared prefixes: running units (of one key head) of the requests, of the groups
 };
 size_t attend_ws_bytes(int R, int H, int D, int max_new, int n_groups);
 void attend_ws_layout(AttendArgs& a, void* ws);
