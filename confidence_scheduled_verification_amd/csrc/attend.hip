@@ -25,6 +25,7 @@
 // value of V that is not a number in such a block is taken out of the product and handed
 // to the columns that see it by counting (see add_special).
 #include <algorithm>
+#include <type_traits>
 
 #include "cache.h"
 #include "common.h"
@@ -43,7 +44,7 @@ constexpr int kT = 256;
 #define WF 128
 #endif
 #ifndef WL
-#define WL 8
+#define WL 4
 #endif
 constexpr int kWideFrom = WF;  // columns of a request or group beyond which the many-rows form runs
 #ifndef FL
@@ -522,6 +523,13 @@ struct PageIds {
     }
 };
 
+// A barrier for what the waves leave each other in LDS; loads from memory stay under way.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // A worker's way through its units: the segment at hand, and the item it belongs to.
 template <int kSet, int kTile, int kUnit>
 struct Cursor {
@@ -670,7 +678,7 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
     int f0 = 0, nf = 0, h = 0;
     // The waves' parts joined, column by column, eight dims to a thread, kDims dims at a time.
     const auto put = [&](int d0) {
-        __syncthreads();
+        lds_barrier();
         if (half == 0) {
             s_m[wave][col] = ms;
             s_l[wave][col] = l;
@@ -683,7 +691,7 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
                 *(float4*)&s_o[wave][col][t * 32 + 8 * j + 4 * half] =
                     make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
             }
-        __syncthreads();
+        lds_barrier();
     };
     const auto take = [&](int d0) {
         for (int e = tid; e < nf * (kDims / 8); e += kT) {
@@ -725,23 +733,22 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
         float m = -kInf;  // of the raw scores; l is this half's share of the sum
         l = 0.f;
         int special_from = -1;     // the first block with values that add_special has to add
-        // K is waited for here, where other loads and stores may be under way as well; inside the
-        // loop its waits then count on the order of the loop's own loads.
-#pragma unroll
-        for (int c = 0; c < NC; ++c) asm volatile("" : "+v"(kf[c]));
-#pragma unroll
-        for (int t = 0; t < NT; ++t) asm volatile("" : "+v"(vf[t][0]), "+v"(vf[t][1]));
-        if (pos < pos_end) do {
+        // One block of 32 keys: scores, weights, and the second product.  kFast: all of its keys
+        // are seen by all columns, and another block follows, whose K and V are requested with no
+        // condition (a load that may be left out would have every later wait count on its absence).
+        const auto block = [&](auto fast) {
+            constexpr bool kFast = decltype(fast)::value;
             f32x16 s = {};
 #pragma unroll
             for (int c = 0; c < NC; ++c) s = E::mfma(kf[c], qf[c], s);
-            // (after the last keys these once more, unused: a load that may be left out would have
-            // every later wait count on its absence)
             const int next = pos + kUnit;
-            bool next_have[2];
-            locate(next < pos_end ? next : pos, next_have);
-            load_k();
-            const bool masked = pos + 31 > first_last || !have[0] || !have[1];
+            const bool follows = kFast || next < pos_end;
+            bool next_have[2] = {false, false};
+            if (follows) {
+                locate(next, next_have);
+                load_k();
+            }
+            const bool masked = !kFast && (pos + 31 > first_last || !have[0] || !have[1]);
             if (masked) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
@@ -767,7 +774,7 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
             for (int j = 0; j < 16; ++j) {
                 const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], a.scale_log2, -mc));
                 l += p;
-                pf[j / 8][j % 8] = (short)E::bits(p);  // weights of at most 1, rounded for the matrix instruction
+                pf[j / 8][j % 8] = (short)E::bits(p);  // the weights, rounded for the matrix instruction
             }
             if (masked) {
                 uint32_t special = 0;
@@ -782,11 +789,22 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) o[t] = E::mfma(vf[t][1], pf[1], E::mfma(vf[t][0], pf[0], o[t]));
-            load_v();
+            if (follows) load_v();
             pos = next;
             have[0] = next_have[0];
             have[1] = next_have[1];
-        } while (pos < pos_end);
+        };
+        if (pos + kUnit < pos_end && pos + 31 <= first_last && have[0] && have[1]) {
+            // What is on its way is waited for here, where other loads and stores may be too; inside
+            // the loop the waits then count on the order of the loop's own loads.
+#pragma unroll
+            for (int c = 0; c < NC; ++c) asm volatile("" : "+v"(kf[c]));
+#pragma unroll
+            for (int t = 0; t < NT; ++t) asm volatile("" : "+v"(vf[t][0]), "+v"(vf[t][1]));
+            do block(std::true_type{});
+            while (pos + kUnit < pos_end && pos + 31 <= first_last && have[0] && have[1]);
+        }
+        while (pos < pos_end) block(std::false_type{});
         l = add_halves(l);
         if (special_from >= 0) {
             pages.fetch(special_from >> a.page_shift, lane);
