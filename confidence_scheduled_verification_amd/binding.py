@@ -323,9 +323,15 @@ def _step_checks(base, markov: MarkovHead, prev0, conf, verify_cost, draft_cost,
     return R, K, V
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def dspark_step(base, markov: MarkovHead, prev0, conf, n_sampling: int, T: int, num_reqs: int, verify_cost,
@@ -505,18 +511,22 @@ class PagedCache:
         self._ref = ctypes.byref(self.handle)
 
 
-def _on(cache: PagedCache, what: str, ints=(), others=()):
-    """The cache's device is the current one, and every tensor of the call lies there; `ints` are
-    int32 and densely packed."""
+def _on(cache: PagedCache, what: str, stream, ints=(), others=()) -> int:
+    """The stream of a call on `cache`: its device is the current one, and every tensor of the
+    call lies there; `ints` are int32 and densely packed."""
     torch = _torch()
+    device = cache.device
     for t in ints:
-        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
+        if t is not None and (t.dtype is not torch.int32 or not t.is_contiguous() or t.device != device):
+            if t.device != device:
+                raise ValueError(f"{what}: a tensor on {t.device}, the cache is on {device}")
             raise ValueError(f"{what}: index tensors must be contiguous int32")
-    for t in (*ints, *others):
-        if t is not None and t.device != cache.device:
-            raise ValueError(f"{what}: a tensor on {t.device}, the cache is on {cache.device}")
-    if cache.device.type != "cuda" or cache.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what}: the cache is on {cache.device}, which is not the current GPU")
+    for t in others:
+        if t is not None and t.device != device:
+            raise ValueError(f"{what}: a tensor on {t.device}, the cache is on {device}")
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: the cache is on {device}, which is not the current GPU")
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
 
 
 def pages_workspace(cache: PagedCache, n: int):
@@ -541,9 +551,9 @@ def dspark_pages_reserve(cache: PagedCache, offsets, lead: int, granted, ws, sta
     """Pages for a step's rows, the lowest free ones in the order of the requests."""
     R = _offsets_rows(cache, offsets, "dspark_pages_reserve")
     _shape(granted, (R,), "dspark_pages_reserve: granted")
-    _on(cache, "dspark_pages_reserve", (offsets, granted), (ws, status))
+    st = _on(cache, "dspark_pages_reserve", stream, (offsets, granted), (ws, status))
     _check(lib().dspark_pages_reserve(cache._ref, _p(offsets), lead, R, _p(granted), _p(status), _p(ws), _ws_bytes(ws),
-                                      _stream(stream)))
+                                      st))
 
 
 def dspark_pages_trim(cache: PagedCache, rows=None, keep=None, status=None, stream=None):
@@ -552,34 +562,34 @@ def dspark_pages_trim(cache: PagedCache, rows=None, keep=None, status=None, stre
     n = cache.rows if rows is None else rows.numel()
     if keep is not None:
         _shape(keep, (n,), "dspark_pages_trim: keep")
-    _on(cache, "dspark_pages_trim", (rows, keep), (status,))
-    _check(lib().dspark_pages_trim(cache._ref, _p(rows), n, _p(keep), _p(status), _stream(stream)))
+    st = _on(cache, "dspark_pages_trim", stream, (rows, keep), (status,))
+    _check(lib().dspark_pages_trim(cache._ref, _p(rows), n, _p(keep), _p(status), st))
 
 
 def dspark_pages_commit(cache: PagedCache, accept_len, lead: int, status=None, stream=None):
     """After dspark_accept_greedy: the accepted rows stay, the pages past them are let go."""
     if accept_len.dim() != 1 or accept_len.shape[0] > cache.rows:
         raise ValueError(f"dspark_pages_commit: accept_len must be [R] with R at most {cache.rows}")
-    _on(cache, "dspark_pages_commit", (accept_len,), (status,))
-    _check(lib().dspark_pages_commit(cache._ref, _p(accept_len), lead, accept_len.shape[0], _p(status), _stream(stream)))
+    st = _on(cache, "dspark_pages_commit", stream, (accept_len,), (status,))
+    _check(lib().dspark_pages_commit(cache._ref, _p(accept_len), lead, accept_len.shape[0], _p(status), st))
 
 
 def dspark_pages_fork(cache: PagedCache, src, dst, forked, ws, deep: bool = False, status=None, stream=None):
     """Rows dst continue rows src: whole pages shared and the last one copied (deep: all copied)."""
     _shape(dst, (src.numel(),), "dspark_pages_fork: dst")
     _shape(forked, (src.numel(),), "dspark_pages_fork: forked")
-    _on(cache, "dspark_pages_fork", (src, dst, forked), (ws, status))
+    st = _on(cache, "dspark_pages_fork", stream, (src, dst, forked), (ws, status))
     _check(lib().dspark_pages_fork(cache._ref, _p(src), _p(dst), src.numel(), int(deep), _p(forked), _p(status), _p(ws),
-                                   _ws_bytes(ws), _stream(stream)))
+                                   _ws_bytes(ws), st))
 
 
 def dspark_pages_compact(cache: PagedCache, page_map, n_live, ws, status=None, stream=None):
     """Live pages to the front; page_map [n_pages] receives each page's new place (-1: free)."""
     _shape(page_map, (cache.n_pages,), "dspark_pages_compact: page_map")
     _shape(n_live, (1,), "dspark_pages_compact: n_live")
-    _on(cache, "dspark_pages_compact", (page_map, n_live), (ws, status))
+    st = _on(cache, "dspark_pages_compact", stream, (page_map, n_live), (ws, status))
     _check(lib().dspark_pages_compact(cache._ref, _p(page_map), _p(n_live), _p(status), _p(ws), _ws_bytes(ws),
-                                      _stream(stream)))
+                                      st))
 
 
 def _packed(cache: PagedCache, t, heads, what: str):
@@ -587,9 +597,10 @@ def _packed(cache: PagedCache, t, heads, what: str):
     if t.dim() != 3 or t.shape[1:] != (heads, cache.head_dim) or t.dtype != cache.torch_dtype:
         raise ValueError(f"{what} must be {cache.torch_dtype} [rows, {heads}, {cache.head_dim}], "
                          f"got {t.dtype} {list(t.shape)}")
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != cache.head_dim)):
+    rows, across, along = t.stride()
+    if t.numel() and (along != 1 or (heads > 1 and across != cache.head_dim)):
         raise ValueError(f"{what}: each row's heads must be densely packed")
-    return t.stride(0) if t.shape[0] > 1 else heads * cache.head_dim
+    return rows if t.shape[0] > 1 else heads * cache.head_dim
 
 
 def dspark_cache_append(cache: PagedCache, layer: int, k_new, v_new, offsets, lead: int, max_new: int, status=None,
@@ -600,9 +611,9 @@ def dspark_cache_append(cache: PagedCache, layer: int, k_new, v_new, offsets, le
     vs = _packed(cache, v_new, cache.n_kv_heads, "dspark_cache_append: v_new")
     if v_new.shape[0] != k_new.shape[0]:
         raise ValueError("dspark_cache_append: k_new and v_new must have as many rows")
-    _on(cache, "dspark_cache_append", (offsets,), (k_new, v_new, status))
+    st = _on(cache, "dspark_cache_append", stream, (offsets,), (k_new, v_new, status))
     _check(lib().dspark_cache_append(cache._ref, layer, _p(k_new), ks, _p(v_new), vs, k_new.shape[0], _p(offsets), lead,
-                                     R, max_new, _p(status), _stream(stream)))
+                                     R, max_new, _p(status), st))
 
 
 def dspark_cache_attend(cache: PagedCache, layer: int, q, offsets, lead: int, max_new: int, scale: float, out, lse=None,
@@ -628,10 +639,10 @@ def dspark_cache_attend(cache: PagedCache, layer: int, q, offsets, lead: int, ma
         n_groups, width = table.shape
         _shape(off, (n_groups + 1,), f"{what}: group_off")
         _shape(pages, (n_groups,), f"{what}: shared_pages")
-    _on(cache, what, (offsets, off, table, pages), (q, out, lse, ws, status))
+    st = _on(cache, what, stream, (offsets, off, table, pages), (q, out, lse, ws, status))
     _check(lib().dspark_cache_attend(cache._ref, layer, _p(q), qs, q.shape[0], H, _p(offsets), lead, R, max_new,
                                      float(scale), n_groups, _p(off), _p(table), width, _p(pages), _p(out), os_, _p(lse),
-                                     _p(status), _p(ws), _ws_bytes(ws), _stream(stream)))
+                                     _p(status), _p(ws), _ws_bytes(ws), st))
 
 
 def dspark_set_launch_mode(mode: int):

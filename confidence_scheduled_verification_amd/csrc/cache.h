@@ -50,7 +50,7 @@ struct AppendArgs {
     const int32_t* table;
     const int32_t* len;
     const int32_t* offsets;
-    int lead, R, rows, max_new, Hkv, D, page, n_pages, width;
+    int lead, R, rows, max_new, Hkv, D, page, page_shift, n_pages, width;
     uint32_t* status;
 };
 hipError_t launch_append(const AppendArgs& a, hipStream_t s);

@@ -3,9 +3,9 @@
 // lowest free pages go first, in the order of the requests, so that every result is a
 // function of the tables and counts alone.
 //
-// Ranking the free pages: the counts are cut into slices of 4096.  A first launch counts
-// each slice; in the second each workgroup adds up the slices before its own, ranks its
-// free pages by a scan, and gives the page of rank k to the request that holds place k of
+// Ranking the free pages: the counts are cut into slices of 4096, sixteen pages to a thread.
+// A first launch counts each slice; in the second each workgroup adds up the slices before
+// its own, ranks its free pages by one scan, and gives the page of rank k to the request that holds place k of
 // the running needs, found by bisection in LDS.  Two launches, whatever the sizes; nothing
 // is kept between calls.
 #include "cache.h"
@@ -43,13 +43,44 @@ __device__ int block_sum(int x, int* tmp) {
     return tmp[0] + tmp[1] + tmp[2] + tmp[3];
 }
 
-// Pages of slice b whose count is (live ? above : equal to) zero.
-__device__ void count_slice(const int32_t* ref, int n_pages, int b, bool live, int32_t* out, int* tmp) {
-    int n = 0;
-    const int end = min(n_pages, (b + 1) * kPageSlice);
-    for (int p = b * kPageSlice + threadIdx.x; p < end; p += kT) n += (ref[p] > 0) == live;
-    n = block_sum(n, tmp);
+// A thread's sixteen pages of slice b, one after the other: bit i says whether page first + i
+// has a count above zero (live) or not (free).
+constexpr int kOwn = kPageSlice / kT;
+static_assert(kOwn == 16, "four 16-byte loads to a thread");
+
+__device__ uint32_t own_pages(const dspark_cache_t& c, int b, bool live, int& first) {
+    first = b * kPageSlice + (int)threadIdx.x * kOwn;
+    uint32_t bits = 0;
+    if (first + kOwn <= c.n_pages && ((uintptr_t)c.ref & 15u) == 0) {
+        int4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = ((const int4*)(c.ref + first))[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            bits |= (uint32_t)(x[i].x > 0) << (4 * i) | (uint32_t)(x[i].y > 0) << (4 * i + 1) |
+                    (uint32_t)(x[i].z > 0) << (4 * i + 2) | (uint32_t)(x[i].w > 0) << (4 * i + 3);
+        return live ? bits : ~bits & 0xFFFFu;
+    }
+    for (int i = 0; i < kOwn && first + i < c.n_pages; ++i) bits |= (uint32_t)((c.ref[first + i] > 0) == live) << i;
+    return bits;
+}
+
+__device__ void count_slice(const dspark_cache_t& c, int b, bool live, int32_t* out, int* tmp) {
+    int first;
+    const int n = block_sum(__popc(own_pages(c, b, live, first)), tmp);
     if (threadIdx.x == 0) out[b] = n;
+}
+
+// The free pages of slice b in order, in LDS; returns how many.
+__device__ int list_free(const dspark_cache_t& c, int b, int* list, int* tmp) {
+    int first;
+    uint32_t mine = own_pages(c, b, false, first);
+    const int upto = block_scan(__popc(mine), tmp);
+    for (int k = upto - __popc(mine); mine; mine &= mine - 1) list[k++] = first + __ffs(mine) - 1;
+    __syncthreads();
+    if (threadIdx.x == kT - 1) tmp[4] = upto;
+    __syncthreads();
+    return tmp[4];
 }
 
 // Counts of the slices before b, and of all.
@@ -66,18 +97,18 @@ __device__ void slices_before(const int32_t* cnt, int n, int b, int& before, int
 
 // Running sums of need[0..n) in LDS: cum[i] = need[0] + ... + need[i-1], cum[n] the total.
 __device__ void running_needs(const int32_t* need, int n, int* cum, int* tmp) {
-    int base = 0;
-    for (int i0 = 0; i0 < n; i0 += kT) {
-        const int i = i0 + threadIdx.x;
-        const int x = i < n ? need[i] : 0;
-        const int y = block_scan(x, tmp);
-        if (i < n) cum[i] = base + y - x;
-        __syncthreads();
-        if (threadIdx.x == kT - 1) tmp[4] = base + y;
-        __syncthreads();
-        base = tmp[4];
+    for (int i = threadIdx.x; i < n; i += kT) cum[i] = need[i];
+    __syncthreads();
+    const int per = (n + kT - 1) / kT, i0 = min(n, (int)threadIdx.x * per), i1 = min(n, i0 + per);
+    int x = 0;
+    for (int i = i0; i < i1; ++i) x += cum[i];
+    int base = block_scan(x, tmp) - x;
+    for (int i = i0; i < i1; ++i) {
+        const int y = cum[i];
+        cum[i] = base;
+        base += y;
     }
-    if (threadIdx.x == 0) cum[n] = base;
+    if (threadIdx.x == kT - 1) cum[n] = base;
     __syncthreads();
 }
 
@@ -125,7 +156,7 @@ __global__ __launch_bounds__(kT) void reserve_needs_kernel(dspark_cache_t c, con
                                                            uint32_t* status) {
     __shared__ int tmp[8];
     if ((int)blockIdx.x < ns) {
-        count_slice(c.ref, c.n_pages, blockIdx.x, false, cnt, tmp);
+        count_slice(c, blockIdx.x, false, cnt, tmp);
         return;
     }
     const int r = (blockIdx.x - ns) * 4 + (threadIdx.x >> 6);
@@ -159,7 +190,7 @@ __global__ __launch_bounds__(kT) void reserve_assign_kernel(dspark_cache_t c, in
                                                             const int32_t* need, const int32_t* have,
                                                             int32_t* granted, uint32_t* status) {
     extern __shared__ int cum[];  // R + 1
-    __shared__ int tmp[8];
+    __shared__ int list[kPageSlice], tmp[8];
     const int b = blockIdx.x;
     int before, all;
     slices_before(cnt, ns, b, before, all, tmp);
@@ -175,22 +206,11 @@ __global__ __launch_bounds__(kT) void reserve_assign_kernel(dspark_cache_t c, in
         if (short_of) raise_status(status, kStatusNoPages);
     }
     if (before >= give) return;
-    const int end = min(c.n_pages, (b + 1) * kPageSlice);
-    int base = before;
-    for (int p0 = b * kPageSlice; p0 < end && base < give; p0 += kT) {
-        const int p = p0 + threadIdx.x;
-        const int free1 = p < end && !(c.ref[p] > 0);
-        const int incl = block_scan(free1, tmp);
-        const int k = base + incl - 1;
-        if (free1 && k < give) {
-            const int r = owner_of(cum, R, k);
-            c.table[(size_t)r * c.width + have[r] + (k - cum[r])] = p;
-            c.ref[p] = 1;
-        }
-        __syncthreads();
-        if (threadIdx.x == kT - 1) tmp[4] = base + incl;
-        __syncthreads();
-        base = tmp[4];
+    const int count = list_free(c, b, list, tmp);
+    for (int i = threadIdx.x; i < count && before + i < give; i += kT) {
+        const int p = list[i], k = before + i, r = owner_of(cum, R, k);
+        c.table[(size_t)r * c.width + have[r] + (k - cum[r])] = p;
+        c.ref[p] = 1;
     }
 }
 
@@ -255,7 +275,7 @@ __global__ __launch_bounds__(kT) void fork_needs_kernel(dspark_cache_t c, const 
     __shared__ int tmp[8];
     __shared__ int tile[kT];
     if ((int)blockIdx.x < ns) {
-        count_slice(c.ref, c.n_pages, blockIdx.x, false, cnt, tmp);
+        count_slice(c, blockIdx.x, false, cnt, tmp);
         return;
     }
     const int i0 = (blockIdx.x - ns) * kT;
@@ -293,7 +313,7 @@ __global__ __launch_bounds__(kT) void fork_assign_kernel(dspark_cache_t c, const
                                                          int32_t* from, int32_t* to, int32_t* n_copies,
                                                          uint32_t* status) {
     extern __shared__ int cum[];  // n + 1
-    __shared__ int tmp[8];
+    __shared__ int list[kPageSlice], tmp[8];
     const int b = blockIdx.x;
     int before, all;
     slices_before(cnt, ns, b < ns ? b : 0, before, all, tmp);
@@ -324,31 +344,20 @@ __global__ __launch_bounds__(kT) void fork_assign_kernel(dspark_cache_t c, const
     const int give = served(cum, n, all);
     if (b == 0 && threadIdx.x == 0) *n_copies = give;
     if (before >= give) return;
-    const int end = min(c.n_pages, (b + 1) * kPageSlice);
-    int base = before;
-    for (int p0 = b * kPageSlice; p0 < end && base < give; p0 += kT) {
-        const int p = p0 + threadIdx.x;
-        const int free1 = p < end && !(c.ref[p] > 0);
-        const int incl = block_scan(free1, tmp);
-        const int k = base + incl - 1;
-        if (free1 && k < give) {
-            const int f = owner_of(cum, n, k);
-            const int at = (deep ? 0 : lens[f] / c.page_size) + (k - cum[f]);
-            from[k] = c.table[(size_t)src[f] * c.width + at];
-            to[k] = p;
-            c.table[(size_t)dst[f] * c.width + at] = p;
-            c.ref[p] = 1;
-        }
-        __syncthreads();
-        if (threadIdx.x == kT - 1) tmp[4] = base + incl;
-        __syncthreads();
-        base = tmp[4];
+    const int count = list_free(c, b, list, tmp);
+    for (int i = threadIdx.x; i < count && before + i < give; i += kT) {
+        const int p = list[i], k = before + i, f = owner_of(cum, n, k);
+        const int at = (deep ? 0 : lens[f] / c.page_size) + (k - cum[f]);
+        from[k] = c.table[(size_t)src[f] * c.width + at];
+        to[k] = p;
+        c.table[(size_t)dst[f] * c.width + at] = p;
+        c.ref[p] = 1;
     }
 }
 
 __global__ __launch_bounds__(kT) void compact_count_kernel(dspark_cache_t c, int32_t* cnt) {
     __shared__ int tmp[8];
-    count_slice(c.ref, c.n_pages, blockIdx.x, true, cnt, tmp);
+    count_slice(c, blockIdx.x, true, cnt, tmp);
 }
 
 // Ranks: with n_live live pages, `low` of them below n_live, the live page p at or above
@@ -365,36 +374,30 @@ __global__ __launch_bounds__(kT) void compact_rank_kernel(dspark_cache_t c, int 
     const int edge = all / kPageSlice;  // the slice that n_live lies in
     int low, unused;
     slices_before(cnt, ns, edge, low, unused, tmp);
-    int x = 0;
-    for (int p = edge * kPageSlice + threadIdx.x; p < all; p += kT) x += c.ref[p] > 0;
-    low += block_sum(x, tmp);
+    int first;
+    uint32_t at_edge = edge < ns ? own_pages(c, edge, true, first) : 0;
+    if (edge < ns) at_edge &= all <= first ? 0u : all - first >= kOwn ? 0xFFFFu : (1u << (all - first)) - 1u;
+    low += block_sum(__popc(at_edge), tmp);
     if (b == 0 && threadIdx.x == 0) {
         *n_live = all;
         *n_moves = all - low;
     }
-    const int end = min(c.n_pages, (b + 1) * kPageSlice);
-    int base = before;
-    for (int p0 = b * kPageSlice; p0 < end; p0 += kT) {
-        const int p = p0 + threadIdx.x;
-        const int live = p < end && c.ref[p] > 0;
-        const int incl = block_scan(live, tmp);
-        const int rank = base + incl - live;  // live pages before p
-        if (p < end) {
-            int m = -1;
-            if (live && p < all) {
-                m = p;
-            } else if (live) {
-                from[rank - low] = p;
-                m = -2 - (rank - low);
-            } else if (p < all) {
-                to[p - rank] = p;
-            }
-            page_map[p] = m;
+    const uint32_t mine = own_pages(c, b, true, first);
+    int rank = before + block_scan(__popc(mine), tmp) - __popc(mine);  // live pages before p
+    for (int i = 0; i < kOwn && first + i < c.n_pages; ++i) {
+        const int p = first + i;
+        const bool live = mine >> i & 1;
+        int m = -1;
+        if (live && p < all) {
+            m = p;
+        } else if (live) {
+            from[rank - low] = p;
+            m = -2 - (rank - low);
+        } else if (p < all) {
+            to[p - rank] = p;
         }
-        __syncthreads();
-        if (threadIdx.x == kT - 1) tmp[4] = base + incl;
-        __syncthreads();
-        base = tmp[4];
+        page_map[p] = m;
+        rank += live;
     }
 }
 
