@@ -12,13 +12,18 @@
 // from memory in the order in which they lie (a block's K as [D/8][16][8], its V as
 // [D][16]), so neither passes through LDS.
 //
-// Work: the keys are cut into units of 128 (four waves of 32).  Every workgroup takes the
-// same number of consecutive units, in the order request, key head, tile, unit, so few
-// long contexts and many short ones fill the device alike; a segment (request, key head,
-// tile) that ends inside one workgroup is finished there, and the parts of one that is
-// split are joined by a second kernel.  A shared prefix is a first launch of the same
-// kernel, whose segments are a group's rows taken together and whose keys are read once a
-// tile of 32 of them; the requests' own segments then add its part as they end.
+// Work: the keys are cut into units of 64 or 128.  Every workgroup, a worker, takes the same
+// number of consecutive units, in the order request, key head, tile, unit, so few long contexts
+// and many short ones fill the device alike; a segment (request, key head, tile) that ends
+// inside one worker is finished there, and the parts of one that is split are joined by a
+// kernel of their own.  Shared prefixes are a launch of their own, whose segments are a group's
+// rows taken together, so that its keys are read once for all of them; where there are such,
+// the last kernel joins each row's own part and its group's.
+//
+// Forms: with few columns the keys' bytes are the bound, and every wave streams its keys from
+// memory straight into the matrix instruction's registers (attend_kernel).  With many the
+// matrix and vector units are, and the keys come to LDS once for all waves
+// (attend_wide_kernel).  Each kernel says what it reaches.
 //
 // Masks: only blocks that reach past a column's last key are masked.  What lies in masked
 // places has no say whatever it is: scores are replaced, V past the end is cleared, and a
@@ -40,18 +45,18 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kT = 256;
-#ifndef WF
-#define WF 128
-#endif
-#ifndef WL
-#define WL 4
-#endif
-constexpr int kWideFrom = WF;  // columns of a request or group beyond which the many-rows form runs
-#ifndef FL
-#define FL 2
-#endif
-constexpr int kFewLeast = FL;    // units of the other
-constexpr int kWideLeast = WL;  // units of that form that are worth a workgroup
+// The form of a launch, by the columns that one request (a group) may have.  Up to 32 fill one
+// wave's tile, up to 64 two waves'; beyond them the many-rows form reads the keys once for 128
+// or 256 columns.  From 33 on it would be slower where few are filled (256 requests of
+// up to 64 columns, 514 tokens each: 177 us against 275), from 129 on the few-rows form would read the
+// keys of 65 to 128 columns twice (two requests of up to 131072 tokens and 72 columns: 194 against 200).
+constexpr int kWideFrom = 64;
+// The units that are worth a workgroup of their own: fewer spread a small call over more of
+// the device, more leave fewer parts to join.  Few rows: 1, 2, 8 give 12.7, 14.7, 24.7 us for
+// four requests of 700 tokens, 31.6, 25.1, 22.1 for one of 8192, 56, 56, 67 for 16 behind 2048
+// shared ones.  Many rows: 1, 4, 8 give 58, 56, 59 us for the last, and 232, 241, 270 where 1145
+// rows share 64 tokens.
+constexpr int kFewLeast = 2, kWideLeast = 4;
 constexpr float kInf = __builtin_huge_valf();
 // The running maximum follows only when it grows by more than this exponent of two; until
 // then the weights are taken relative to the older one, at most 2^8, and nothing that has
@@ -179,6 +184,13 @@ struct Split {
     __device__ __forceinline__ int worker_of(uint32_t u) const {
         const uint32_t big = more * (each + 1);
         return (int)(u < big ? u / (each + 1) : more + (u - big) / each);
+    }
+    // Which worker a workgroup is.  Those of one XCD, every eighth workgroup, take units next to
+    // each other, so that keys which many columns see come through its L2 (two groups of 4096
+    // tokens, 4096 rows: 265 to 257 us).  A segment's worker w is then not workgroup w.
+    __device__ __forceinline__ int by_xcd() const {
+        const int b = blockIdx.x, xcd = b & 7;
+        return b < workers ? xcd * (workers / 8) + min(xcd, workers % 8) + (b >> 3) : b;
     }
 };
 
@@ -587,11 +599,16 @@ __device__ __forceinline__ void load_q(const AttendArgs& a, s16x8 (&qf)[D / 16],
 
 // The few-rows form.  A workgroup takes kTiles tiles of the segment's columns: its four
 // waves are 4 / kTiles groups of keys by kTiles tiles, so that up to 64 columns read the
-// keys once.  Each wave streams: the next block's K is requested as soon as the first
-// product has used this one's, the next V after the second product, so about 16 KB a wave
-// are under way while it computes; and the next segment's rows, page ids and first keys
-// are requested before this one's waves are joined (kSet 0: the requests' own keys; 1: the
-// groups' shared ones).
+// keys once.  Each wave streams: the next block's K is requested as soon as the first product
+// has used this one's, the next V after the second product, so about 16 KB a wave are under way
+// while it computes; and the next segment's rows, page ids and first keys are requested before
+// this one's waves are joined (kSet 0: the requests' own keys; 1: the groups' shared ones).
+//
+// 256 requests of 1145 rows, 64 query and 8 key heads of 128, bf16: 177 us for 131500 tokens
+// (539 MB, 3.0 TB/s), 512 for four times as many (4.2 TB/s): the loads bound it, and the joining
+// of four waves at each of 2048 segments.  Four single tokens, 1750 tokens in all: 12 us, of
+// which the bytes would take 1.3; the others are loads that wait for each other, from the
+// requests' rows to their page ids, keys, values and the parts.
 template <class E, int D, int kSet, int kTiles>
 __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs a) {
     constexpr int NT = D / 32, NC = D / 16;
@@ -835,10 +852,24 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
 }
 
 // The many-rows form, for groups and prompts: a wave takes 32 columns, the workgroup eight
-// (at head_dim 64 and 256: four) times as many, and all waves read the same 64 keys from LDS, which
-// the next 64 are brought to meanwhile (global_load_lds: memory to LDS with no registers
-// between).  The lanes of such a load pick their 16 bytes so that what a wave reads later,
-// an operand of a matrix instruction, lies in LDS lane after lane.
+// (at head_dim 64 and 256: four) times as many, and all waves read the same 64 keys from LDS,
+// which the next 64 are brought to meanwhile (global_load_lds: memory to LDS with no registers
+// between).  The lanes of such a load pick their 16 bytes so that what 16 lanes read later,
+// for an operand of a matrix instruction, lies in different banks.
+//
+// With eight waves two share a SIMD, and they are half a stage apart: while one multiplies, the
+// other makes weights of its scores, which takes the vector unit about as long (1024 matrix
+// cycles and 1000 of the other a stage), so both units work.  In step with each other, every
+// wave's operands waited for one by one, the same loop took 350 us where this one takes 318.
+// Reading the operands a group ahead, four at a time, is worth a further third of the product's
+// time; nothing with a mask is in the products' path (see clean), for two paths cost copies of
+// the accumulators and spills.
+//
+// 1145 rows behind 8192 shared tokens, 64 query and 8 key heads of 128, bf16: 318 us, 970
+// TFLOP/s.  What bounds it: LDS, which gives an operand of 1 KB to one matrix instruction of 32
+// cycles only, so that four SIMDs ask for all of its 128 bytes a cycle, beside what is brought.
+// More columns a wave would need twice the accumulators, and leave one wave a SIMD and nothing
+// to work while it waits.
 template <int D>
 struct Wide {
     static constexpr int kWaves = D == 128 ? 8 : 4;
@@ -853,7 +884,7 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
     constexpr int NT = D / 32, NC = D / 16;
     constexpr int kStage = 8 * W::kBlock * 2, kJoin = W::kWaves * 32 * kPitch * 4;  // bytes
     __shared__ __attribute__((aligned(16))) char s_mem[2 * kStage > kJoin ? 2 * kStage : kJoin];
-    __shared__ int s_have[2][4];
+    __shared__ int s_have[4][4], s_special;
     __shared__ uint32_t s_base[8];
     extern __shared__ uint32_t s_cum[];  // running units, n + 1, then the requests
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -861,16 +892,17 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
     const int n = kSet ? a.n_groups : a.R;
     const uint32_t total = plan<kSet, W::kThreads>(a, n, s_cum, s_base);
     const Split split(a, kSet, total);
-    if (kSet == 0 && tid == 0) a.ends[blockIdx.x].units = 0;
-    if ((int)blockIdx.x >= split.workers) return;
+    const int me = split.by_xcd();
+    if (kSet == 0 && tid == 0) a.ends[me].units = 0;
+    if (me >= split.workers) return;
     const int shift = a.page_shift - 4, in_page = (1 << shift) - 1;  // blocks of 16 in a page
     const int head_shift = __builtin_ctz(D) + a.page_shift;          // a head's elements in a page
     // where this lane's 16 bytes of each 1 KB of a block come from: K's keys with bits 2 and 3 of
     // their number swapped, V's halves of 16 tokens one after the other
     const int key = lane & 15, k_from = (lane >> 4) * 128 + ((key & 3) | ((key & 4) << 1) | ((key & 8) >> 1)) * 8;
-    const int v_from = col * 16 + half * 8;
+    const int v_from = lane / 2 * 16 + ((lane ^ (lane >> 4)) & 1) * 8, v_at = (col * 2 + (half ^ ((col >> 3) & 1))) * 16;
 
-    Cursor<kSet, W::kTile, W::kUnit> cur(split, blockIdx.x, tid == 0);
+    Cursor<kSet, W::kTile, W::kUnit> cur(split, me, tid == 0);
     do {
         cur.look(a, split, n, s_cum);
         const Work& q = cur.q;
@@ -881,7 +913,7 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
         // The column's last key; the wave's earliest and latest of them, and the tile's latest.
         const int last = cur.last_of(a, f), first_last = cur.last_of(a, f0 + min(wave * 32, nf - 1));
         const int wave_end = wave * 32 >= nf ? 0 : cur.last_of(a, f0 + min(wave * 32 + 31, nf - 1)) + 1;
-        const int tile_end = cur.last_of(a, f0 + nf - 1) + 1;
+        const int tile_end = cur.last_of(a, f0 + nf - 1) + 1, tile_first = cur.last_of(a, f0);
 
         f32x16 o[NT];
 #pragma unroll
@@ -889,70 +921,86 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
         float m = -kInf, l = 0.f;  // m of the raw scores; l this half's share of the sum
         int pos = q.kb + (int)(cur.unit0 * W::kUnit);
         const int pos_end = min(tile_end, q.kb + (int)(cur.unit1 * W::kUnit));
-        int special_from = -1;
-        bool bad_page = false;
-        PageIds pages;
-        if (pos < pos_end)
-            pages.start(q.table, (q.ke + (1 << a.page_shift) - 1) >> a.page_shift,
-                        min(pos + (wave & 3) * 16, q.ke - 1) >> a.page_shift, lane);
+        const int stages = pos < pos_end ? (pos_end - pos + W::kUnit - 1) / W::kUnit : 0, pos0 = pos;
 
-        // Block b of the 64 keys at p: whether it is there, and its first element of K and V.
-        const auto locate = [&](int p, int b, size_t& at) {
-            const int blk = (p >> 4) + b;
-            bool there = p + b * 16 < q.ke;
-            int page = there ? pages.at(blk >> shift, lane) : 0;
-            if ((unsigned)page >= (unsigned)a.n_pages) {
-                page = 0;
-                there = false;
-                bad_page = true;
-            }
-            at = (((size_t)(unsigned)page * (unsigned)a.Hkv + h) << head_shift) + (size_t)(blk & in_page) * W::kBlock;
-            return there;
+        // The first four waves each bring a block's K and the others its V, or each of four waves
+        // the K and a stage later the V.  Where the blocks of 64 stages are stands in the lanes.
+        uint32_t at_low = 0, at_high = 0;
+        uint64_t there = 0, bad_pages = 0;
+        const auto element = [&](int page, int p) {
+            return (((size_t)(unsigned)page * (unsigned)a.Hkv + h) << head_shift) + (size_t)(p >> 4 & in_page) * W::kBlock;
         };
-        const auto bring = [&](int p, int buf) {
-            const int b = wave & 3;
-            size_t at;
-            const bool there = locate(p, b, at);
-            if (wave < 4 && lane == 0) s_have[buf][b] = there;
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                if (W::kWaves == 8 && kv != wave >> 2) continue;  // waves 0-3 bring K, 4-7 V; or each both
-                const uint16_t* from = kv ? a.v + at + v_from : a.k + at + k_from;
-                char* to = s_mem + buf * kStage + (kv * 4 + b) * (W::kBlock * 2);
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j)
-                    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from + j * 512),
-                                                     (__attribute__((address_space(3))) void*)(to + j * 1024), 16, 0, 0);
-            }
+        const auto locate = [&](int t) {
+            const int p = pos0 + (t + lane) * W::kUnit + (wave & 3) * 16;
+            const bool wanted = t + lane < stages && p < q.ke;
+            int page = wanted ? q.table[p >> a.page_shift] : 0;
+            const bool bad = (unsigned)page >= (unsigned)a.n_pages;
+            if (bad) page = 0;
+            there = __ballot(wanted && !bad);
+            bad_pages |= __ballot(bad);
+            const size_t at = element(page, p);
+            at_low = (uint32_t)at, at_high = (uint32_t)(at >> 32);
         };
-
-        __syncthreads();  // LDS is free
-        if (pos < pos_end) {
-            pages.settle();
-            bring(pos, 0);
-        }
-        for (int buf = 0; pos < pos_end; buf ^= 1, pos += W::kUnit) {
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's share of the 64 keys has landed
-            __syncthreads();                                  // everyone's has, and the other buffer is free
-            if (pos + W::kUnit < pos_end) bring(pos + W::kUnit, buf ^ 1);
-            if (pos >= wave_end) continue;  // the wave's columns see none of these
-            const char* mem = s_mem + buf * kStage;
-            f32x16 s[2];
+        size_t at = 0;
+        const auto find = [&](int t) {
+            if (!(t & 63)) locate(t);
+            at = (size_t)__builtin_amdgcn_readlane(at_high, t & 63) << 32 |
+                 (uint32_t)__builtin_amdgcn_readlane(at_low, t & 63);
+        };
+        const auto bring = [&](int t, int kv) {
+            const uint16_t* from = kv ? a.v + at + v_from : a.k + at + k_from;
+            char* to = s_mem + (t & 1) * kStage + (kv * 4 + (wave & 3)) * (W::kBlock * 2);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                s[b] = f32x16{};
-                const char* kl = mem + (2 * b + (col >> 4)) * (W::kBlock * 2) + (half * 16 + (col & 15)) * 16;
+            for (int j = 0; j < D / 32; ++j)
+                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from + j * 512),
+                                                 (__attribute__((address_space(3))) void*)(to + j * 1024), 16, 0, 0);
+        };
+        const auto bring_keys = [&](int t) {
+            if (t >= stages) return;
+            find(t);
+            if (lane == 0) s_have[t & 3][wave & 3] = (int)(there >> (t & 63)) & 1;
+            bring(t, 0);
+        };
+        const auto bring_values = [&](int t) {
+            if (t >= stages) return;
+            if (W::kWaves == 8) find(t);
+            bring(t, 1);
+        };
+        const auto wait_loads = [] { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
+        // Stage t's scores; its weights, from the scores; its second product, from the weights.
+        f32x16 s[2];
+        s16x8 pf[4];
+        bool masked = false;
+        const auto scores = [&](int t) {
+            const char* mem = s_mem + (t & 1) * kStage + (half * 16 + (col & 15)) * 16 + (col >> 4) * (W::kBlock * 2);
+            s[0] = s[1] = f32x16{};
+            s16x8 kf[2][4];
+            const auto read = [&](int g) {
 #pragma unroll
-                for (int c = 0; c < NC; ++c) s[b] = E::mfma(*(const s16x8*)(kl + c * 512), qf[c], s[b]);
+                for (int j = 0; j < 4; ++j)
+                    kf[g & 1][j] = *(const s16x8*)(mem + (j & 1) * (W::kBlock * 4) + (g * 2 + j / 2) * 512);
+            };
+            const int4 have = *(const int4*)s_have[t & 3];
+            read(0);
+#pragma unroll
+            for (int g = 0; g < NC / 2; ++g) {
+                if (g + 1 < NC / 2) read(g + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[j & 1] = E::mfma(kf[g & 1][j], qf[g * 2 + j / 2], s[j & 1]);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            const int4 have = *(const int4*)s_have[buf];
-            const bool all = uniform(have.x & have.y & have.z & have.w);
-            const bool masked = pos + 63 > first_last || !all;
+            masked = pos0 + t * W::kUnit + 63 > first_last || !uniform(have.x & have.y & have.z & have.w);
+        };
+        const auto weights = [&](int t) {
             if (masked) {
+                const int4 have = *(const int4*)s_have[t & 3];
+                int left = last - (pos0 + t * W::kUnit) - half * 8;
+                asm volatile("" : "+v"(left));  // so that no key's number takes a register in the loop
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
                     const int there = j < 8 ? have.x : j < 16 ? have.y : j < 24 ? have.z : have.w;
-                    if (pos + (j / 8) * 16 + half * 8 + j % 8 > last || !there) s[j / 16][j % 16] = -kInf;
+                    if ((j / 8) * 16 + j % 8 > left || !there) s[j / 16][j % 16] = -kInf;
                 }
             }
             float mx = s[0][0];
@@ -965,64 +1013,132 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
                 m = m_new;
                 l *= alpha;
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int i = 0; i < NT; ++i)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) o[t][j] *= alpha;
+                    for (int j = 0; j < 16; ++j) o[i][j] *= alpha;
             }
             const float mc = m == -kInf ? 0.f : m * a.scale_log2;
-            s16x8 pf[4];
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
                 const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j / 16][j % 16], a.scale_log2, -mc));
                 l += p;
                 pf[j / 8][j % 8] = (short)E::bits(p);  // the weights, rounded for the matrix instruction
             }
-            const char* vl = mem + 4 * (W::kBlock * 2) + lane * 16;
-            if (!masked) {
+        };
+        const auto values = [&](int t) {
+            const char* vl = s_mem + (t & 1) * kStage + 4 * (W::kBlock * 2) + v_at;
+            s16x8 vf[2][4];
+            const auto read = [&](int g) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int j = 0; j < 4; ++j)
+                    vf[g & 1][j] = *(const s16x8*)(vl + ((g & 1) * 2 + j / 2) * (W::kBlock * 2) + (g / 2 * 2 + (j & 1)) * 1024);
+            };
+            read(0);
 #pragma unroll
-                    for (int b = 0; b < 4; ++b)
-                        o[t] = E::mfma(*(const s16x8*)(vl + b * (W::kBlock * 2) + t * 1024), pf[b], o[t]);
-            } else {
-                uint32_t special = 0;
+            for (int g = 0; g < NT; ++g) {
+                if (g + 1 < NT) read(g + 1);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        s16x8 v = *(const s16x8*)(vl + b * (W::kBlock * 2) + t * 1024);
-                        const int there = b == 0 ? have.x : b == 1 ? have.y : b == 2 ? have.z : have.w;
-                        special |= clear_masked<E>(v, there ? q.ke - (pos + b * 16 + half * 8) : 0);
-                        o[t] = E::mfma(v, pf[b], o[t]);
-                        __builtin_amdgcn_sched_barrier(0);  // one after the other, in few registers
-                    }
-                if (special_from < 0 && __ballot(special != 0)) special_from = pos;
+                for (int j = 0; j < 4; ++j)
+                    o[g / 2 * 2 + (j & 1)] = E::mfma(vf[g & 1][j], pf[(g & 1) * 2 + j / 2], o[g / 2 * 2 + (j & 1)]);
+                __builtin_amdgcn_sched_barrier(0);
             }
+        };
+        // Where a column of the tile does not see all of stage t, its weights there are zero, but
+        // zero times what is not finite is not: the wave that brought a block's V removes such
+        // values, and all behind the last key, before anyone reads them.  What is removed and
+        // seen is added behind the loop, from the first such stage on.
+        const auto clean = [&](int t) {
+            if (t >= stages) return;
+            const int p = pos0 + t * W::kUnit + (wave & 3) * 16;
+            const bool is_there = uniform(s_have[t & 3][wave & 3]);
+            if (is_there && pos0 + t * W::kUnit + 63 <= tile_first) return;
+            char* block = s_mem + (t & 1) * kStage + (4 + (wave & 3)) * (W::kBlock * 2) + lane * 16;
+            const int keys = is_there ? q.ke - p - ((lane ^ (lane >> 4)) & 1) * 8 : 0;
+            uint32_t special = 0;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                s16x8 v = *(const s16x8*)(block + i * 1024);
+                special |= clear_masked<E>(v, keys);
+                *(s16x8*)(block + i * 1024) = v;
+                __builtin_amdgcn_sched_barrier(0);  // one after the other, in few registers
+            }
+            if (__ballot(special != 0) && lane == 0) atomicMin(&s_special, t);
+        };
+        const int seen = wave_end > pos0 ? min(stages, (wave_end - pos0 + W::kUnit - 1) / W::kUnit) : 0;  // by the wave
+
+        if (tid == 0) s_special = 1 << 30;
+        __syncthreads();  // LDS is free
+        const bool late = wave >= 4;  // half a stage behind: a barrier more before, one fewer after
+#pragma unroll
+        for (int c = 0; c < NC; ++c) asm volatile("" : "+v"(qf[c]));  // there, so that no later wait is for them
+        if (!late) bring_keys(0);
+        wait_loads();
+        lds_barrier();
+        if (late) {
+            bring_values(0);
+            lds_barrier();
         }
+        // K of stage t + 1 and V of stage t come while the early waves make stage t's weights and the
+        // late ones are still at its scores: into the halves of LDS whose readers the barrier
+        // before has let go, to be read after the next.  (Four waves, one a SIMD: in one step.)
+        for (int t = 0; t <= stages; ++t) {
+            if (W::kWaves == 4) {
+                bring_values(t);
+                bring_keys(t + 1);
+            }
+            if (t > 0 && t <= seen) values(t - 1);
+            if (t < seen) scores(t);
+            if (W::kWaves == 8) {
+                if (late) {
+                    wait_loads();
+                    clean(t);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                lds_barrier();
+                if (late)
+                    bring_values(t + 1);
+                else
+                    bring_keys(t + 1);
+            }
+            if (t < seen) weights(t);
+            if (!late) wait_loads();
+            if (W::kWaves == 4) clean(t);
+            __builtin_amdgcn_sched_barrier(0);
+            lds_barrier();
+        }
+        if (W::kWaves == 8 && !late) lds_barrier();
         l = add_halves(l);
-        if (bad_page && lane == 0) raise_status(a.status, kStatusBadPage);
-        if (special_from >= 0) {
-            pages.fetch(special_from >> a.page_shift, lane);
-            pages.settle();
-            for (pos = special_from; pos < min(pos_end, wave_end); pos += 32) {
+        if (bad_pages && lane == 0) raise_status(a.status, kStatusBadPage);
+        const int special_from = uniform(s_special);
+        if (special_from < stages) {
+            for (pos = pos0 + special_from * W::kUnit; pos < min(pos_end, wave_end); pos += 32) {
                 size_t at[2];
-                const bool have[2] = {locate(pos, 0, at[0]), locate(pos, 1, at[1])};
+                bool have[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int p = pos + b * 16;
+                    const int page = p < q.ke ? q.table[p >> a.page_shift] : -1;
+                    have[b] = (unsigned)page < (unsigned)a.n_pages;
+                    at[b] = element(have[b] ? page : 0, p);
+                }
                 s16x8 sees[2];
+                int left = last - pos - half * 8;
+                asm volatile("" : "+v"(left));
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    sees[j / 8][j % 8] =
-                        pos + (j / 8) * 16 + half * 8 + j % 8 <= last && have[j / 8] ? (short)E::kOne : (short)0;
+                    sees[j / 8][j % 8] = (j / 8) * 16 + j % 8 <= left && have[j / 8] ? (short)E::kOne : (short)0;
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
-                    add_special<E>(o[t], *(const s16x8*)(a.v + at[0] + t * 512 + v_from),
-                                   *(const s16x8*)(a.v + at[1] + t * 512 + v_from), sees[0], sees[1]);
+                    add_special<E>(o[t], *(const s16x8*)(a.v + at[0] + t * 512 + col * 16 + half * 8),
+                                   *(const s16x8*)(a.v + at[1] + t * 512 + col * 16 + half * 8), sees[0], sees[1]);
             }
         }
         m = m == -kInf ? -kInf : m * a.scale_log2;
 
         const bool whole = cur.whole();
         __syncthreads();  // LDS is free
-        finish_wave<E, kSet, NT>(a, (float*)s_mem + wave * (32 * kPitch), blockIdx.x, whole && q.kb == 0, whole, cur.unit0 == 0, f0, wave * 32, nf,
+        finish_wave<E, kSet, NT>(a, (float*)s_mem + wave * (32 * kPitch), me, whole && q.kb == 0, whole, cur.unit0 == 0, f0, wave * 32, nf,
                                  h, m, l, o);
     } while (cur.step());
 }
