@@ -564,9 +564,10 @@ int dspark_cache_append(const dspark_cache_t* cache, int layer, const void* k_ne
  * already.  Row j of request r sees the positions 0..len[r] + j of its table row:
  *   out[row, head] = sum_p softmax_p(scale * q[row, head] . K[p, g]) V[p, g]
  *   lse[row, head] = ln sum_p exp(scale * q[row, head] . K[p, g])        g = head / (H / n_kv_heads)
- * Scores, the softmax and the sums are held in fp32; the weights (at most 1, relative to
- * the row's largest) are rounded to the cache's dtype for the second product, and out once.
- * A position that a row does not see has no influence on it, whatever its K and V hold.
+ * Scores, the softmax and the sums are held in fp32; the weights, relative to a running
+ * maximum (and at most 2^8, since it follows in steps), are rounded to the cache's dtype for
+ * the second product, and out once.  A position that a row does not see has no influence on
+ * it, whatever its K and V hold.
  *   q, out   [n_rows] rows of [H, head_dim], q_stride and out_stride elements apart
  *            (multiples of 8; 16-byte aligned), in the cache's dtype; they must not alias
  *   lse      [n_rows, H] fp32 output, or NULL

@@ -329,3 +329,130 @@ def test_determinism_and_a_captured_call():
         c.call(p, out=eager)
         torch.cuda.synchronize()
         assert torch.equal(eager, p["out"])
+
+
+# Requests and groups of more than 64 columns, which the kernels bring to LDS for all waves.
+
+@pytest.mark.parametrize("special", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64), ("bf16", 256), ("fp16", 128)])
+def test_masked_values_have_no_say_in_prompts(special, dtype, D):
+    # values that are not numbers early, at a stage's end and in the last row's own place: rows
+    # before them see none of it, rows from there on all of it
+    _say("attend special, prompts", special, dtype, D)
+    c = Case(16, [10, 130, 0], [90, 75, 130], 4, 2, D, dtype)
+    st = c.st
+    for r, j, head in ((0, 3, 0), (0, 89, 1), (1, 62, 0), (2, 127, 1), (2, 64, 0)):
+        p = st.len[r] + j
+        st.v[0, st.table[r][p // 16], head, p % 16, 3:20] = special
+        st.v[0, st.table[r][p // 16], head, p % 16, D - 1] = -special
+    if math.isnan(special):
+        p = st.len[1] + 50
+        st.k[0, st.table[1][p // 16], 1, p % 16, 0] = special
+    want = c.want()
+    assert np.isfinite(want[0][:3]).all() and np.isfinite(want[0][165:165 + 64]).all()
+    assert not np.isfinite(want[0][3]).all() and not np.isfinite(want[0][-1]).all()
+    c.check(want=want)
+
+
+@pytest.mark.parametrize("special", [math.nan, math.inf])
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64), ("bf16", 256)])
+def test_special_values_in_a_shared_prefix(special, dtype, D):
+    # a prefix that ends inside a stage of 64, with one such value near its start and one near its end
+    _say("attend special, prefix", special, dtype, D)
+    c = Case(17, [9 * 16 + 5] * 12, [8] * 12, 4, 2, D, dtype, groups=[(6, 9), (6, 9)])
+    st = c.st
+    for g, p in ((0, 3), (0, 140)):
+        st.v[0, c.shared[g][p // 16], 1, p % 16, 7:9] = special
+    want = c.want()
+    assert not np.isfinite(want[0][:48]).all() and np.isfinite(want[0][48:]).all()
+    c.check(want=want)
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64), ("bf16", 256)])
+def test_bad_pages_of_prompts_and_prefixes(dtype, D):
+    # pages that are not there in the middle and at the ends: their tokens are left out
+    _say("attend bad pages, many rows", dtype, D)
+    for bad_id in (-1, 1 << 30, -(1 << 31)):
+        c = Case(18, [200, 20], [80, 100], 4, 2, D, dtype)
+        for r, i in ((0, 0), (0, 5), (0, 6), (0, 7), (0, 8), (1, 2)):
+            c.st.table[r][i] = bad_id
+        c.check(status=B.STATUS_BAD_PAGE)
+    c = Case(18, [13 * 16 + 9] * 20, [8] * 20, 4, 2, D, dtype, groups=[(20, 13)])
+    for r in range(20):
+        c.st.table[r][4] = c.st.table[r][12] = -1
+    c.shared[0][4] = c.shared[0][12] = -1
+    c.check(status=B.STATUS_BAD_PAGE)
+
+
+@pytest.mark.parametrize("rows,lens", [([64, 1, 0, 65], [0, 300, 12, 63]), ([16, 17], [64, 0]), ([300], [0]), ([129, 2, 128], [-1, 5, 1])])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_ragged_prompts(rows, lens, D):
+    # tiles and stages that end early, requests with none of the other's columns, vacant ones
+    _say("attend ragged prompts", rows, lens, D)
+    Case(19, lens, rows, 4, 1, D, "bf16", 64, lead=0, pad=3).check()
+
+
+def test_long_context_of_many_columns():
+    # more than 64 stages of 64 keys to a workgroup, against float64 on the device
+    _say("attend long, many columns")
+    D, Hkv, H, page, T, rows = 128, 8, 64, 16, 150001, 9
+    n_pages = -(-(T + rows) // page)
+    st = B.PagedCache(1, n_pages + 2, page, Hkv, D, B.DSPARK_BF16, 1, n_pages, device=cu.DEV)
+    g = torch.Generator(device=cu.DEV).manual_seed(5)
+    st.k.normal_(generator=g)
+    st.v.normal_(generator=g)
+    ids = torch.randperm(n_pages + 2, generator=g, device=cu.DEV)[:n_pages]
+    st.table[0] = ids.to(torch.int32)
+    st.len.fill_(T)
+    q = torch.randn((rows, H, D), generator=g, device=cu.DEV).bfloat16()
+    out, lse = torch.empty_like(q), torch.empty((rows, H), device=cu.DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=cu.DEV)
+    scale = 1 / math.sqrt(D)
+    B.dspark_cache_attend(st, 0, q, cu.i32([0, rows - 1]), 1, rows, scale, out, lse=lse,
+                          ws=B.cache_workspace(st, 1, H, rows), status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    want = [np.empty((rows, H, D)), np.empty((rows, H)), np.empty((rows, H, D)), np.empty((rows, H))]
+    last = T + torch.arange(rows, device=cu.DEV)
+    for h in range(Hkv):
+        k = st.k[0, ids, h, 0].double().permute(0, 2, 1, 3).reshape(-1, D)
+        v = st.v[0, ids, h, 0].double().permute(0, 2, 1).reshape(-1, D)
+        hs = slice(h * (H // Hkv), (h + 1) * (H // Hkv))
+        x = q[:, hs].double().reshape(-1, D)
+        s = scale * torch.mm(x, k.t().contiguous())
+        s.masked_fill_(torch.arange(k.shape[0], device=cu.DEV)[None] > last.repeat_interleave(H // Hkv)[:, None], -math.inf)
+        l = torch.logsumexp(s, 1)
+        w = torch.exp(s - l[:, None])
+        reach = scale * torch.mm(x.abs(), k.abs().t().contiguous()).amax(1)
+        for i, y in enumerate((torch.mm(w, v), l, torch.mm(w, v.abs()), reach)):
+            want[i][:, hs] = y.reshape((rows, H // Hkv) + tuple(y.shape[1:])).cpu().numpy()
+    cu.assert_attend(out, lse, want, "bf16", T + rows, D)
+
+
+def test_two_captured_calls_share_a_workspace():
+    _say("attend two graphs, one workspace")
+    a = Case(20, [70, 90, 33], [40, 8, 30], 4, 2, 128, groups=[(2, 3)])
+    b = Case(21, [700, -1, 9], [2, 1, 8], 8, 2, 64, "fp16")
+    pa, pb = a.prepared(), b.prepared()
+    if pb["ws"].numel() > pa["ws"].numel():
+        pa["ws"] = pb["ws"]
+    else:
+        pb["ws"] = pa["ws"]
+    s, graphs = torch.cuda.Stream(), []
+    with torch.cuda.stream(s):
+        a.call(pa)
+        b.call(pb)
+    s.synchronize()
+    want = [pa["out"].clone(), pb["out"].clone()]
+    for c, p in ((a, pa), (b, pb)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.call(p)
+        graphs.append(g)
+    for order in ((0, 1), (1, 0), (0, 0, 1), (1, 1, 0)):
+        pa["out"].fill_(7.0)
+        pb["out"].fill_(7.0)
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(pa["out"], want[0]) and torch.equal(pb["out"], want[1])
