@@ -233,6 +233,9 @@ template <int kSet, int kThreads>
 __device__ uint32_t plan(const AttendArgs& a, int n, uint32_t* s_cum, uint32_t* s_base) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     Request* s_info = (Request*)(s_cum + n + 1);
+    // More units than 32 bits number can only come from offsets that fall and rise again, so
+    // that requests or groups share rows: the sums then stop past the bound, and none are served.
+    const uint32_t most = min(0x7FFFFFFFu / (uint32_t)a.Hkv, 0x7FFFFFFEu);
     uint32_t base = 0, bad = 0;
     for (int i0 = 0; i0 < n; i0 += kThreads) {
         const int i = i0 + tid;
@@ -252,18 +255,24 @@ __device__ uint32_t plan(const AttendArgs& a, int n, uint32_t* s_cum, uint32_t* 
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const uint32_t z = __shfl_up(y, d, 64);
-            if (lane >= d) y += z;
+            if (lane >= d) y = min(y + z, most + 1);
         }
         __syncthreads();
         if (lane == 63) s_base[wave] = y;
         __syncthreads();
-        for (int w = 0; w < wave; ++w) y += s_base[w];
-        if (i < n) s_cum[i] = base + y - x;
+        for (int w = 0; w < wave; ++w) y = min(y + s_base[w], most + 1);
+        if (i < n) s_cum[i] = min(base + y, most + 1) - x;
 #pragma unroll
-        for (int w = 0; w < kThreads / 64; ++w) base += s_base[w];
+        for (int w = 0; w < kThreads / 64; ++w) base = min(base + s_base[w], most + 1);
     }
     if (tid == 0) s_cum[n] = base;
     __syncthreads();
+    if (base > most) {
+        for (int i = tid; i <= n; i += kThreads) s_cum[i] = 0;
+        base = 0;
+        bad = kStatusBadRow;
+        __syncthreads();
+    }
     if (blockIdx.x == 0) {
         if (a.n_groups)
             for (int i = tid; i <= n; i += kThreads) a.cum[kSet][i] = s_cum[i];
@@ -1166,7 +1175,9 @@ __global__ __launch_bounds__(kT) void attend_join_shared_kernel(AttendArgs a) {
     Request q;
     uint32_t bad = 0;
     if (request_of(a, r, q, bad) != 1) return;
-    const Split own(a, 0, a.cum[0][a.R] * a.Hkv), common(a, 1, a.cum[1][a.n_groups] * a.Hkv);
+    const uint32_t own_units = a.cum[0][a.R] * a.Hkv, common_units = a.cum[1][a.n_groups] * a.Hkv;
+    if (own_units == 0) return;  // offsets out of all bounds (see plan)
+    const Split own(a, 0, own_units), common(a, 1, common_units);
     const uint32_t u0 = a.cum[0][r] * a.Hkv, units = units_in(a, 0, q.ln + q.n - q.kb);
     const int tiles = tiles_in(a, 0, q.n), f0 = q.start * a.G;
     if (q.kb == 0 && own.worker_of(u0) == own.worker_of(u0 + a.Hkv * tiles * units - 1)) return;  // all done already
@@ -1176,7 +1187,7 @@ __global__ __launch_bounds__(kT) void attend_join_shared_kernel(AttendArgs a) {
         g = shared_of(a, q.group, bad);
         g_u0 = a.cum[1][q.group] * a.Hkv;
         // (rows outside the group's, as offsets that fall would have it, have no part there)
-        if (q.start < g.start || q.start + q.n > g.start + g.n) g.ke = 0;
+        if (q.start < g.start || q.start + q.n > g.start + g.n || common_units == 0) g.ke = 0;
     }
     const int end = min((blockIdx.z + 1) * kJoinItems, (uint32_t)(q.n * a.G * chunks));
     for (int e = blockIdx.z * kJoinItems + threadIdx.x; e < end; e += kT) {
@@ -1274,10 +1285,12 @@ hipError_t launch_attend(AttendArgs a, int cus, hipStream_t s) {
     cus = std::min(cus, kAttendMaxCus);
     for (int set = 0; set < 2; ++set) {
         const long long columns = (long long)(set ? a.rows : a.max_new) * a.G;
-        a.tile[set] = columns > kWideFrom ? wide : columns > 32 ? 64 : 32;
+        // (at head_dim 256 the keys leave LDS for 4096 requests' running units beside them)
+        const bool many = columns > kWideFrom && (set || a.D < 256 || a.R <= 4096);
+        a.tile[set] = many ? wide : columns > 32 ? 64 : 32;
         a.unit[set] = columns > 32 ? 64 : 128;
-        a.workers[set] = cus * (columns > kWideFrom ? wide_per_cu : a.D <= 128 ? 2 : 1);
-        a.least[set] = columns > kWideFrom ? kWideLeast : kFewLeast;
+        a.workers[set] = cus * (many ? wide_per_cu : a.D <= 128 ? 2 : 1);
+        a.least[set] = many ? kWideLeast : kFewLeast;
         a.tile_shift[set] = __builtin_ctz(a.tile[set]);
         a.unit_shift[set] = __builtin_ctz(a.unit[set]);
     }

@@ -49,6 +49,7 @@ struct AppendArgs {
     uint16_t* v;
     const int32_t* table;
     const int32_t* len;
+    const int32_t* ref;
     const int32_t* offsets;
     int lead, R, rows, max_new, Hkv, D, page, page_shift, n_pages, width;
     uint32_t* status;

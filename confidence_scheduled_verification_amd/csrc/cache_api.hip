@@ -159,7 +159,7 @@ int dspark_cache_append(const dspark_cache_t* c, int layer, const void* k_new, i
     if (!offsets) return fail(DSPARK_EINVAL, "%s: offsets is NULL", who);
     const size_t at = layer * layer_elems(c);
     const dspark::AppendArgs a{(const uint16_t*)k_new, (const uint16_t*)v_new, k_stride, v_stride,
-                               (uint16_t*)c->k + at, (uint16_t*)c->v + at, c->table, c->len, offsets, lead, R, n_rows,
+                               (uint16_t*)c->k + at, (uint16_t*)c->v + at, c->table, c->len, c->ref, offsets, lead, R, n_rows,
                                max_new, c->n_kv_heads, c->head_dim, c->page_size, __builtin_ctz(c->page_size),
                                c->n_pages, c->width, status};
     return done(dspark::launch_append(a, (hipStream_t)stream), who);

@@ -5,9 +5,17 @@
 //
 // Ranking the free pages: the counts are cut into slices of 4096, sixteen pages to a thread.
 // A first launch counts each slice; in the second each workgroup adds up the slices before
-// its own, ranks its free pages by one scan, and gives the page of rank k to the request that holds place k of
-// the running needs, found by bisection in LDS.  Two launches, whatever the sizes; nothing
-// is kept between calls.
+// its own, ranks its free pages by one scan, and gives the page of rank k to the request that
+// holds place k of the running needs, found by bisection in LDS.  Two launches, whatever the
+// sizes; nothing is kept between calls.
+//
+// What bounds them: the launches and a few loads that wait for each other, where only numbers
+// are moved (trim and reserve together: 15 us for 64 requests and 16 for 1024 over a nearly
+// full cache; with the free pages of a slice found one by one by bisection over the counts, 37),
+// and the copy of the pages elsewhere, read and written once.  64 forks, a last page of 64
+// tokens, 8 heads of 128 and 8 layers each (268 MB): the copy is 50 of 66 us, 5.4 TB/s; 24 whole
+// copies (710 MB) 133 of 157 us, 5.3; 6000 of 12000 pages made compact (3.1 GB) 605 of 634 us, 5.2.
+// A large library copy reaches 5.5.
 #include "cache.h"
 #include "common.h"
 

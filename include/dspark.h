@@ -552,8 +552,9 @@ int dspark_pages_compact(const dspark_cache_t* cache, int32_t* page_map, int32_t
  *                 apart (multiples of 8; 16-byte aligned), in the cache's dtype
  *   offsets       [R+1], lead: the step's rows; max_new >= every n_r
  * A request with n_r < 0 or > max_new, rows outside the tensors or tokens past its table
- * is left out (DSPARK_STATUS_BAD_ROW); so are tokens whose page id is none
- * (DSPARK_STATUS_BAD_PAGE).
+ * is left out (DSPARK_STATUS_BAD_ROW); so are tokens whose page id is none, or whose page has
+ * a count above 1 and so is another row's too: a row that was cut back into a page it shares
+ * goes on as a fork, which has a copy of that page (DSPARK_STATUS_BAD_PAGE).
  */
 int dspark_cache_append(const dspark_cache_t* cache, int layer, const void* k_new, int64_t k_stride, const void* v_new,
                         int64_t v_stride, int n_rows, const int32_t* offsets, int lead, int R, int max_new,
@@ -583,8 +584,9 @@ int dspark_cache_append(const dspark_cache_t* cache, int layer, const void* k_ne
  *   [n_groups, shared_width] int32, shared_pages [n_groups] int32
  * Rows that see nothing (vacant requests) get zeros and lse -inf; so do those of a request
  * whose length fits neither its table nor its group (DSPARK_STATUS_BAD_ROW).  A request
- * with n_r < 0 or > max_new or rows outside the tensors is left out with the same status,
- * and rows that belong to no request stay as they are.  Page ids outside the cache are not
+ * with n_r < 0 or > max_new or rows outside the tensors, or from row R * max_new on, is left
+ * out with the same status, and rows that belong to no request stay as they are.  So do all
+ * rows where offsets that fall and rise make more work than 32-bit numbers hold.  Page ids outside the cache are not
  * read: their tokens are left out (DSPARK_STATUS_BAD_PAGE).  Results are the same in every
  * run.  More rows, heads and tokens than 32-bit numbers of work units hold return
  * DSPARK_EUNSUPPORTED.

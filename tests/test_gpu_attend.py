@@ -456,3 +456,42 @@ def test_two_captured_calls_share_a_workspace():
             graphs[i].replay()
         torch.cuda.synchronize()
         assert torch.equal(pa["out"], want[0]) and torch.equal(pb["out"], want[1])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_requests_of_many_columns(D):
+    # the running units of as many requests as a call takes, beside the keys in LDS
+    _say("attend many requests, many columns", D)
+    R = 8192
+    rng = np.random.default_rng(2)
+    lens = np.where(rng.random(R) < 0.99, -1, rng.integers(0, 40, R)).tolist()
+    rows = [1] * R
+    lens[5], rows[5], lens[8000], rows[8000] = 100, 40, 3, 37
+    Case(22, lens, rows, 2, 1, D).check()
+
+
+def test_offsets_that_fall_and_rise_past_all_bounds():
+    # requests, then groups, that all name the same rows: more units than 32 bits number
+    _say("attend falling offsets")
+    R, n, page, width = 8192, 4096, 256, 4200
+    st = B.PagedCache(1, 2, page, 1, 64, B.DSPARK_BF16, R, width, device=cu.DEV)
+    st.table.zero_()
+    st.len.fill_(width * page - n)
+    q = torch.zeros((n, 1, 64), dtype=torch.bfloat16, device=cu.DEV)
+    out = torch.full_like(q, 7.0)
+    status = torch.zeros(1, dtype=torch.int32, device=cu.DEV)
+    B.dspark_cache_attend(st, 0, q, cu.i32(np.arange(R + 1) % 2 * n), 0, n, 1.0, out, ws=B.cache_workspace(st, R, 1, n),
+                          status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == B.STATUS_BAD_ROW and (out == 7).all()
+    groups, pages = 1024, 16500
+    st.len.fill_(-1)
+    q = torch.zeros((R, 1, 64), dtype=torch.bfloat16, device=cu.DEV)
+    out = torch.full_like(q, 7.0)
+    shared = (cu.i32(np.arange(groups + 1) % 2 * R), torch.zeros((groups, pages), dtype=torch.int32, device=cu.DEV),
+              cu.i32([pages] * groups))
+    status.zero_()
+    B.dspark_cache_attend(st, 0, q, cu.i32(np.arange(R + 1)), 0, 1, 1.0, out, shared=shared,
+                          ws=B.cache_workspace(st, R, 1, 1, groups), status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == B.STATUS_BAD_ROW and (out == 0).all()

@@ -389,3 +389,29 @@ def test_bookkeeping_in_a_captured_graph():
     w, _ = oc.reserve(st.table, st.len, st.ref, offsets, 1, 16)
     np.testing.assert_array_equal(granted.cpu().numpy(), w)
     st.assert_books()
+
+
+def test_a_shared_page_is_not_written_to():
+    # a fork cut back into a page that its parent holds too: its tokens are left out
+    _say("append to a shared page")
+    rng = np.random.default_rng(23)
+    st = cu.State(rng, 1, 8, 16, 1, 64, "bf16", 2, 4)
+    st.len = [40, -1]
+    st.give(0, 3)
+    st.put(0, st.table[0], 0, 48)
+    c = st.upload()
+    status = torch.zeros(1, dtype=torch.int32, device=cu.DEV)
+    ws, flag = B.pages_workspace(c, 2), torch.zeros(2, dtype=torch.int32, device=cu.DEV)
+    B.dspark_pages_fork(c, cu.i32([0]), cu.i32([1]), flag[:1], ws, status=status)
+    B.dspark_pages_trim(c, cu.i32([1]), cu.i32([20]), status=status)
+    offsets = cu.i32([0, 0, 3])
+    B.dspark_pages_reserve(c, offsets, 0, flag, ws, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    before = c.k.clone(), c.v.clone()
+    kn = torch.ones((3, 1, 64), dtype=torch.bfloat16, device=cu.DEV)
+    B.dspark_cache_append(c, 0, kn, kn, offsets, 0, 3, status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == B.STATUS_BAD_PAGE
+    for a, b in zip(before, (c.k, c.v)):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
