@@ -52,11 +52,12 @@ constexpr int kT = 256;
 // keys of 65 to 128 columns twice (two requests of up to 131072 tokens and 72 columns: 194 against 200).
 constexpr int kWideFrom = 64;
 // The units that are worth a workgroup of their own: fewer spread a small call over more of
-// the device, more leave fewer parts to join.  Few rows: 1, 2, 8 give 12.7, 14.7, 24.7 us for
-// four requests of 700 tokens, 31.6, 25.1, 22.1 for one of 8192, 56, 56, 67 for 16 behind 2048
-// shared ones.  Many rows: 1, 4, 8 give 58, 56, 59 us for the last, and 232, 241, 270 where 1145
-// rows share 64 tokens.
-constexpr int kFewLeast = 2, kWideLeast = 4;
+// the device, more leave fewer parts to join.  Many rows: 1, 4, 8 give 58, 56, 59 us for 16
+// requests behind 2048 shared tokens, and 232, 241, 270 where 1145 rows share 64.  Few rows: an
+// eighth of what a request brings to a key head on average, at least 1 and at most 8, so that a
+// segment has about eight parts: four single tokens after up to 700 take 12.7 us with 1 and 24.7
+// with 8, one after 8192 takes 31.6 with 1 and 22.1 with 8; with 2 for both, 14.7 and 25.1.
+constexpr int kWideLeast = 4, kFewParts = 8, kFewMost = 8;
 constexpr float kInf = __builtin_huge_valf();
 // The running maximum follows only when it grows by more than this exponent of two; until
 // then the weights are taken relative to the older one, at most 2^8, and nothing that has
@@ -176,7 +177,9 @@ struct Split {
     uint32_t each, more;
     int workers;
     __device__ __forceinline__ Split(const AttendArgs& a, int set, uint32_t total) {
-        workers = min((uint32_t)a.workers[set], (total + a.least[set] - 1) / a.least[set]);
+        const uint32_t least =
+            a.least[set] ? (uint32_t)a.least[set] : min(max(total / a.parts[set], 1u), (uint32_t)kFewMost);
+        workers = min((uint32_t)a.workers[set], (total + least - 1) / least);
         each = workers ? total / (uint32_t)workers : 0;
         more = workers ? total % (uint32_t)workers : 0;
     }
@@ -615,7 +618,7 @@ __device__ __forceinline__ void load_q(const AttendArgs& a, s16x8 (&qf)[D / 16],
 //
 // 256 requests of 1145 rows, 64 query and 8 key heads of 128, bf16: 177 us for 131500 tokens
 // (539 MB, 3.0 TB/s), 512 for four times as many (4.2 TB/s): the loads bound it, and the joining
-// of four waves at each of 2048 segments.  Four single tokens, 1750 tokens in all: 12 us, of
+// of four waves at each of 2048 segments.  Four single tokens, 1750 tokens in all: 9 us, of
 // which the bytes would take 1.3; the others are loads that wait for each other, from the
 // requests' rows to their page ids, keys, values and the parts.
 template <class E, int D, int kSet, int kTiles>
@@ -1290,7 +1293,8 @@ hipError_t launch_attend(AttendArgs a, int cus, hipStream_t s) {
         a.tile[set] = many ? wide : columns > 32 ? 64 : 32;
         a.unit[set] = columns > 32 ? 64 : 128;
         a.workers[set] = cus * (many ? wide_per_cu : a.D <= 128 ? 2 : 1);
-        a.least[set] = many ? kWideLeast : kFewLeast;
+        a.least[set] = many ? kWideLeast : 0;
+        a.parts[set] = (uint32_t)kFewParts * a.Hkv * std::max(set ? a.n_groups : a.R, 1);
         a.tile_shift[set] = __builtin_ctz(a.tile[set]);
         a.unit_shift[set] = __builtin_ctz(a.unit[set]);
     }

@@ -89,7 +89,10 @@ struct AttendArgs {
     uint16_t* out;
     float* lse;
     uint32_t* status;
-    int tile[2], unit[2], tile_shift[2], unit_shift[2], workers[2], least[2];  // the launches' forms: [0] the requests' own keys, [1] the shared ones
+    // the launches' forms: [0] the requests' own keys, [1] the shared ones
+    int tile[2], unit[2], tile_shift[2], unit_shift[2], workers[2];
+    int least[2];       // units that are worth a worker; 0: all units over `parts`
+    uint32_t parts[2];  // of the key heads of all requests (groups), a few each
     float* slots[2];   // parts of split segments: of the requests' own keys, of the shared ones
     float* dense[2];   // with shared prefixes: the parts of whole segments, [Hkv][rows G][D], then maxima and sums
     AttendEnd* ends;   // [workers[0]]
