@@ -568,7 +568,8 @@ int dspark_cache_append(const dspark_cache_t* cache, int layer, const void* k_ne
  * Scores, the softmax and the sums are held in fp32; the weights, relative to a running
  * maximum (and at most 2^8, since it follows in steps), are rounded to the cache's dtype for
  * the second product, and out once.  A position that a row does not see has no influence on
- * it, whatever its K and V hold.
+ * it, whatever its K and V hold.  Where a row does see a value of V that is not finite, its
+ * result there is not finite either; an infinity whose weight rounds to zero may make it NaN.
  *   q, out   [n_rows] rows of [H, head_dim], q_stride and out_stride elements apart
  *            (multiples of 8; 16-byte aligned), in the cache's dtype; they must not alias
  *   lse      [n_rows, H] fp32 output, or NULL
