@@ -335,8 +335,10 @@ __device__ void check_prefix(const AttendArgs& a, const Work& q) {
 }
 
 // Adds a part (maximum pm and sum pl of one column, x and y eight of its values) to a running one.
+// A part that saw no key has a sum of zero.  Its maximum does not say so: scores that are all NaN
+// leave it at -inf too, and their part has to make the result NaN.
 __device__ __forceinline__ void join(float& m, float& l, float (&acc)[8], float pm, float pl, float4 x, float4 y) {
-    if (pm == -kInf) return;
+    if (pl == 0.f) return;
     const float mx = fmaxf(m, pm);
     const float s0 = __builtin_amdgcn_exp2f(m - mx), s1 = __builtin_amdgcn_exp2f(pm - mx);
     m = mx;

@@ -570,6 +570,9 @@ int dspark_cache_append(const dspark_cache_t* cache, int layer, const void* k_ne
  * the second product, and out once.  A position that a row does not see has no influence on
  * it, whatever its K and V hold.  Where a row does see a value of V that is not finite, its
  * result there is not finite either; an infinity whose weight rounds to zero may make it NaN.
+ * A score that is NaN or +infinity (by what is not finite in q or in a K that the row sees)
+ * makes the row's result of that head and its lse NaN; a score of -infinity weighs nothing, and
+ * where all of a row's are -infinity the result is zero and lse -inf.
  *   q, out   [n_rows] rows of [H, head_dim], q_stride and out_stride elements apart
  *            (multiples of 8; 16-byte aligned), in the cache's dtype; they must not alias
  *   lse      [n_rows, H] fp32 output, or NULL
