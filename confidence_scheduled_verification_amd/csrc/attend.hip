@@ -99,6 +99,29 @@ __device__ int group_of(const AttendArgs& a, int r) {
     return lo > 0 && r < a.group_off[lo] ? lo - 1 : -1;
 }
 
+// A group's rows [start, start + n) and the keys [0, ke) that they share; ke = 0 for none.
+// The rows end where the buffer does: a request of the group whose rows pass it is left out
+// by itself.
+struct Group {
+    int start, n, ke;
+};
+
+__device__ Group shared_of(const AttendArgs& a, int g, uint32_t& bad) {
+    Group q{0, 0, 0};
+    const int r0 = a.group_off[g], r1 = a.group_off[g + 1], sp = a.shared_pages[g];
+    if (r0 < 0 || r1 < r0 || r1 > a.R || sp < 0 || sp > a.shared_width) {
+        bad = kStatusBadRow;
+        return q;
+    }
+    const long long all = a.rows, s0 = (long long)a.offsets[r0] + (long long)a.lead * r0,
+                    s1 = (long long)a.offsets[r1] + (long long)a.lead * r1;
+    const long long from = min(max(s0, 0ll), all), to = min(max(s1, from), all);
+    q.start = (int)from;
+    q.n = (int)(to - from);
+    q.ke = sp * a.page;
+    return q;
+}
+
 __device__ int request_of(const AttendArgs& a, int r, Request& q, uint32_t& bad) {
     const int o = a.offsets[r];
     const long long n = (long long)a.offsets[r + 1] - o + a.lead, start = (long long)o + (long long)a.lead * r;
@@ -120,39 +143,19 @@ __device__ int request_of(const AttendArgs& a, int r, Request& q, uint32_t& bad)
     if (a.n_groups) {
         q.group = group_of(a, r);
         if (q.group >= 0) {
-            const int sp = a.shared_pages[q.group];
-            if (sp < 0 || sp > a.shared_width || (long long)sp * a.page > q.ln) {
-                bad = kStatusBadRow;
-                return 0;
+            // Where the group does not fit, or its rows are not around this request's (as offsets
+            // that fall have it), the request reads its own table, which holds those keys too.
+            const Group g = shared_of(a, q.group, bad);
+            if (q.start >= g.start && q.start + q.n <= g.start + g.n) {
+                if (g.ke > q.ln) {
+                    bad = kStatusBadRow;
+                    return 0;
+                }
+                q.kb = g.ke;
             }
-            q.kb = sp * a.page;
         }
     }
     return 1;
-}
-
-// A group's rows [start, start + n) and the keys [0, ke) that they share; ke = 0 for none.
-struct Group {
-    int start, n, ke;
-};
-
-__device__ Group shared_of(const AttendArgs& a, int g, uint32_t& bad) {
-    Group q{0, 0, 0};
-    const int r0 = a.group_off[g], r1 = a.group_off[g + 1], sp = a.shared_pages[g];
-    if (r0 < 0 || r1 < r0 || r1 > a.R || sp < 0 || sp > a.shared_width) {
-        bad = kStatusBadRow;
-        return q;
-    }
-    const long long s0 = (long long)a.offsets[r0] + (long long)a.lead * r0,
-                    s1 = (long long)a.offsets[r1] + (long long)a.lead * r1;
-    if (s0 < 0 || s1 < s0 || s1 > a.rows) {
-        bad = kStatusBadRow;
-        return q;
-    }
-    q.start = (int)s0;
-    q.n = (int)(s1 - s0);
-    q.ke = sp * a.page;
-    return q;
 }
 
 template <int kTile>
@@ -1189,10 +1192,9 @@ __global__ __launch_bounds__(kT) void attend_join_shared_kernel(AttendArgs a) {
     Group g{};
     uint32_t g_u0 = 0;
     if (q.kb > 0) {
+        if (common_units == 0) return;  // groups out of all bounds
         g = shared_of(a, q.group, bad);
         g_u0 = a.cum[1][q.group] * a.Hkv;
-        // (rows outside the group's, as offsets that fall would have it, have no part there)
-        if (q.start < g.start || q.start + q.n > g.start + g.n || common_units == 0) g.ke = 0;
     }
     const int end = min((blockIdx.z + 1) * kJoinItems, (uint32_t)(q.n * a.G * chunks));
     for (int e = blockIdx.z * kJoinItems + threadIdx.x; e < end; e += kT) {

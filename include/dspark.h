@@ -589,9 +589,12 @@ int dspark_cache_append(const dspark_cache_t* cache, int layer, const void* k_ne
  * Rows that see nothing (vacant requests) get zeros and lse -inf; so do those of a request
  * whose length fits neither its table nor its group (DSPARK_STATUS_BAD_ROW).  A request
  * with n_r < 0 or > max_new or rows outside the tensors, or from row R * max_new on, is left
- * out with the same status, and rows that belong to no request stay as they are.  So do all
- * rows where offsets that fall and rise make more work than 32-bit numbers hold.  Page ids outside the cache are not
- * read: their tokens are left out (DSPARK_STATUS_BAD_PAGE).  Results are the same in every
+ * out with the same status, and rows that belong to no request stay as they are.  A group whose
+ * group_off do not lie in 0 .. R or fall, or whose shared_pages do not lie in 0 .. shared_width,
+ * counts as none (DSPARK_STATUS_BAD_ROW): its requests read all of their own.  Where offsets or
+ * group_off that fall and rise make more work than 32-bit numbers hold, the rows concerned (all,
+ * or those behind a prefix) stay as they are (DSPARK_STATUS_BAD_ROW).  Page ids outside the cache
+ * are not read: their tokens are left out (DSPARK_STATUS_BAD_PAGE).  Results are the same in every
  * run.  More rows, heads and tokens than 32-bit numbers of work units hold return
  * DSPARK_EUNSUPPORTED.
  */
