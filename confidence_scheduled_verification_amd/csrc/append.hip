@@ -67,6 +67,7 @@ __global__ __launch_bounds__(kT) void append_kernel(AppendArgs a) {
         if (blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) raise_status(a.status, kStatusBadRow);
         return;
     }
+    if (n == 0) return;  // (the block that the tokens kept end in is not this step's)
     const int shift = a.page_shift;
     const int row8 = (lane >> 5) * 4 + (lane >> 4 & 1) * 2 + (lane & 1);  // token of the eight; afterwards dim of the eight
     const int c8 = lane >> 1 & 7;                                        // eight dims of the 64
