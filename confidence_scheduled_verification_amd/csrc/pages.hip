@@ -16,6 +16,8 @@
 // tokens, 8 heads of 128 and 8 layers each (268 MB): the copy is 50 of 66 us, 5.4 TB/s; 24 whole
 // copies (710 MB) 133 of 157 us, 5.3; 6000 of 12000 pages made compact (3.1 GB) 605 of 634 us, 5.2.
 // A large library copy reaches 5.5.
+#include <algorithm>
+
 #include "cache.h"
 #include "common.h"
 
@@ -241,18 +243,22 @@ __device__ void drop_pages(const dspark_cache_t& c, int row, int first, uint32_t
     if (bad) raise_status(status, kStatusBadPage);
 }
 
+// A wave a row; more rows than kTrimBlocks hold are taken in rounds, since a grid has at most
+// 2^32 threads and a table may have 2^31 rows.
+constexpr int kTrimBlocks = 1 << 20;
+
 __global__ __launch_bounds__(kT) void trim_kernel(dspark_cache_t c, const int32_t* rows, int n, const int32_t* keep,
                                                   uint32_t* status) {
-    const int i = blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (i >= n) return;
-    const int row = rows ? rows[i] : i;
-    const int kp = keep ? keep[i] : 0;
-    if (row < 0 || row >= c.rows) {
-        if ((threadIdx.x & 63) == 0) raise_status(status, kStatusBadRow);
-        return;
+    for (long long i = (long long)blockIdx.x * 4 + (threadIdx.x >> 6); i < n; i += (long long)gridDim.x * 4) {
+        const int row = rows ? rows[i] : (int)i;
+        const int kp = keep ? keep[i] : 0;
+        if (row < 0 || row >= c.rows) {
+            if ((threadIdx.x & 63) == 0) raise_status(status, kStatusBadRow);
+            continue;
+        }
+        drop_pages(c, row, pages_of(kp > 0 ? kp : 0, c.page_size), status);
+        if ((threadIdx.x & 63) == 0) atomicMin(&c.len[row], kp < 0 ? -1 : kp);
     }
-    drop_pages(c, row, pages_of(kp > 0 ? kp : 0, c.page_size), status);
-    if ((threadIdx.x & 63) == 0) atomicMin(&c.len[row], kp < 0 ? -1 : kp);
 }
 
 __global__ __launch_bounds__(kT) void commit_kernel(dspark_cache_t c, const int32_t* accept_len, int lead, int R,
@@ -504,7 +510,8 @@ hipError_t launch_reserve(const dspark_cache_t& c, const int32_t* offsets, int l
 
 hipError_t launch_trim(const dspark_cache_t& c, const int32_t* rows, int n, const int32_t* keep, uint32_t* status,
                        hipStream_t s) {
-    hipLaunchKernelGGL(trim_kernel, dim3((n + 3) / 4), dim3(kT), 0, s, c, rows, n, keep, status);
+    const int blocks = (int)std::min(((long long)n + 3) / 4, (long long)kTrimBlocks);
+    hipLaunchKernelGGL(trim_kernel, dim3(blocks), dim3(kT), 0, s, c, rows, n, keep, status);
     return hipGetLastError();
 }
 

@@ -29,3 +29,22 @@ def test_a_request_without_rows_appends_nothing(lead):
     assert int(status.item()) == 0
     for a, b in zip(before, (c.k, c.v)):
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def test_trim_of_as_many_rows_as_a_grid_has_threads():
+    # more rows than 2^32 threads hold at a wave a row
+    print("trim, many rows", flush=True)
+    rows = (1 << 26) + 5
+    c = B.PagedCache(1, 64, 16, 1, 64, B.DSPARK_BF16, rows, 1, device=cu.DEV, data=False)
+    c.len.zero_()
+    held = [0, 3, (1 << 26) - 1, 1 << 26, rows - 1]
+    for p, r in enumerate(held):
+        c.table[r, 0], c.len[r], c.ref[p] = p, 9, 1
+    keep = torch.full((rows,), 7, dtype=torch.int32, device=cu.DEV)
+    keep[3] = keep[rows - 1] = 0
+    status = torch.zeros(1, dtype=torch.int32, device=cu.DEV)
+    B.dspark_pages_trim(c, None, keep, status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    assert c.table[held, 0].tolist() == [0, -1, 2, 3, -1] and c.len[held].tolist() == [7, 0, 7, 7, 0]
+    assert c.ref[:5].tolist() == [1, 0, 1, 1, 0] and int((c.len != 0).sum()) == 3
