@@ -44,7 +44,7 @@ EXPORTS = ["dspark_last_error", "dspark_version", "dspark_workspace_bytes", "dsp
            "dspark_step", "dspark_step_sized", "dspark_step_static", "dspark_schedule", "dspark_accept_greedy", "dspark_set_timing_events",
            "dspark_force_monotone", "dspark_profile_shapes", "dspark_build_cost_table", "dspark_set_launch_mode",
            "dspark_get_launch_mode", "dspark_pages_workspace_bytes", "dspark_pages_reserve", "dspark_pages_trim",
-           "dspark_pages_commit", "dspark_pages_fork", "dspark_pages_compact", "dspark_cache_append",
+           "dspark_pages_commit", "dspark_pages_commit_granted", "dspark_pages_fork", "dspark_pages_compact", "dspark_cache_append",
            "dspark_cache_attend_workspace_bytes", "dspark_cache_attend"]
 
 # int fn(int shape, void* user, void* stream)
@@ -121,6 +121,7 @@ def lib():
         L.dspark_pages_reserve.argtypes = [p, p, i, i, p, p, p, sz, p]
         L.dspark_pages_trim.argtypes = [p, p, i, p, p, p]
         L.dspark_pages_commit.argtypes = [p, p, i, i, p, p]
+        L.dspark_pages_commit_granted.argtypes = [p, p, p, i, i, p, p]
         L.dspark_pages_fork.argtypes = [p, p, p, i, i, p, p, p, sz, p]
         L.dspark_pages_compact.argtypes = [p, p, p, p, p, sz, p]
         L.dspark_cache_append.argtypes = [p, i, p, i64, p, i64, i, p, i, i, i, p, p]
@@ -566,12 +567,16 @@ def dspark_pages_trim(cache: PagedCache, rows=None, keep=None, status=None, stre
     _check(lib().dspark_pages_trim(cache._ref, _p(rows), n, _p(keep), _p(status), st))
 
 
-def dspark_pages_commit(cache: PagedCache, accept_len, lead: int, status=None, stream=None):
-    """After dspark_accept_greedy: the accepted rows stay, the pages past them are let go."""
+def dspark_pages_commit(cache: PagedCache, accept_len, lead: int, status=None, stream=None, granted=None):
+    """After dspark_accept_greedy: the accepted rows stay, the pages past them are let go.  Requests
+    that `granted` (dspark_pages_reserve's) says were refused stay as they are."""
     if accept_len.dim() != 1 or accept_len.shape[0] > cache.rows:
         raise ValueError(f"dspark_pages_commit: accept_len must be [R] with R at most {cache.rows}")
-    st = _on(cache, "dspark_pages_commit", stream, (accept_len,), (status,))
-    _check(lib().dspark_pages_commit(cache._ref, _p(accept_len), lead, accept_len.shape[0], _p(status), st))
+    R = accept_len.shape[0]
+    if granted is not None:
+        _shape(granted, (R,), "dspark_pages_commit: granted")
+    st = _on(cache, "dspark_pages_commit", stream, (accept_len, granted), (status,))
+    _check(lib().dspark_pages_commit_granted(cache._ref, _p(accept_len), _p(granted), lead, R, _p(status), st))
 
 
 def dspark_pages_fork(cache: PagedCache, src, dst, forked, ws, deep: bool = False, status=None, stream=None):

@@ -34,8 +34,9 @@ hipError_t launch_reserve(const dspark_cache_t& c, const int32_t* offsets, int l
                           uint32_t* status, int32_t* ws, hipStream_t s);
 hipError_t launch_trim(const dspark_cache_t& c, const int32_t* rows, int n, const int32_t* keep, uint32_t* status,
                        hipStream_t s);
-hipError_t launch_commit(const dspark_cache_t& c, const int32_t* accept_len, int lead, int R, uint32_t* status,
-                         hipStream_t s);
+// granted: NULL where every request of the step was served
+hipError_t launch_commit(const dspark_cache_t& c, const int32_t* accept_len, const int32_t* granted, int lead, int R,
+                         uint32_t* status, hipStream_t s);
 hipError_t launch_fork(const dspark_cache_t& c, const int32_t* src, const int32_t* dst, int n, int deep,
                        int32_t* forked, uint32_t* status, int32_t* ws, int num_cu, hipStream_t s);
 hipError_t launch_compact(const dspark_cache_t& c, int32_t* page_map, int32_t* n_live, uint32_t* status, int32_t* ws,

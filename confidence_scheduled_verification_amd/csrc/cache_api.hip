@@ -107,14 +107,19 @@ int dspark_pages_trim(const dspark_cache_t* c, const int32_t* rows, int n, const
     return done(dspark::launch_trim(*c, rows, n, keep, status, (hipStream_t)stream), who);
 }
 
-int dspark_pages_commit(const dspark_cache_t* c, const int32_t* accept_len, int lead, int R, uint32_t* status,
-                        void* stream) {
+int dspark_pages_commit_granted(const dspark_cache_t* c, const int32_t* accept_len, const int32_t* granted, int lead,
+                                int R, uint32_t* status, void* stream) {
     const char* who = "pages_commit";
     int rc = check_pages(c, who);
     if (rc != DSPARK_OK || (rc = check_requests(c, R, lead, who)) != DSPARK_OK) return rc;
     if (R == 0) return DSPARK_OK;
     if (!accept_len) return fail(DSPARK_EINVAL, "%s: accept_len is NULL", who);
-    return done(dspark::launch_commit(*c, accept_len, lead, R, status, (hipStream_t)stream), who);
+    return done(dspark::launch_commit(*c, accept_len, granted, lead, R, status, (hipStream_t)stream), who);
+}
+
+int dspark_pages_commit(const dspark_cache_t* c, const int32_t* accept_len, int lead, int R, uint32_t* status,
+                        void* stream) {
+    return dspark_pages_commit_granted(c, accept_len, nullptr, lead, R, status, stream);
 }
 
 int dspark_pages_fork(const dspark_cache_t* c, const int32_t* src, const int32_t* dst, int n, int deep,

@@ -261,12 +261,12 @@ __global__ __launch_bounds__(kT) void trim_kernel(dspark_cache_t c, const int32_
     }
 }
 
-__global__ __launch_bounds__(kT) void commit_kernel(dspark_cache_t c, const int32_t* accept_len, int lead, int R,
-                                                    uint32_t* status) {
+__global__ __launch_bounds__(kT) void commit_kernel(dspark_cache_t c, const int32_t* accept_len,
+                                                    const int32_t* granted, int lead, int R, uint32_t* status) {
     const int r = blockIdx.x * 4 + (threadIdx.x >> 6);
     if (r >= R) return;
     const int ln = c.len[r];
-    if (ln < 0) return;
+    if (ln < 0 || (granted && granted[r] == 0)) return;
     const int acc = accept_len[r];
     const long long kp = (long long)ln + lead + acc;
     const long long first = (kp + c.page_size - 1) / c.page_size;
@@ -515,9 +515,9 @@ hipError_t launch_trim(const dspark_cache_t& c, const int32_t* rows, int n, cons
     return hipGetLastError();
 }
 
-hipError_t launch_commit(const dspark_cache_t& c, const int32_t* accept_len, int lead, int R, uint32_t* status,
-                         hipStream_t s) {
-    hipLaunchKernelGGL(commit_kernel, dim3((R + 3) / 4), dim3(kT), 0, s, c, accept_len, lead, R, status);
+hipError_t launch_commit(const dspark_cache_t& c, const int32_t* accept_len, const int32_t* granted, int lead, int R,
+                         uint32_t* status, hipStream_t s) {
+    hipLaunchKernelGGL(commit_kernel, dim3((R + 3) / 4), dim3(kT), 0, s, c, accept_len, granted, lead, R, status);
     return hipGetLastError();
 }
 

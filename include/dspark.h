@@ -441,7 +441,8 @@ int dspark_accept_greedy(const int32_t* ver_tokens, const int32_t* offsets, cons
  *   dspark_cache_append    one layer's K and V of the rows into them;
  *   dspark_cache_attend    one layer's attention of the rows;
  *   dspark_pages_commit    after the acceptance: the accepted rows stay, the pages past
- *                          them are let go;
+ *                          them are let go (dspark_pages_commit_granted where requests may
+ *                          have been refused pages);
  *   dspark_pages_trim      rows cut back or freed;
  *   dspark_pages_fork      a request's cache continued by another one;
  *   dspark_pages_compact   the live pages moved to the front.
@@ -511,10 +512,20 @@ int dspark_pages_trim(const dspark_cache_t* cache, const int32_t* rows, int n, c
  * After the acceptance: request r keeps its first lead + accept_len[r] rows of the step
  * (accept_len from dspark_accept_greedy), len[r] += lead + accept_len[r], and the pages
  * past them leave its row as in dspark_pages_trim.  Vacant rows stay as they are; so does
- * one whose accept_len is negative or reaches past its pages (DSPARK_STATUS_BAD_ROW).
+ * one whose accept_len is negative or reaches past its pages (DSPARK_STATUS_BAD_ROW).  For
+ * steps whose requests were all served: a request that dspark_pages_reserve refused may have
+ * room for some of its rows, and they would be kept though nothing was written there.
  */
 int dspark_pages_commit(const dspark_cache_t* cache, const int32_t* accept_len, int lead, int R, uint32_t* status,
                         void* stream);
+
+/*
+ * The same for a step of which some requests may have been refused: those with granted[r] == 0
+ * stay as they are, whatever their accept_len, and set no status.
+ *   granted  [R] int32 as dspark_pages_reserve wrote it, or NULL (all served)
+ */
+int dspark_pages_commit_granted(const dspark_cache_t* cache, const int32_t* accept_len, const int32_t* granted, int lead,
+                                int R, uint32_t* status, void* stream);
 
 /*
  * Forks: table row dst[i], which holds no pages (len <= 0), continues row src[i]: it

@@ -111,10 +111,10 @@ def trim(table, length, ref, rows, keep, page):
     return status
 
 
-def commit(table, length, ref, accept, lead, page):
+def commit(table, length, ref, accept, lead, page, granted=None):
     status = 0
     for r, a in enumerate(accept):
-        if length[r] < 0:
+        if length[r] < 0 or (granted is not None and not granted[r]):
             continue
         kept = length[r] + lead + a
         first = _pages(kept, page)

@@ -165,3 +165,23 @@ def test_binding_refuses():
         B.dspark_pages_commit(c, off[:3].long(), 1)
     with pytest.raises(ValueError, match="granted must be"):
         B.dspark_pages_reserve(c, off, 1, off, ws)
+
+
+def test_commit_with_granted_refuses():
+    L, p = B.lib(), _fake()
+    for kw, rc in BOOKS:
+        assert L.dspark_pages_commit_granted(_cache(**kw), p, p, 1, 4, None, None) == rc, kw
+    c = _cache(k=None, v=None)
+    assert L.dspark_pages_commit_granted(None, p, p, 1, 4, None, None) == -1
+    assert L.dspark_pages_commit_granted(c, None, p, 1, 4, None, None) == -1
+    assert L.dspark_pages_commit_granted(c, p, p, 1, 9, None, None) == -2
+    assert L.dspark_pages_commit_granted(c, p, p, 3, 4, None, None) == -2
+    assert L.dspark_pages_commit_granted(c, None, None, 1, 0, None, None) == 0
+    books = B.PagedCache(1, 4, 16, 1, 64, B.DSPARK_F16, 3, 5, device="cpu", data=False)
+    n = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="granted must be"):
+        B.dspark_pages_commit(books, n, 1, granted=n[:2])
+    with pytest.raises(ValueError, match="contiguous int32"):
+        B.dspark_pages_commit(books, n, 1, granted=n.float())
+    with pytest.raises(ValueError, match="not the current GPU"):
+        B.dspark_pages_commit(books, n, 1, granted=n)

@@ -415,3 +415,80 @@ def test_a_shared_page_is_not_written_to():
     assert int(status.item()) == B.STATUS_BAD_PAGE
     for a, b in zip(before, (c.k, c.v)):
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def test_refused_requests_are_not_committed():
+    # a step in which one request's rows pass its table and another one's find no pages, while the
+    # acceptance counted their (meaningless) tokens: both stay as they were, the others go on
+    _say("commit, refused requests")
+    rng = np.random.default_rng(61)
+    R, page, width, lead = 5, 16, 10, 1
+    st = cu.State(rng, 1, 22, page, 2, 64, "bf16", R, width)
+    st.len = [155, 30, 33, -1, 20]
+    for r, n in enumerate((10, 2, 3, 0, 2)):
+        st.give(r, n)
+        st.put(0, st.table[r], 0, max(st.len[r], 0))
+    c = st.upload()
+    rows = [8, 5, 100, 2, 12]
+    offsets = np.concatenate([[0], np.cumsum(np.asarray(rows) - lead)]).tolist()
+    off, n = cu.i32(offsets), sum(rows)
+    granted, status = torch.zeros(R, dtype=torch.int32, device=cu.DEV), _status()
+    ws = B.pages_workspace(c, R)
+    B.dspark_pages_reserve(c, off, lead, granted, ws, status)
+    kv = torch.randn((2, n, 2, 64), device=cu.DEV).to(torch.bfloat16)
+    B.dspark_cache_append(c, 0, kv[0], kv[1], off, lead, max(rows), status)
+    torch.cuda.synchronize()
+    want, w_st = oc.reserve(st.table, st.len, st.ref, offsets, lead, page)
+    assert want == [0, 1, 0, 0, 1] == granted.cpu().tolist() and w_st == B.STATUS_NO_PAGES
+    status.zero_()
+    accept = [4, 2, 7, 0, 11]   # requests 0 and 2 have room for as many
+    B.dspark_pages_commit(c, cu.i32(accept), lead, status, granted=granted)
+    torch.cuda.synchronize()
+    assert int(status.item()) == oc.commit(st.table, st.len, st.ref, accept, lead, page, want) == 0
+    assert st.len == [155, 33, 33, -1, 32]
+    st.assert_books()
+    accept = [3, -1, 2_000_000_000, 5, 60]   # a refused request's count is not looked at
+    B.dspark_pages_commit(c, cu.i32(accept), lead, status, granted=granted)
+    torch.cuda.synchronize()
+    assert int(status.item()) == oc.commit(st.table, st.len, st.ref, accept, lead, page, want) == B.STATUS_BAD_ROW
+    st.assert_books()
+
+
+def test_steps_of_a_cache_that_runs_out():
+    # reserve and commit step after step in a captured graph, with granted handed on, until most
+    # requests are refused
+    _say("books, running out")
+    st, rng = _books(62, 24, 6, 90, fill=0.8)
+    R = 24
+    off, accept = cu.i32([0] * (R + 1)), cu.i32([0] * R)
+    granted, status, ws = torch.zeros(R, dtype=torch.int32, device=cu.DEV), _status(), B.pages_workspace(st.cache, R)
+
+    def step():
+        B.dspark_pages_reserve(st.cache, off, 1, granted, ws, status)
+        B.dspark_pages_commit(st.cache, accept, 1, status, granted=granted)
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        step()
+    s.synchronize()
+    g_, _ = oc.reserve(st.table, st.len, st.ref, [0] * (R + 1), 1, 16)
+    oc.commit(st.table, st.len, st.ref, [0] * R, 1, 16, g_)
+    st.assert_books()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    refused = 0
+    for _ in range(8):
+        drafts = rng.integers(0, 8, R)
+        offsets, acc = np.concatenate([[0], np.cumsum(drafts)]).tolist(), [int(rng.integers(0, d + 1)) for d in drafts]
+        off.copy_(cu.i32(offsets))
+        accept.copy_(cu.i32(acc))
+        status.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        g_, s0 = oc.reserve(st.table, st.len, st.ref, offsets, 1, 16)
+        s1 = oc.commit(st.table, st.len, st.ref, acc, 1, 16, g_)
+        assert granted.cpu().tolist() == g_ and int(status.item()) == s0 | s1
+        st.assert_books()
+        refused += sum(not x and n >= 0 for x, n in zip(g_, st.len))
+    assert refused
