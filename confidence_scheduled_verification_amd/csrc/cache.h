@@ -65,6 +65,9 @@ hipError_t launch_append(const AppendArgs& a, hipStream_t s);
 constexpr int kAttendMinTile = 32;  // columns (row, head of the group) of one tile, at least
 constexpr int kAttendMinUnit = 64;  // keys of one unit, at least
 constexpr int kAttendMaxCus = 256;  // compute units that a launch uses
+// Tokens of one table row, at most: positions are 32-bit numbers, and the kernels look up to 64
+// stages of 64 keys and a unit past the last one before they compare.
+constexpr long long kAttendMaxTokens = (1ll << 31) - 8192;
 
 // A worker's first segment, where an earlier worker began it (units = 0: it did not): the
 // workers that have parts of it, and its columns.

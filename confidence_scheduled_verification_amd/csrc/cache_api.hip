@@ -207,9 +207,9 @@ int dspark_cache_attend(const dspark_cache_t* c, int layer, const void* q, int64
     const long long shared_units = (long long)shared_width * c->page_size / dspark::kAttendMinUnit + 1;
     if ((long long)rows * H > INT32_MAX || tiles > 65535 ||
         std::min(tiles * R, row_tiles / c->n_kv_heads + R) * c->n_kv_heads * units > INT32_MAX ||
-        (long long)c->width * c->page_size > INT32_MAX ||
+        (long long)c->width * c->page_size > dspark::kAttendMaxTokens ||
         (n_groups && ((row_tiles + (long long)n_groups * c->n_kv_heads) * shared_units > INT32_MAX ||
-                      (long long)shared_width * c->page_size > INT32_MAX)))
+                      (long long)shared_width * c->page_size > dspark::kAttendMaxTokens)))
         return fail(DSPARK_EUNSUPPORTED, "%s: %d rows of %d heads over up to %lld tokens are too many for one call", who,
                     n_rows, H, (long long)c->width * c->page_size);
     if ((rc = check_ws(ws, ws_bytes, dspark_cache_attend_workspace_bytes(R, H, c->head_dim, max_new, n_groups), who)) !=

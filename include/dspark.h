@@ -606,8 +606,8 @@ int dspark_cache_append(const dspark_cache_t* cache, int layer, const void* k_ne
  * group_off that fall and rise make more work than 32-bit numbers hold, the rows concerned (all,
  * or those behind a prefix) stay as they are (DSPARK_STATUS_BAD_ROW).  Page ids outside the cache
  * are not read: their tokens are left out (DSPARK_STATUS_BAD_PAGE).  Results are the same in every
- * run.  More rows, heads and tokens than 32-bit numbers of work units hold return
- * DSPARK_EUNSUPPORTED.
+ * run.  More rows, heads and tokens than 32-bit numbers of work units hold, and tables or
+ * prefixes of more than 2^31 - 8192 tokens (width * page_size), return DSPARK_EUNSUPPORTED.
  */
 size_t dspark_cache_attend_workspace_bytes(int R, int H, int head_dim, int max_new, int n_groups);
 int dspark_cache_attend(const dspark_cache_t* cache, int layer, const void* q, int64_t q_stride, int n_rows, int H,

@@ -185,3 +185,19 @@ def test_commit_with_granted_refuses():
         B.dspark_pages_commit(books, n, 1, granted=n.float())
     with pytest.raises(ValueError, match="not the current GPU"):
         B.dspark_pages_commit(books, n, 1, granted=n)
+
+
+def test_attend_refuses_tables_that_32_bit_positions_do_not_hold():
+    # (no workspace, so that a call that passes the checks of sizes still launches nothing)
+    L, p = B.lib(), _fake()
+
+    def call(width, page, shared_width=0):
+        groups = (1, p, p, shared_width, p) if shared_width else (0, None, None, 0, None)
+        return L.dspark_cache_attend(_cache(width=width, page_size=page, rows=1), 0, p, 256, 4, 4, p, 1, 1, 8, 0.125, *groups,
+                                     p, 256, None, None, None, 0, None)
+    for page in (16, 256):
+        most = ((1 << 31) - 8192) // page
+        assert call(most, page) == -4
+        assert call(most + 1, page) == call((1 << 31) // page - 1, page) == -3
+        assert call(1, page, most) == -4
+        assert call(1, page, most + 1) == call(1, page, (1 << 31) // page - 1) == -3
