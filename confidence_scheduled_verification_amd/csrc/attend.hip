@@ -1175,8 +1175,8 @@ __global__ __launch_bounds__(kT) void attend_join_kernel(AttendArgs a) {
 }
 
 // Joins everything where prefixes are shared: a workgroup the columns of a request with one
-// key head (up to kJoinItems of eight dims), from its own launch and its group's.
-constexpr int kJoinItems = 4 * kT;
+// key head (up to kAttendJoinItems of eight dims), from its own launch and its group's.
+static_assert(kAttendJoinItems % kT == 0, "as many items to every thread");
 template <class E>
 __global__ __launch_bounds__(kT) void attend_join_shared_kernel(AttendArgs a) {
     const int r = blockIdx.x, h = blockIdx.y, chunks = a.D / 8;
@@ -1196,8 +1196,8 @@ __global__ __launch_bounds__(kT) void attend_join_shared_kernel(AttendArgs a) {
         g = shared_of(a, q.group, bad);
         g_u0 = a.cum[1][q.group] * a.Hkv;
     }
-    const int end = min((blockIdx.z + 1) * kJoinItems, (uint32_t)(q.n * a.G * chunks));
-    for (int e = blockIdx.z * kJoinItems + threadIdx.x; e < end; e += kT) {
+    const int end = min((blockIdx.z + 1) * kAttendJoinItems, (uint32_t)(q.n * a.G * chunks));
+    for (int e = blockIdx.z * kAttendJoinItems + threadIdx.x; e < end; e += kT) {
         const int c = e / chunks, c8 = e % chunks;
         float m = -kInf, l = 0.f, acc[8] = {};
         if (q.kb == 0) {  // its whole tiles are done already
@@ -1234,7 +1234,7 @@ hipError_t run(const AttendArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
     if (a.n_groups)
         hipLaunchKernelGGL(attend_join_shared_kernel<E>,
-                           dim3(a.R, a.Hkv, ((size_t)a.max_new * a.G * (D / 8) + kJoinItems - 1) / kJoinItems), dim3(kT), 0,
+                           dim3(a.R, a.Hkv, ((size_t)a.max_new * a.G * (D / 8) + kAttendJoinItems - 1) / kAttendJoinItems), dim3(kT), 0,
                            s, a);
     else
         hipLaunchKernelGGL(attend_join_kernel<E>, dim3(a.workers[0], a.tile[0] / (kT / (D / 8))), dim3(kT), 0, s, a);
@@ -1284,7 +1284,7 @@ void attend_ws_layout(AttendArgs& a, void* ws) {
     a.dense[1] = (float*)take(dense_bytes(a.R, a.H, a.D, a.max_new));
 }
 
-hipError_t launch_attend(AttendArgs a, int cus, hipStream_t s) {
+void attend_forms(AttendArgs& a, int cus) {
     // The many-rows form where a request (a group) may have more columns than kWideFrom; else
     // workers of two waves where it may have more than the 32 of one.
     const int wide = a.D == 64 ? Wide<64>::kTile : a.D == 128 ? Wide<128>::kTile : Wide<256>::kTile;
@@ -1302,6 +1302,9 @@ hipError_t launch_attend(AttendArgs a, int cus, hipStream_t s) {
         a.tile_shift[set] = __builtin_ctz(a.tile[set]);
         a.unit_shift[set] = __builtin_ctz(a.unit[set]);
     }
+}
+
+hipError_t launch_attend(const AttendArgs& a, hipStream_t s) {
     return a.dtype == DSPARK_F16 ? run_dim<F16>(a, s) : run_dim<Bf16>(a, s);
 }
 

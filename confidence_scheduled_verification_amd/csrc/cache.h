@@ -62,9 +62,8 @@ hipError_t launch_append(const AppendArgs& a, hipStream_t s);
 // workers where it has to be.  A worker leaves a split segment's part in one of its two
 // slots: slot 0 for the segment that an earlier worker began, slot 1 for the one that it
 // begins and does not end.
-constexpr int kAttendMinTile = 32;  // columns (row, head of the group) of one tile, at least
-constexpr int kAttendMinUnit = 64;  // keys of one unit, at least
 constexpr int kAttendMaxCus = 256;  // compute units that a launch uses
+constexpr int kAttendJoinItems = 1024;  // eight dims of a column each: what a joining workgroup takes
 // Tokens of one table row, at most: positions are 32-bit numbers, and the kernels look up to 64
 // stages of 64 keys and a unit past the last one before they compare.
 constexpr long long kAttendMaxTokens = (1ll << 31) - 8192;
@@ -93,7 +92,8 @@ struct AttendArgs {
     uint16_t* out;
     float* lse;
     uint32_t* status;
-    // the launches' forms: [0] the requests' own keys, [1] the shared ones
+    // the launches' forms (attend_forms): [0] the requests' own keys, [1] the shared ones;
+    // tile: columns (row, head of the group) taken together, unit: keys dealt to workers at a time
     int tile[2], unit[2], tile_shift[2], unit_shift[2], workers[2];
     int least[2];       // units that are worth a worker; 0: all units over `parts`
     uint32_t parts[2];  // of the key heads of all requests (groups), a few each
@@ -102,8 +102,9 @@ struct AttendArgs {
     AttendEnd* ends;   // [workers[0]]
     uint32_t* cum[2];  // with shared prefixes: running units (of one key head) of the requests, of the groups
 };
+void attend_forms(AttendArgs& a, int num_cu);  // from the sizes and the device
 size_t attend_ws_bytes(int R, int H, int D, int max_new, int n_groups);
 void attend_ws_layout(AttendArgs& a, void* ws);
-hipError_t launch_attend(AttendArgs a, int num_cu, hipStream_t s);
+hipError_t launch_attend(const AttendArgs& a, hipStream_t s);
 
 }  // namespace dspark

@@ -198,25 +198,36 @@ int dspark_cache_attend(const dspark_cache_t* c, int layer, const void* q, int64
         (rc = check_rows(out, out_stride, H, c->head_dim, who, "out")) != DSPARK_OK)
         return rc;
     if (!offsets) return fail(DSPARK_EINVAL, "%s: offsets is NULL", who);
-    const int G = H / c->n_kv_heads;
-    // rows past R * max_new belong to no request; the work is numbered with 32 bits
-    const int rows = (int)std::min<long long>(n_rows, (long long)R * max_new);
-    const long long tiles = ((long long)max_new * G + dspark::kAttendMinTile - 1) / dspark::kAttendMinTile;
-    const long long row_tiles = ((long long)rows * H + dspark::kAttendMinTile - 1) / dspark::kAttendMinTile;
-    const long long units = (long long)c->width * c->page_size / dspark::kAttendMinUnit + 1;
-    const long long shared_units = (long long)shared_width * c->page_size / dspark::kAttendMinUnit + 1;
-    if ((long long)rows * H > INT32_MAX || tiles > 65535 ||
-        std::min(tiles * R, row_tiles / c->n_kv_heads + R) * c->n_kv_heads * units > INT32_MAX ||
-        (long long)c->width * c->page_size > dspark::kAttendMaxTokens ||
-        (n_groups && ((row_tiles + (long long)n_groups * c->n_kv_heads) * shared_units > INT32_MAX ||
-                      (long long)shared_width * c->page_size > dspark::kAttendMaxTokens)))
+    const long long tokens = (long long)c->width * c->page_size, shared_tokens = (long long)shared_width * c->page_size;
+    dspark::AttendArgs a{};
+    a.lead = lead;
+    a.R = R;
+    a.rows = (int)std::min<long long>(n_rows, (long long)R * max_new);  // rows past those belong to no request
+    a.max_new = std::min(max_new, n_rows);                              // (more would not lie in the tensors)
+    a.H = H;
+    a.Hkv = c->n_kv_heads;
+    a.G = H / c->n_kv_heads;
+    a.D = c->head_dim;
+    a.n_groups = n_groups;
+    dspark::attend_forms(a, dspark::num_cu());
+    // The work is numbered with 32 bits: columns, the units of the requests' own keys and those of
+    // the groups', as many as these sizes allow, and the joining launch's grid.
+    const auto tiles = [&](int set, long long columns) { return (columns + a.tile[set] - 1) / a.tile[set]; };
+    const auto units = [&](int set, long long keys) { return (long long)a.Hkv * (keys / a.unit[set] + 1); };
+    const bool fits = (long long)a.rows * H <= INT32_MAX - 1023 && tokens <= dspark::kAttendMaxTokens &&
+                      std::min(R * tiles(0, (long long)a.max_new * a.G), R + tiles(0, (long long)a.rows * a.G)) *
+                              units(0, tokens) <= INT32_MAX;
+    const bool groups_fit =
+        !n_groups || (shared_tokens <= dspark::kAttendMaxTokens &&
+                      (n_groups + tiles(1, (long long)a.rows * a.G)) * units(1, shared_tokens) <= INT32_MAX &&
+                      (long long)a.max_new * a.G * (a.D / 8) <= 65535ll * dspark::kAttendJoinItems);
+    if (!fits || !groups_fit)
         return fail(DSPARK_EUNSUPPORTED, "%s: %d rows of %d heads over up to %lld tokens are too many for one call", who,
-                    n_rows, H, (long long)c->width * c->page_size);
+                    n_rows, H, tokens);
     if ((rc = check_ws(ws, ws_bytes, dspark_cache_attend_workspace_bytes(R, H, c->head_dim, max_new, n_groups), who)) !=
         DSPARK_OK)
         return rc;
     const size_t at = layer * layer_elems(c);
-    dspark::AttendArgs a{};
     a.q = (const uint16_t*)q;
     a.q_stride = q_stride;
     a.out_stride = out_stride;
@@ -225,21 +236,12 @@ int dspark_cache_attend(const dspark_cache_t* c, int layer, const void* q, int64
     a.table = c->table;
     a.len = c->len;
     a.offsets = offsets;
-    a.lead = lead;
-    a.R = R;
-    a.rows = rows;
-    a.max_new = max_new;
-    a.H = H;
-    a.Hkv = c->n_kv_heads;
-    a.G = G;
-    a.D = c->head_dim;
     a.dtype = c->dtype;
     a.page = c->page_size;
     a.page_shift = __builtin_ctz(c->page_size);
     a.n_pages = c->n_pages;
     a.width = c->width;
     a.scale_log2 = (float)((double)scale * 1.4426950408889634);
-    a.n_groups = n_groups;
     a.shared_width = shared_width;
     a.group_off = group_off;
     a.shared_table = shared_table;
@@ -248,7 +250,7 @@ int dspark_cache_attend(const dspark_cache_t* c, int layer, const void* q, int64
     a.lse = lse;
     a.status = status;
     dspark::attend_ws_layout(a, ws);
-    return done(dspark::launch_attend(a, dspark::num_cu(), (hipStream_t)stream), who);
+    return done(dspark::launch_attend(a, (hipStream_t)stream), who);
 }
 
 }  // extern "C"

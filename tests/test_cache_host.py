@@ -201,3 +201,21 @@ def test_attend_refuses_tables_that_32_bit_positions_do_not_hold():
         assert call(most + 1, page) == call((1 << 31) // page - 1, page) == -3
         assert call(1, page, most) == -4
         assert call(1, page, most + 1) == call(1, page, (1 << 31) // page - 1) == -3
+
+
+def test_attend_prices_the_work_by_the_form_that_does_it():
+    # long prompts over long tables fit; more units than 32 bits number do not (no workspace: nothing runs)
+    L, p = B.lib(), _fake()
+
+    def call(rows, H, Hkv, tokens, D=128, groups=0, R=1, most=None):
+        c = _cache(width=tokens // 16, rows=R, n_kv_heads=Hkv, head_dim=D)
+        g = (groups, p, p, tokens // 16, p) if groups else (0, None, None, 0, None)
+        return L.dspark_cache_attend(c, 0, p, H * D, rows, H, p, 1, R, most or rows, 0.125, *g, p, H * D, None, None, None, 0, None)
+    assert call(131072, 64, 8, 1 << 20) == -4          # one prompt, a table of a million tokens
+    assert call(131072, 32, 2, 1 << 20) == -4          # sixteen heads to a key head
+    assert call(131072, 64, 8, 1 << 20, groups=1) == -4
+    assert call(300, 64, 8, 1 << 21, R=256, most=(1 << 31) - 1) == -4   # a bound that says nothing
+    assert call(1 << 20, 64, 8, 1 << 24) == -3
+    assert call(1 << 20, 64, 8, 1 << 24, groups=1) == -3
+    assert call(1 << 25, 64, 8, 1 << 20) == -3         # more columns than 2^31
+    assert call(1 << 20, 64, 1, 1 << 16, D=256, groups=1) == call(1 << 20, 64, 1, 1 << 16, D=256, groups=1, R=2) == -3

@@ -122,3 +122,24 @@ def test_large_pages_and_their_ends(page):
         for groups in ([], [(3, 1)]):
             lens = [page - 1 if not groups else page, 2 * page, page + 1, 3]
             Case(45, lens, rows, 4, 2, 128, "bf16", page, groups=groups).check()
+
+
+def test_a_long_bound_over_a_long_table():
+    # rows and a table of a million tokens whose product is large, of which the call uses little
+    print("attend, long bounds", flush=True)
+    c = Case(46, [700, 40, 90], [70, 1, 130], 8, 2, 64)
+    p, n = c.prepared(), 131072
+    st, R = c.st, 3
+    table = torch.full((R, 1 << 16), -1, dtype=torch.int32, device=cu.DEV)
+    table[:, :st.cache.width] = st.cache.table
+    cache = B.PagedCache(1, st.cache.n_pages, 16, 2, 64, B.DSPARK_BF16, R, 1 << 16, k=st.cache.k, v=st.cache.v, table=table,
+                         len=st.cache.len, ref=st.cache.ref)
+    q = torch.zeros((n, 8, 64), dtype=torch.bfloat16, device=cu.DEV)
+    q[:c.rows] = p["q"]
+    out = torch.full_like(q, 7.0)
+    for most in (n, (1 << 31) - 1):
+        out.fill_(7.0)
+        B.dspark_cache_attend(cache, 0, q, p["offsets"], 1, most, c.scale, out, ws=p["ws"], status=p["status"])
+        torch.cuda.synchronize()
+        assert int(p["status"].item()) == 0 and (out[c.rows:] == 7).all()
+        cu.assert_attend(out[:c.rows], None, c.want(), "bf16", 830, 64)
