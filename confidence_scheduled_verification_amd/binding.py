@@ -536,8 +536,11 @@ def pages_workspace(cache: PagedCache, n: int):
     return _torch().empty(nbytes // 4, dtype=_torch().int32, device=cache.device)
 
 
-def cache_workspace(cache: PagedCache, R: int, H: int, max_new: int, n_groups: int = 0):
-    """Workspace of dspark_cache_attend for up to R requests of up to max_new rows."""
+def cache_workspace(cache: PagedCache, R: int, H: int, max_new: int, n_groups: int = 0, n_rows: Optional[int] = None):
+    """Workspace of dspark_cache_attend for up to R requests of up to max_new rows each, or of up
+    to n_rows rows in all (fewer bytes where one long prompt sets max_new)."""
+    if n_rows is not None and n_rows < R * max_new:
+        R, max_new = max(R, n_rows), 1
     nbytes = int(lib().dspark_cache_attend_workspace_bytes(R, H, cache.head_dim, max_new, n_groups))
     return _torch().empty((nbytes + 15) // 16 * 4, dtype=_torch().int32, device=cache.device)
 

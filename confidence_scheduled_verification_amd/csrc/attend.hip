@@ -1253,17 +1253,15 @@ size_t slots_bytes(int D) {
     return round256((size_t)kAttendMaxCus * columns * 2 * (D + 2) * sizeof(float));
 }
 constexpr int kMaxWorkers = kAttendMaxCus * 3;  // of any form
-size_t dense_bytes(int R, int H, int D, int max_new) {
-    return round256((size_t)R * max_new * H * (D + 2) * sizeof(float));
-}
+size_t dense_bytes(int rows, int H, int D) { return round256((size_t)rows * H * (D + 2) * sizeof(float)); }
 
 }  // namespace
 
-size_t attend_ws_bytes(int R, int H, int D, int max_new, int n_groups) {
+size_t attend_ws_bytes(int R, int H, int D, int rows, int n_groups) {
     size_t n = slots_bytes(D) + round256(kMaxWorkers * sizeof(AttendEnd));
     if (n_groups)
         n += slots_bytes(D) + round256((size_t)(R + 1) * 4) + round256((size_t)(n_groups + 1) * 4) +
-             2 * dense_bytes(R, H, D, max_new);
+             2 * dense_bytes(rows, H, D);
     return n;
 }
 
@@ -1280,8 +1278,8 @@ void attend_ws_layout(AttendArgs& a, void* ws) {
     a.slots[1] = (float*)take(slots_bytes(a.D));
     a.cum[0] = (uint32_t*)take(round256((size_t)(a.R + 1) * 4));
     a.cum[1] = (uint32_t*)take(round256((size_t)(a.n_groups + 1) * 4));
-    a.dense[0] = (float*)take(dense_bytes(a.R, a.H, a.D, a.max_new));
-    a.dense[1] = (float*)take(dense_bytes(a.R, a.H, a.D, a.max_new));
+    a.dense[0] = (float*)take(dense_bytes(a.rows, a.H, a.D));
+    a.dense[1] = (float*)take(dense_bytes(a.rows, a.H, a.D));
 }
 
 void attend_forms(AttendArgs& a, int cus) {

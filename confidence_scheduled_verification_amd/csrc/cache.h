@@ -103,7 +103,7 @@ struct AttendArgs {
     uint32_t* cum[2];  // with shared prefixes: running units (of one key head) of the requests, of the groups
 };
 void attend_forms(AttendArgs& a, int num_cu);  // from the sizes and the device
-size_t attend_ws_bytes(int R, int H, int D, int max_new, int n_groups);
+size_t attend_ws_bytes(int R, int H, int D, int rows, int n_groups);
 void attend_ws_layout(AttendArgs& a, void* ws);
 hipError_t launch_attend(const AttendArgs& a, hipStream_t s);
 

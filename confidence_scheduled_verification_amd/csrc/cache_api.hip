@@ -172,7 +172,7 @@ int dspark_cache_append(const dspark_cache_t* c, int layer, const void* k_new, i
 
 size_t dspark_cache_attend_workspace_bytes(int R, int H, int head_dim, int max_new, int n_groups) {
     if (R < 1 || H < 1 || max_new < 1 || n_groups < 0) return 0;
-    return dspark::attend_ws_bytes(R, H, head_dim, max_new, n_groups);
+    return dspark::attend_ws_bytes(R, H, head_dim, (int)std::min<long long>((long long)R * max_new, INT32_MAX), n_groups);
 }
 
 int dspark_cache_attend(const dspark_cache_t* c, int layer, const void* q, int64_t q_stride, int n_rows, int H,
@@ -224,9 +224,7 @@ int dspark_cache_attend(const dspark_cache_t* c, int layer, const void* q, int64
     if (!fits || !groups_fit)
         return fail(DSPARK_EUNSUPPORTED, "%s: %d rows of %d heads over up to %lld tokens are too many for one call", who,
                     n_rows, H, tokens);
-    if ((rc = check_ws(ws, ws_bytes, dspark_cache_attend_workspace_bytes(R, H, c->head_dim, max_new, n_groups), who)) !=
-        DSPARK_OK)
-        return rc;
+    if ((rc = check_ws(ws, ws_bytes, dspark::attend_ws_bytes(R, H, a.D, a.rows, n_groups), who)) != DSPARK_OK) return rc;
     const size_t at = layer * layer_elems(c);
     a.q = (const uint16_t*)q;
     a.q_stride = q_stride;

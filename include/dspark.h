@@ -609,6 +609,9 @@ int dspark_cache_append(const dspark_cache_t* cache, int layer, const void* k_ne
  * run.  More rows, heads and tokens than 32-bit numbers of work units hold, and tables or
  * prefixes of more than 2^31 - 8192 tokens (width * page_size), return DSPARK_EUNSUPPORTED.
  */
+/* Bytes of workspace (16-byte aligned) of up to R requests of up to max_new rows each.  A call
+ * needs only what its tensors' n_rows rows take: the bytes for max(R, n_rows) requests of one
+ * row will do whatever its max_new is, and far fewer where one long prompt sets that. */
 size_t dspark_cache_attend_workspace_bytes(int R, int H, int head_dim, int max_new, int n_groups);
 int dspark_cache_attend(const dspark_cache_t* cache, int layer, const void* q, int64_t q_stride, int n_rows, int H,
                         const int32_t* offsets, int lead, int R, int max_new, float scale, int n_groups,

@@ -219,3 +219,24 @@ def test_attend_prices_the_work_by_the_form_that_does_it():
     assert call(1 << 20, 64, 8, 1 << 24, groups=1) == -3
     assert call(1 << 25, 64, 8, 1 << 20) == -3         # more columns than 2^31
     assert call(1 << 20, 64, 1, 1 << 16, D=256, groups=1) == call(1 << 20, 64, 1, 1 << 16, D=256, groups=1, R=2) == -3
+
+
+def test_attend_needs_the_workspace_of_its_rows():
+    # 255 single tokens and a prompt of 4096 rows behind a prefix (a workspace that is large enough
+    # but not aligned is refused as such, so that nothing runs)
+    L, p, R, H, n = B.lib(), _fake(), 256, 64, 4351
+    c = _cache(rows=R, n_kv_heads=8, head_dim=128, width=600)
+
+    def call(nbytes, max_new=4096, rows=n):
+        return L.dspark_cache_attend(c, 0, p, H * 128, rows, H, p, 1, R, max_new, 0.125, 1, p, p, 4, p, p, H * 128, None, None,
+                                     p + 8, nbytes, None)
+    few, many = (L.dspark_cache_attend_workspace_bytes(*a, 1) for a in ((n, H, 128, 1), (R, H, 128, 4096)))
+    assert few < 1 << 30 and many > 1 << 36
+    assert call(few) == -1 and b"aligned" in L.dspark_last_error()
+    assert call(few, rows=2 * n) == -4 and call(1 << 20) == -4
+    assert call(many, rows=R * 4096) == -1
+    # sizes whose product passes 64 bits do not wrap round to a few bytes
+    assert L.dspark_cache_attend_workspace_bytes(8192, 65535, 256, (1 << 31) - 1, 1) > 1 << 50
+    cpu = B.PagedCache(1, 4, 16, 8, 128, B.DSPARK_BF16, R, 5, device="cpu", data=False)
+    assert B.cache_workspace(cpu, 4, H, 100, 1, n_rows=103).numel() * 4 < B.cache_workspace(cpu, 4, H, 100, 1).numel() * 4
+    assert B.cache_workspace(cpu, 4, H, 3, 1, n_rows=103).numel() == B.cache_workspace(cpu, 4, H, 3, 1).numel()

@@ -143,3 +143,21 @@ def test_a_long_bound_over_a_long_table():
         torch.cuda.synchronize()
         assert int(p["status"].item()) == 0 and (out[c.rows:] == 7).all()
         cu.assert_attend(out[:c.rows], None, c.want(), "bf16", 830, 64)
+
+
+@pytest.mark.parametrize("D,rows", [(128, [1] * 11 + [300]), (64, [300] + [1] * 5), (256, [1, 90, 2])])
+def test_a_workspace_of_the_rows_alone(D, rows):
+    # single tokens and a prompt behind a prefix, in a workspace sized by the rows: nothing is
+    # written behind it
+    print("attend, workspace by rows", D, rows, flush=True)
+    R = len(rows)
+    c = Case(47, [40 + 3 * r for r in range(R)], rows, 4, 2, D, groups=[(R - 1, 2)])
+    p = c.prepared()
+    n = B.cache_workspace(c.st.cache, R, c.H, c.max_new, 1, n_rows=c.rows).numel()
+    assert n < p["ws"].numel()
+    p["ws"].fill_(0x7FC00000)
+    whole, p["ws"] = p["ws"], p["ws"][:n]
+    c.call(p)
+    torch.cuda.synchronize()
+    assert int(p["status"].item()) == 0 and (whole[n:] == 0x7FC00000).all()
+    cu.assert_attend(p["out"], p["lse"], c.want(), c.dtype, 400, D, c.left)
