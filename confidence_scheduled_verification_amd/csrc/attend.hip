@@ -633,7 +633,8 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
     constexpr int kUnit = 32 * kKeyWaves;
     constexpr int kDims = D <= 128 ? D : 128;  // dims joined over the waves at a time
     constexpr int kRow = kDims + 4;
-    __shared__ float s_o[4][32][kRow];
+    __shared__ __attribute__((aligned(16))) float s_o[4][32][kRow];
+    static_assert(__alignof__(s_o) == 16 && kRow % 4 == 0, "read as float4");
     __shared__ float s_m[4][32], s_l[4][32];
     __shared__ uint32_t s_base[8];
     extern __shared__ uint32_t s_cum[];  // running units, n + 1, then the requests
@@ -901,7 +902,9 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
     constexpr int NT = D / 32, NC = D / 16;
     constexpr int kStage = 8 * W::kBlock * 2, kJoin = W::kWaves * 32 * kPitch * 4;  // bytes
     __shared__ __attribute__((aligned(16))) char s_mem[2 * kStage > kJoin ? 2 * kStage : kJoin];
-    __shared__ int s_have[4][4], s_special;
+    __shared__ __attribute__((aligned(16))) int s_have[4][4];
+    static_assert(__alignof__(s_have) == 16 && __alignof__(s_mem) == 16, "read as int4, float4 and eight 16-bit values");
+    __shared__ int s_special;
     __shared__ uint32_t s_base[8];
     extern __shared__ uint32_t s_cum[];  // running units, n + 1, then the requests
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
