@@ -61,10 +61,15 @@ constexpr int kWideLeast = 4, kFewParts = 8, kFewMost = 8;
 constexpr float kInf = __builtin_huge_valf();
 // The running maximum follows only when it grows by more than this exponent of two; until
 // then the weights are taken relative to the older one, at most 2^8, and nothing that has
-// been summed has to be rescaled.
+// been summed has to be rescaled.  The weights and their sums are besides scaled by 2^kRaise of
+// their type: an fp16 weight below half of its smallest number, 2^-24, would be zero in the
+// second product and not in the sum, and a long row of such keys would be missing from the
+// result (600 keys of 2^-26 each: 38% of it).  With 2^6 that ends at 2^-31, and the largest
+// weight, 2^14, stays a factor of four below fp16's largest number.  bf16 has fp32's exponents.
 constexpr float kLag = 8.f;
 
 struct Bf16 {
+    static constexpr float kRaise = 0.f;
     static constexpr uint32_t kExp = 0x7F80u, kMant = 0x007Fu, kOne = 0x3F80u, k64 = 0x4280u, k4096 = 0x4580u;
     static __device__ __forceinline__ f32x16 mfma(s16x8 a, s16x8 b, f32x16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
@@ -73,6 +78,7 @@ struct Bf16 {
     static __device__ __forceinline__ uint16_t bits(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
 };
 struct F16 {
+    static constexpr float kRaise = 6.f;
     static constexpr uint32_t kExp = 0x7C00u, kMant = 0x03FFu, kOne = 0x3C00u, k64 = 0x5400u, k4096 = 0x6C00u;
     static __device__ __forceinline__ f32x16 mfma(s16x8 a, s16x8 b, f32x16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
@@ -803,7 +809,7 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
 #pragma unroll
                     for (int j = 0; j < 16; ++j) o[t][j] *= alpha;
             }
-            const float mc = m == -kInf ? 0.f : m * a.scale_log2;
+            const float mc = m == -kInf ? 0.f : m * a.scale_log2 - E::kRaise;
             s16x8 pf[2];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
@@ -857,7 +863,7 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
                                    *(const s16x8*)(vp[1] + (t * 32 + col) * 16 + half * 8), sees[0], sees[1]);
             }
         }
-        ms = m == -kInf ? -kInf : m * a.scale_log2;
+        ms = m == -kInf ? -kInf : m * a.scale_log2 - E::kRaise;
         whole = cur.whole();
         begins = cur.unit0 == 0;
         f0 = cur.f0;
@@ -1037,7 +1043,7 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
 #pragma unroll
                     for (int j = 0; j < 16; ++j) o[i][j] *= alpha;
             }
-            const float mc = m == -kInf ? 0.f : m * a.scale_log2;
+            const float mc = m == -kInf ? 0.f : m * a.scale_log2 - E::kRaise;
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
                 const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j / 16][j % 16], a.scale_log2, -mc));
@@ -1154,7 +1160,7 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
                                    *(const s16x8*)(a.v + at[1] + t * 512 + col * 16 + half * 8), sees[0], sees[1]);
             }
         }
-        m = m == -kInf ? -kInf : m * a.scale_log2;
+        m = m == -kInf ? -kInf : m * a.scale_log2 - E::kRaise;
 
         const bool whole = cur.whole();
         __syncthreads();  // LDS is free

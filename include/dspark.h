@@ -578,7 +578,7 @@ int dspark_cache_append(const dspark_cache_t* cache, int layer, const void* k_ne
  *   lse[row, head] = ln sum_p exp(scale * q[row, head] . K[p, g])        g = head / (H / n_kv_heads)
  * Scores, the softmax and the sums are held in fp32; the weights, relative to a running
  * maximum (and at most 2^8, since it follows in steps), are rounded to the cache's dtype for
- * the second product, and out once.  A position that a row does not see has no influence on
+ * the second product (fp16: in steps of 2^-30 at the smallest), and out once.  A position that a row does not see has no influence on
  * it, whatever its K and V hold.  Where a row does see a value of V that is not finite, its
  * result there is not finite either; an infinity whose weight rounds to zero may make it NaN.
  * A score that is NaN or +infinity (by what is not finite in q or in a K that the row sees)

@@ -109,3 +109,37 @@ def test_infinite_scores(rows, groups, dtype, D):
     for t, h in alone:
         out[t, h], spread[t, h], lse[t, h] = 0.0, 0.0, -math.inf
     c.check(want=(out, lse, spread, reach))
+
+
+@pytest.mark.parametrize("rows,lens,groups", [([1, 1], [600, 40], []), ([70, 40], [600, 33], []),
+                                              ([2, 1], [608, 600], [(2, 37)]), ([40, 70], [608, 600], [(2, 37)])])
+@pytest.mark.parametrize("dtype,D", [("fp16", 64), ("fp16", 128), ("fp16", 256), ("bf16", 128)])
+def test_many_small_weights_beside_a_large_one(rows, lens, groups, dtype, D):
+    """The first key outweighs each other one by 2^26, and its value is zero, so that the result is
+    the others' alone.  A weight of 2^-26 is below fp16's smallest number, 2^-24, and half of it;
+    the kernels scale fp16 weights by 2^6, so that the rounding of each is off by at most
+    half of 2^-24, 2^-31 of the largest weight (a bf16 weight by 2^-8 of itself)."""
+    print("attend, small weights", rows, lens, groups, dtype, D, flush=True)
+    c = Case(36, lens, rows, 2, 1, D, dtype, 16, groups=groups)
+    st = c.st
+    c.scale, value = 0.125, 1000.0
+    c.q.zero_()
+    c.q[:, :, 1] = 12.0
+    for r, n in enumerate(lens):
+        for p in range(n + rows[r]):
+            at = (0, st.table[r][p // 16], slice(None), p % 16)
+            st.k[at], st.v[at] = 0.0, value if p else 0.0
+            if p == 0:
+                st.k[at + (1,)] = 12.0
+    out, lse, spread, reach = c.want()
+    keys = max(lens) + max(rows)
+    p = c.prepared()
+    c.call(p)
+    assert out.max() > 0.9 * value * max(lens) * math.exp(-18.0)
+    off = np.abs(p["out"].cpu().double().numpy() - out)
+    # e: the score's and exp2's roundings (18 is exact in either type); the sums' of up to `keys` terms
+    rel = 2 * (2.0 ** -24 * 4 * 26 + 2.0 ** -21) + 2 * keys * 2.0 ** -24
+    step = 2.0 ** -8 * out if dtype == "bf16" else keys * 2.0 ** -31 * value
+    bound = 1.05 * (step + rel * out) + out * (2.0 ** -8 if dtype == "bf16" else 2.0 ** -11) + 2.0 ** -25
+    assert int(p["status"].item()) == 0 and (off <= bound).all(), (off.max(), bound.max(), out.max())
+    assert (np.abs(p["lse"].cpu().double().numpy() - lse) <= rel + 2.0 ** -22 * np.abs(lse)).all()
