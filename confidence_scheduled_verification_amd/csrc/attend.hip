@@ -67,6 +67,11 @@ constexpr float kInf = __builtin_huge_valf();
 // result (600 keys of 2^-26 each: 38% of it).  With 2^6 that ends at 2^-31, and the largest
 // weight, 2^14, stays a factor of four below fp16's largest number.  bf16 has fp32's exponents.
 constexpr float kLag = 8.f;
+// A weight is exp2 of one fused multiply-add, score times scale minus the scaled maximum, whose
+// rounding all weights of a part have in common.  Past this exponent of two that rounding (2^-4
+// here) would grow to whole powers of two, at 2^25 past fp16's range and at 2^31 past fp32's; such
+// a wave subtracts the maximum from its scores first, which is exact near the maximum.
+constexpr float kLarge = 1048576.f;
 
 struct Bf16 {
     static constexpr float kRaise = 0.f;
@@ -520,6 +525,11 @@ __device__ __forceinline__ void finish_wave(const AttendArgs& a, float* s_o, int
     }
 }
 
+// Whether a column's maximum m (of the raw scores) is finite and larger than kLarge says.
+__device__ __forceinline__ bool any_large(float m, float scale_log2) {
+    return __ballot(m != -kInf && fabsf(m) * scale_log2 > kLarge) != 0;
+}
+
 // The larger of a lane's value and that of the lane 32 on; and their sum.
 __device__ __forceinline__ float max_halves(float x) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -771,7 +781,8 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
         if (!more) break;
 #pragma unroll
         for (int t = 0; t < NT; ++t) o[t] = f32x16{};
-        float m = -kInf;  // of the raw scores; l is this half's share of the sum
+        float m = -kInf, mc = 0.f;  // of the raw scores, and scaled; l is this half's share of the sum
+        bool large = false;
         l = 0.f;
         int special_from = -1;     // the first block with values that add_special has to add
         // One block of 32 keys: scores, weights, and the second product.  kFast: all of its keys
@@ -799,17 +810,23 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
 #pragma unroll
             for (int j = 1; j < 16; ++j) mx = fmaxf(mx, s[j]);
             mx = max_halves(mx);
-            if (__ballot((mx - m) * a.scale_log2 > kLag)) {
+            if (__ballot((mx - m) * a.scale_log2 > kLag) || large) {
                 const float m_new = fmaxf(m, mx);
                 const float alpha = __builtin_amdgcn_exp2f((m - (m_new == -kInf ? 0.f : m_new)) * a.scale_log2);
                 m = m_new;
+                mc = m == -kInf ? 0.f : m * a.scale_log2 - E::kRaise;
                 l *= alpha;
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) o[t][j] *= alpha;
+                large = any_large(m, a.scale_log2);
+                if (large) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) s[j] -= m == -kInf ? 0.f : m;
+                    mc = -E::kRaise;
+                }
             }
-            const float mc = m == -kInf ? 0.f : m * a.scale_log2 - E::kRaise;
             s16x8 pf[2];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
@@ -944,7 +961,8 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
         f32x16 o[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) o[t] = f32x16{};
-        float m = -kInf, l = 0.f;  // m of the raw scores; l this half's share of the sum
+        float m = -kInf, mc = 0.f, l = 0.f;  // m of the raw scores, mc scaled; l this half's share of the sum
+        bool large = false;
         int pos = q.kb + (int)(cur.unit0 * W::kUnit);
         const int pos_end = min(tile_end, q.kb + (int)(cur.unit1 * W::kUnit));
         const int stages = pos < pos_end ? (pos_end - pos + W::kUnit - 1) / W::kUnit : 0, pos0 = pos;
@@ -1033,17 +1051,23 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
 #pragma unroll
             for (int j = 1; j < 32; ++j) mx = fmaxf(mx, s[j / 16][j % 16]);
             mx = max_halves(mx);
-            if (__ballot((mx - m) * a.scale_log2 > kLag)) {
+            if (__ballot((mx - m) * a.scale_log2 > kLag) || large) {
                 const float m_new = fmaxf(m, mx);
                 const float alpha = __builtin_amdgcn_exp2f((m - (m_new == -kInf ? 0.f : m_new)) * a.scale_log2);
                 m = m_new;
+                mc = m == -kInf ? 0.f : m * a.scale_log2 - E::kRaise;
                 l *= alpha;
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) o[i][j] *= alpha;
+                large = any_large(m, a.scale_log2);
+                if (large) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) s[j / 16][j % 16] -= m == -kInf ? 0.f : m;
+                    mc = -E::kRaise;
+                }
             }
-            const float mc = m == -kInf ? 0.f : m * a.scale_log2 - E::kRaise;
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
                 const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j / 16][j % 16], a.scale_log2, -mc));

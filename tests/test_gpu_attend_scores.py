@@ -6,6 +6,7 @@ import math
 
 import numpy as np
 import pytest
+import torch
 
 import cache_util as cu
 from test_gpu_attend import Case
@@ -143,3 +144,47 @@ def test_many_small_weights_beside_a_large_one(rows, lens, groups, dtype, D):
     bound = 1.05 * (step + rel * out) + out * (2.0 ** -8 if dtype == "bf16" else 2.0 ** -11) + 2.0 ** -25
     assert int(p["status"].item()) == 0 and (off <= bound).all(), (off.max(), bound.max(), out.max())
     assert (np.abs(p["lse"].cpu().double().numpy() - lse) <= rel + 2.0 ** -22 * np.abs(lse)).all()
+
+
+@pytest.mark.parametrize("shape", list(SHAPES))
+@pytest.mark.parametrize("dtype,D,size", [("bf16", 128, 1e5), ("fp16", 64, 4e3), ("bf16", 256, 1e15), ("fp16", 128, 4e3)])
+def test_very_large_finite_scores(shape, dtype, D, size):
+    """Scores so large that a rounding of one is many powers of two: the largest still has a
+    weight of one, and where it leads by far the result is its value."""
+    print("attend, large scores", shape, dtype, D, flush=True)
+    c = _case(37, shape, D, dtype)
+    c.q = cu.rounded(c.q.double().numpy() * size, dtype)
+    k = c.st.k[0]
+    k[np.isfinite(k)] *= size
+    c.st.k[0] = cu.rounded(k, dtype).double().numpy()
+    out, lse, _, reach = c.want()
+    p = c.prepared()
+    c.call(p)
+    got, got_lse = p["out"].cpu().double().numpy(), p["lse"].cpu().double().numpy()
+    assert int(p["status"].item()) == 0 and np.isfinite(got).all() and np.isfinite(got_lse).all()
+    # scores and lse are off by at most (D + 8) 2^-24 of the largest sum of |q||k|; where the second
+    # score lies behind by more than twice that, and by 40, its weight is below every rounding, and
+    # what is left are the roundings of the one weight and of the result, half a step each, and exp2's
+    err = (D + 8) * 2.0 ** -24 * reach
+    assert (np.abs(got_lse - lse) <= 1.05 * err + 2.0 ** -22 * np.abs(lse) + 2.0 ** -20).all()
+    first, second = _two_largest(c)
+    clear = first - second > 2 * err + 40
+    assert clear.mean() > 0.5
+    half = float(torch.finfo(cu.DT[dtype][1]).eps) / 2
+    off = np.abs(got - out)[clear]
+    assert (off <= 1.05 * (2 * half + 2.0 ** -21) * np.abs(out)[clear] + 2.0 ** -25).all(), off.max()
+
+
+def _two_largest(c):
+    """Each (row, head)'s two largest scores, -inf where there is no second key."""
+    st, q = c.st, c.q.double().numpy()
+    G, two = c.H // st.k.shape[2], np.full((2, c.rows, c.H), -math.inf)
+    for r, n in enumerate(st.len):
+        a, b = c.offsets[r] + r, c.offsets[r + 1] + r + 1
+        pos = np.arange(n + b - a)
+        ids = np.array(st.table[r])[pos // c.page]
+        for t in range(a, b):
+            for h in range(c.H):
+                s = np.sort(c.scale * (st.k[0][ids, h // G, pos % c.page][:n + 1 + t - a] @ q[t, h]))
+                two[:s[-2:].size, t, h] = s[::-1][:2]
+    return two
