@@ -24,7 +24,7 @@ int check_pages(const dspark_cache_t* c, const char* who) {
                     c->page_size);
     if (c->rows < 0 || c->width < 1 || (long long)c->rows * c->width > INT32_MAX)
         return fail(DSPARK_EUNSUPPORTED, "%s: a table of %d rows and %d entries", who, c->rows, c->width);
-    if (!c->table || !c->len || !c->ref) return fail(DSPARK_EINVAL, "%s: table, len or ref is NULL", who);
+    if ((c->rows > 0 && (!c->table || !c->len)) || !c->ref) return fail(DSPARK_EINVAL, "%s: table, len or ref is NULL", who);
     return DSPARK_OK;
 }
 

@@ -240,3 +240,16 @@ def test_attend_needs_the_workspace_of_its_rows():
     cpu = B.PagedCache(1, 4, 16, 8, 128, B.DSPARK_BF16, R, 5, device="cpu", data=False)
     assert B.cache_workspace(cpu, 4, H, 100, 1, n_rows=103).numel() * 4 < B.cache_workspace(cpu, 4, H, 100, 1).numel() * 4
     assert B.cache_workspace(cpu, 4, H, 3, 1, n_rows=103).numel() == B.cache_workspace(cpu, 4, H, 3, 1).numel()
+
+
+def test_a_cache_without_rows():
+    # its table and lengths are empty (pages that the caller alone holds can be made compact)
+    L, p = B.lib(), _fake()
+    c = _cache(rows=0, table=None, len=None)
+    assert L.dspark_pages_reserve(c, None, 1, 0, None, None, None, 0, None) == 0
+    assert L.dspark_pages_trim(c, None, 0, None, None, None) == 0
+    assert L.dspark_pages_commit(c, None, 1, 0, None, None) == 0
+    assert L.dspark_pages_compact(c, p, p, None, None, 0, None) == -4  # its workspace, no more
+    assert L.dspark_pages_trim(c, None, 1, None, None, None) == -2
+    assert L.dspark_pages_reserve(c, p, 1, 1, p, None, p, 1 << 20, None) == -2
+    assert L.dspark_pages_reserve(_cache(rows=0, table=None, len=None, ref=None), None, 1, 0, None, None, None, 0, None) == -1

@@ -48,3 +48,18 @@ def test_trim_of_as_many_rows_as_a_grid_has_threads():
     assert int(status.item()) == 0
     assert c.table[held, 0].tolist() == [0, -1, 2, 3, -1] and c.len[held].tolist() == [7, 0, 7, 7, 0]
     assert c.ref[:5].tolist() == [1, 0, 1, 1, 0] and int((c.len != 0).sum()) == 3
+
+
+def test_compact_without_rows():
+    # pages that the caller alone holds
+    print("compact, no rows", flush=True)
+    c = B.PagedCache(1, 5, 16, 1, 64, B.DSPARK_BF16, 0, 3, device=cu.DEV)
+    c.ref.copy_(cu.i32([0, 1, 0, 0, 2]))
+    c.k[0, 4], c.v[0, 4] = 4.0, 5.0
+    page_map, n_live = torch.zeros(5, dtype=torch.int32, device=cu.DEV), torch.zeros(1, dtype=torch.int32, device=cu.DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=cu.DEV)
+    B.dspark_pages_compact(c, page_map, n_live, B.pages_workspace(c, 0), status)
+    B.dspark_pages_trim(c)
+    torch.cuda.synchronize()
+    assert page_map.tolist() == [-1, 1, -1, -1, 0] and n_live.item() == 2 and status.item() == 0
+    assert c.ref.tolist() == [2, 1, 0, 0, 0] and (c.k[0, 0] == 4).all() and (c.v[0, 0] == 5).all()
