@@ -14,9 +14,10 @@
 // not fill are written one by one, so that what stands beside them is neither read nor
 // written.  A page that another row holds too is not written to either.
 //
-// The bytes bound it: once read, once written.  1145 rows of 8 key heads of 128 (9.4 MB): 9.8
-// us, which are the loads that wait for each other (rows, page ids, counts) and the launch; eight
-// prompts of 14351 rows (117 MB): 36 us, 3.3 TB/s, where a large copy reaches 5.5.  A wave to
+// Its floor is the bytes, once read, once written.  1145 rows of 8 key heads of 128 (9.4 MB): 9.8
+// us, which are the launch and loads that wait for each other (rows, page ids, counts, and behind
+// them the data, which does not depend on the last two); eight prompts of 14351 rows (117 MB):
+// 36 us, 3.3 TB/s, where a large copy reaches 5.5.  A wave to
 // every (block, 64 dims) rather than a workgroup that walks the heads: 36 against 41 us.  V
 // turned over through LDS instead of in registers: 82.
 #include <algorithm>

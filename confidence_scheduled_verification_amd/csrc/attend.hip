@@ -637,8 +637,8 @@ __device__ __forceinline__ void load_q(const AttendArgs& a, s16x8 (&qf)[D / 16],
 // while it computes; and the next segment's rows, page ids and first keys are requested before
 // this one's waves are joined (kSet 0: the requests' own keys; 1: the groups' shared ones).
 //
-// 256 requests of 1145 rows, 64 query and 8 key heads of 128, bf16: 177 us for 131500 tokens
-// (539 MB, 3.0 TB/s), 512 for four times as many (4.2 TB/s): the loads bound it, and the joining
+// 256 requests of 1145 rows, 64 query and 8 key heads of 128, bf16: 176 us for 131500 tokens
+// (539 MB, 3.1 TB/s), 512 for four times as many (4.2 TB/s): the loads bound it, and the joining
 // of four waves at each of 2048 segments.  Four single tokens, 1750 tokens in all: 9 us, of
 // which the bytes would take 1.3; the others are loads that wait for each other, from the
 // requests' rows to their page ids, keys, values and the parts.
@@ -901,14 +901,15 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
 // With eight waves two share a SIMD, and they are half a stage apart: while one multiplies, the
 // other makes weights of its scores, which takes the vector unit about as long (1024 matrix
 // cycles and 1000 of the other a stage), so both units work.  In step with each other, every
-// wave's operands waited for one by one, the same loop took 350 us where this one takes 318.
+// wave's operands waited for one by one, the same loop took 350 us where this one takes 320.
 // Reading the operands a group ahead, four at a time, is worth a further third of the product's
 // time; nothing with a mask is in the products' path (see clean), for two paths cost copies of
 // the accumulators and spills.
 //
-// 1145 rows behind 8192 shared tokens, 64 query and 8 key heads of 128, bf16: 318 us, 970
-// TFLOP/s.  What bounds it: LDS, which gives an operand of 1 KB to one matrix instruction of 32
-// cycles only, so that four SIMDs ask for all of its 128 bytes a cycle, beside what is brought.
+// 1145 rows behind 8192 shared tokens, 64 query and 8 key heads of 128, bf16: 320 us, 960
+// TFLOP/s.  No unit is the bound: the matrix units are busy 44% of the time and LDS 24%.  Waves
+// spend 39% of theirs on an issue slot or a result and 28% at the two barriers a stage and on loads,
+// which are asked for in the half stage that ends by waiting for them.
 // More columns a wave would need twice the accumulators, and leave one wave a SIMD and nothing
 // to work while it waits.
 template <int D>
