@@ -102,6 +102,7 @@ struct Request {
 };
 
 __device__ int group_of(const AttendArgs& a, int r) {
+    if (a.cum[1][a.n_groups] == 0) return -1;  // no group counts, as their launch has found (see plan)
     int lo = 0, hi = a.n_groups;  // the last group that starts at or before r
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -252,6 +253,8 @@ __device__ uint32_t plan(const AttendArgs& a, int n, uint32_t* s_cum, uint32_t* 
     Request* s_info = (Request*)(s_cum + n + 1);
     // More units than 32 bits number can only come from offsets that fall and rise again, so
     // that requests or groups share rows: the sums then stop past the bound, and none are served.
+    // So do the groups' where group_off fall: groups may then have requests in common, and each
+    // would leave parts of their rows.  Without groups the requests read their own tables.
     const uint32_t most = min(0x7FFFFFFFu / (uint32_t)a.Hkv, 0x7FFFFFFEu);
     uint32_t base = 0, bad = 0;
     for (int i0 = 0; i0 < n; i0 += kThreads) {
@@ -261,6 +264,7 @@ __device__ uint32_t plan(const AttendArgs& a, int n, uint32_t* s_cum, uint32_t* 
             if (kSet) {
                 const Group g = shared_of(a, i, bad);
                 x = (uint32_t)tiles_in(a, 1, g.n) * units_in(a, 1, g.ke);
+                if (a.group_off[i + 1] < a.group_off[i]) x = most + 1;
             } else {
                 Request q;
                 const int state = request_of(a, i, q, bad);
@@ -1226,7 +1230,6 @@ __global__ __launch_bounds__(kT) void attend_join_shared_kernel(AttendArgs a) {
     Group g{};
     uint32_t g_u0 = 0;
     if (q.kb > 0) {
-        if (common_units == 0) return;  // groups out of all bounds
         g = shared_of(a, q.group, bad);
         g_u0 = a.cum[1][q.group] * a.Hkv;
     }

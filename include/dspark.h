@@ -578,8 +578,8 @@ int dspark_cache_append(const dspark_cache_t* cache, int layer, const void* k_ne
  *   lse[row, head] = ln sum_p exp(scale * q[row, head] . K[p, g])        g = head / (H / n_kv_heads)
  * Scores, the softmax and the sums are held in fp32; the weights, relative to a running
  * maximum (and at most 2^8, since it follows in steps), are rounded to the cache's dtype for
- * the second product (fp16: in steps of 2^-30 at the smallest), and out once.  A position that a row does not see has no influence on
- * it, whatever its K and V hold.  Where a row does see a value of V that is not finite, its
+ * the second product (fp16: in steps of 2^-30 at the smallest), and out once.  A position that
+ * a row does not see has no influence on it, whatever its K and V hold.  Where a row does see a value of V that is not finite, its
  * result there is not finite either; an infinity whose weight rounds to zero may make it NaN.
  * A score that is NaN or +infinity (by what is not finite in q or in a K that the row sees)
  * makes the row's result of that head and its lse NaN; a score of -infinity weighs nothing, and
@@ -600,13 +600,14 @@ int dspark_cache_append(const dspark_cache_t* cache, int layer, const void* k_ne
  * Rows that see nothing (vacant requests) get zeros and lse -inf; so do those of a request
  * whose length fits neither its table nor its group (DSPARK_STATUS_BAD_ROW).  A request
  * with n_r < 0 or > max_new or rows outside the tensors, or from row R * max_new on, is left
- * out with the same status, and rows that belong to no request stay as they are.  A group whose
- * group_off do not lie in 0 .. R or fall, or whose shared_pages do not lie in 0 .. shared_width,
- * counts as none (DSPARK_STATUS_BAD_ROW): its requests read all of their own.  Where offsets or
- * group_off that fall and rise make more work than 32-bit numbers hold, the rows concerned (all,
- * or those behind a prefix) stay as they are (DSPARK_STATUS_BAD_ROW).  Page ids outside the cache
- * are not read: their tokens are left out (DSPARK_STATUS_BAD_PAGE).  Results are the same in every
- * run.  More rows, heads and tokens than 32-bit numbers of work units hold, and tables or
+ * out with the same status, and rows that belong to no request stay as they are.  (Rows that two
+ * requests name, as offsets that fall and rise have it, hold nothing certain.  Where such offsets
+ * make more work than 32-bit numbers hold, all rows stay as they are.)  A group whose group_off
+ * do not lie in 0 .. R, or whose shared_pages do not lie in 0 .. shared_width, counts as none
+ * (DSPARK_STATUS_BAD_ROW): its requests read all of their own.  So do all requests where
+ * group_off fall, or the groups' work passes 32-bit numbers.  Page ids outside the cache are not
+ * read: their tokens are left out (DSPARK_STATUS_BAD_PAGE).  Results are the same in every run.
+ * More rows, heads and tokens than 32-bit numbers of work units hold, and tables or
  * prefixes of more than 2^31 - 8192 tokens (width * page_size), return DSPARK_EUNSUPPORTED.
  */
 /* Bytes of workspace (16-byte aligned) of up to R requests of up to max_new rows each.  A call

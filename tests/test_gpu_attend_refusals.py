@@ -161,3 +161,14 @@ def test_a_workspace_of_the_rows_alone(D, rows):
     torch.cuda.synchronize()
     assert int(p["status"].item()) == 0 and (whole[n:] == 0x7FC00000).all()
     cu.assert_attend(p["out"], p["lse"], c.want(), c.dtype, 400, D, c.left)
+
+
+def test_groups_that_have_requests_in_common():
+    # group_off that fall: no group counts, whatever each one's own range is
+    print("attend, overlapping groups", flush=True)
+    for rows in ([1, 2, 1, 3], [40, 70, 1, 36]):
+        c = Case(48, [50, 34, 700, 40], rows, 4, 2, 128, groups=[(2, 2), (1, 1), (1, 2)])
+        p = c.prepared()
+        _run(c, p, c.offsets, 0)
+        for off in ([0, 3, 1, 4], [0, 4, 0, 4], [2, 4, 1, 3]):
+            _run(c, p, c.offsets, B.STATUS_BAD_ROW, group_off=off)
