@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(PKG, "libdspark.so")
 
 DSPARK_F32 = 0
 DSPARK_BF16 = 1
-DSPARK_F16 = 2  # the paged cache alone
+DSPARK_F16 = 2  # the paged cache and dspark_target_tokens
 STATUS_PREV_CLAMPED = 1
 STATUS_CONF_SANITIZED = 2
 STATUS_COST_INVALID = 4
@@ -28,6 +28,7 @@ STATUS_BAD_ALLOCATION = 16
 STATUS_BAD_PAGE = 32
 STATUS_BAD_ROW = 64
 STATUS_NO_PAGES = 128
+STATUS_NO_TOKEN = 256
 LAUNCH_RESIDENT = 0
 LAUNCH_COOPERATIVE = 1
 MAX_SLOTS = 16384
@@ -35,6 +36,9 @@ RULE_ARGMAX = 0
 RULE_FIRST_DROP = 1
 CHAIN_PRUNED = 0
 CHAIN_DENSE = 1
+TREE_MAX_NODES = 64
+TARGET_MAX_ROWS = 256
+ROTARY_SCALING = {"none": 0, "linear": 1, "bands": 2, "ramp": 3}
 MARKOV_MAGIC = 0x31766b6d6b707364
 MARKOV_HEADER_BYTES = 256
 
@@ -45,7 +49,10 @@ EXPORTS = ["dspark_last_error", "dspark_version", "dspark_workspace_bytes", "dsp
            "dspark_force_monotone", "dspark_profile_shapes", "dspark_build_cost_table", "dspark_set_launch_mode",
            "dspark_get_launch_mode", "dspark_pages_workspace_bytes", "dspark_pages_reserve", "dspark_pages_trim",
            "dspark_pages_commit", "dspark_pages_commit_granted", "dspark_pages_fork", "dspark_pages_compact", "dspark_cache_append",
-           "dspark_cache_attend_workspace_bytes", "dspark_cache_attend"]
+           "dspark_cache_attend_workspace_bytes", "dspark_cache_attend", "dspark_tree_merge", "dspark_tree_plan",
+           "dspark_rotary_frequencies", "dspark_rotary_turns", "dspark_cache_append_rotary", "dspark_cache_attend_tree",
+           "dspark_accept_tree", "dspark_cache_keep_path", "dspark_history_words", "dspark_history_clear", "dspark_history_add",
+           "dspark_target_workspace_bytes", "dspark_target_tokens"]
 
 # int fn(int shape, void* user, void* stream)
 SHAPE_FN = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p)
@@ -63,6 +70,28 @@ class dspark_cache_t(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p), ("len", ctypes.c_void_p),
                 ("ref", ctypes.c_void_p)] + [(n, ctypes.c_int32) for n in (
                     "layers", "n_pages", "page_size", "n_kv_heads", "head_dim", "dtype", "rows", "width")]
+
+
+class dspark_rotary_t(ctypes.Structure):
+    """The C handle of rotary positions (include/dspark.h)."""
+    _fields_ = [("turns", ctypes.c_void_p), ("dim", ctypes.c_int32), ("first", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("attention", ctypes.c_float)]
+
+
+class dspark_history_t(ctypes.Structure):
+    """The C handle of the record of seen tokens (include/dspark.h)."""
+    _fields_ = [("seen", ctypes.c_void_p), ("count", ctypes.c_void_p), ("rows", ctypes.c_int32), ("V", ctypes.c_int32)]
+
+
+class dspark_target_t(ctypes.Structure):
+    """The arguments of dspark_target_tokens (include/dspark.h)."""
+    _fields_ = [("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_int64)] + \
+        [(n, ctypes.c_int32) for n in ("n_rows", "V", "dtype", "R", "lead", "max_new")] + \
+        [(n, ctypes.c_void_p) for n in ("offsets", "history", "repetition", "presence", "frequency", "ver_tokens", "anc",
+                                        "bias_off", "bias_tok", "bias_val", "allowed", "allowed_row")] + \
+        [("allowed_stride", ctypes.c_int64)] + \
+        [(n, ctypes.c_int32) for n in ("n_nodes", "n_bias", "n_allowed", "reserved")] + \
+        [("target", ctypes.c_void_p), ("adjusted", ctypes.c_void_p), ("adjusted_stride", ctypes.c_int64)]
 
 
 class DSparkError(RuntimeError):
@@ -129,10 +158,28 @@ def lib():
         L.dspark_cache_attend_workspace_bytes.argtypes = [i, i, i, i, i]
         L.dspark_cache_attend.argtypes = [p, i, p, i64, i, i, p, i, i, i, ctypes.c_float, i, p, p, i, p, p, i64, p, p, p,
                                           sz, p]
+        d = ctypes.c_double
+        L.dspark_tree_merge.argtypes = [p, p, i, i, i, p, p, p, p, p, p]
+        L.dspark_tree_plan.argtypes = [p, i, p, i, i, i, p, p, p, p]
+        L.dspark_accept_tree.argtypes = [p, i, p, p, p, i, i, p, p, p, p, p, p]
+        L.dspark_rotary_frequencies.argtypes = [i, i, d, d, d, d, d, p]
+        L.dspark_rotary_turns.argtypes = [p, i, p]
+        L.dspark_cache_append_rotary.argtypes = [p, i, p, p, i64, i, p, i64, p, i64, p, i64, i, p, i, i, i, p, p, p]
+        L.dspark_cache_attend_tree.argtypes = [p, i, p, i64, i, i, p, i, i, i, p, ctypes.c_float, i, p, p, i, p, p, i64, p,
+                                               p, p, sz, p]
+        L.dspark_cache_keep_path.argtypes = [p, p, i, p, p, i, i, p, p]
+        L.dspark_history_words.restype = sz
+        L.dspark_history_words.argtypes = [i]
+        L.dspark_history_clear.argtypes = [p, p, i, p, p]
+        L.dspark_history_add.argtypes = [p, p, i, i, p, i, p, p]
+        L.dspark_target_workspace_bytes.restype = sz
+        L.dspark_target_workspace_bytes.argtypes = [i, i]
+        L.dspark_target_tokens.argtypes = [p, p, p, sz, p]
         for name in EXPORTS:
             if name not in ("dspark_last_error", "dspark_version", "dspark_workspace_bytes",
                             "dspark_markov_state_bytes", "dspark_pages_workspace_bytes",
-                            "dspark_cache_attend_workspace_bytes"):
+                            "dspark_cache_attend_workspace_bytes", "dspark_history_words",
+                            "dspark_target_workspace_bytes"):
                 getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -512,9 +559,9 @@ class PagedCache:
         self._ref = ctypes.byref(self.handle)
 
 
-def _on(cache: PagedCache, what: str, stream, ints=(), others=()) -> int:
-    """The stream of a call on `cache`: its device is the current one, and every tensor of the
-    call lies there; `ints` are int32 and densely packed."""
+def _on(cache, what: str, stream, ints=(), others=(), words=()) -> int:
+    """The stream of a call on `cache` (or what else has a device): its device is the current one, and
+    every tensor of the call lies there; `ints` are int32, `words` int64, both densely packed."""
     torch = _torch()
     device = cache.device
     for t in ints:
@@ -522,7 +569,10 @@ def _on(cache: PagedCache, what: str, stream, ints=(), others=()) -> int:
             if t.device != device:
                 raise ValueError(f"{what}: a tensor on {t.device}, the cache is on {device}")
             raise ValueError(f"{what}: index tensors must be contiguous int32")
-    for t in others:
+    for t in words:
+        if t is not None and (t.dtype is not torch.int64 or not t.is_contiguous()):
+            raise ValueError(f"{what}: nodes' words must be contiguous int64")
+    for t in (*others, *words):
         if t is not None and t.device != device:
             raise ValueError(f"{what}: a tensor on {t.device}, the cache is on {device}")
     if device.type != "cuda" or device.index != torch.cuda.current_device():
@@ -624,11 +674,8 @@ def dspark_cache_append(cache: PagedCache, layer: int, k_new, v_new, offsets, le
                                      R, max_new, _p(status), st))
 
 
-def dspark_cache_attend(cache: PagedCache, layer: int, q, offsets, lead: int, max_new: int, scale: float, out, lse=None,
-                        shared=None, ws=None, status=None, stream=None):
-    """One layer's attention of a step's rows.  `shared`: (group_off [n+1], shared_table [n, w],
-    shared_pages [n]) of prefixes that requests share, whose keys are read once for all of them."""
-    what = "dspark_cache_attend"
+def _attend(what: str, entry, cache: PagedCache, layer: int, q, offsets, lead: int, max_new: int, anc, scale: float, out, lse,
+            shared, ws, status, stream):
     R = _offsets_rows(cache, offsets, what)
     H = q.shape[1] if q.dim() == 3 else 0
     qs = _packed(cache, q, H, f"{what}: q")
@@ -647,10 +694,253 @@ def dspark_cache_attend(cache: PagedCache, layer: int, q, offsets, lead: int, ma
         n_groups, width = table.shape
         _shape(off, (n_groups + 1,), f"{what}: group_off")
         _shape(pages, (n_groups,), f"{what}: shared_pages")
-    st = _on(cache, what, stream, (offsets, off, table, pages), (q, out, lse, ws, status))
-    _check(lib().dspark_cache_attend(cache._ref, layer, _p(q), qs, q.shape[0], H, _p(offsets), lead, R, max_new,
-                                     float(scale), n_groups, _p(off), _p(table), width, _p(pages), _p(out), os_, _p(lse),
-                                     _p(status), _p(ws), _ws_bytes(ws), st))
+    if anc is not None and anc.numel() < q.shape[0]:
+        raise ValueError(f"{what}: anc has {anc.numel()} words for {q.shape[0]} rows")
+    st = _on(cache, what, stream, (offsets, off, table, pages), (q, out, lse, ws, status), (anc,))
+    tree = () if entry is lib().dspark_cache_attend else (_p(anc),)
+    _check(entry(cache._ref, layer, _p(q), qs, q.shape[0], H, _p(offsets), lead, R, max_new, *tree, float(scale), n_groups,
+                 _p(off), _p(table), width, _p(pages), _p(out), os_, _p(lse), _p(status), _p(ws), _ws_bytes(ws), st))
+
+
+def dspark_cache_attend(cache: PagedCache, layer: int, q, offsets, lead: int, max_new: int, scale: float, out, lse=None,
+                        shared=None, ws=None, status=None, stream=None):
+    """One layer's attention of a step's rows.  `shared`: (group_off [n+1], shared_table [n, w],
+    shared_pages [n]) of prefixes that requests share, whose keys are read once for all of them."""
+    _attend("dspark_cache_attend", lib().dspark_cache_attend, cache, layer, q, offsets, lead, max_new, None, scale, out, lse,
+            shared, ws, status, stream)
+
+
+def dspark_cache_attend_tree(cache: PagedCache, layer: int, q, offsets, lead: int, max_new: int, anc, scale: float, out,
+                             lse=None, shared=None, ws=None, status=None, stream=None):
+    """One layer's attention of the rows of trees: each sees its request's tokens and the nodes of its
+    word `anc` [rows] (int64, dspark_tree_plan)."""
+    if anc is None:
+        raise ValueError("dspark_cache_attend_tree: anc is needed")
+    _attend("dspark_cache_attend_tree", lib().dspark_cache_attend_tree, cache, layer, q, offsets, lead, max_new, anc, scale,
+            out, lse, shared, ws, status, stream)
+
+
+def dspark_tree_merge(tokens, prefix_len, S: int, counts, offsets, ver_tokens, parent, status=None, stream=None):
+    """The chains [R*S, K] of each request as one tree, equal beginnings taken once; prefix_len [R*S]: the
+    tokens of each that count (None: all)."""
+    what = "dspark_tree_merge"
+    if tokens.dim() != 2 or S < 1 or tokens.shape[0] % S:
+        raise ValueError(f"{what}: tokens must be [R*S, K] with S = {S}")
+    R, K = tokens.shape[0] // S, tokens.shape[1]
+    if prefix_len is not None:
+        _shape(prefix_len, (R * S,), f"{what}: prefix_len")
+    _shape(counts, (R,), f"{what}: counts")
+    _shape(offsets, (R + 1,), f"{what}: offsets")
+    if ver_tokens.numel() < R * S * K or parent.numel() < R * S * K + R:
+        raise ValueError(f"{what}: ver_tokens and parent must have room for {R * S * K} drafts of {R} requests")
+    st = _on(tokens, what, stream, (tokens, prefix_len, counts, offsets, ver_tokens, parent), (status,))
+    _check(lib().dspark_tree_merge(_p(tokens), _p(prefix_len), R, S, K, _p(counts), _p(offsets), _p(ver_tokens), _p(parent),
+                                   _p(status), st))
+
+
+def dspark_tree_plan(parent, offsets, lead: int, max_new: int, depth, anc, status=None, stream=None):
+    """Depth [rows] int32 and visible nodes [rows] int64 of a step's rows, from their parents."""
+    what, n = "dspark_tree_plan", parent.numel()
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError(f"{what}: offsets must be [R+1]")
+    if depth.numel() < n or anc.numel() < n:
+        raise ValueError(f"{what}: depth and anc must have an entry for each of {n} rows")
+    st = _on(parent, what, stream, (parent, offsets, depth), (status,), (anc,))
+    _check(lib().dspark_tree_plan(_p(parent), n, _p(offsets), lead, offsets.shape[0] - 1, max_new, _p(depth), _p(anc),
+                                  _p(status), st))
+
+
+def dspark_accept_tree(ver_tokens, offsets, parent, target, accept_len, path, next_prev0, out_tokens=None, status=None,
+                       stream=None):
+    """Greedy verification of trees: the accepted path's nodes [R, K], its length, and the bonus token."""
+    what = "dspark_accept_tree"
+    if path.dim() != 2:
+        raise ValueError(f"{what}: path must be [R, K]")
+    (R, K), n = path.shape, ver_tokens.numel()
+    _shape(offsets, (R + 1,), f"{what}: offsets")
+    _shape(accept_len, (R,), f"{what}: accept_len")
+    _shape(next_prev0, (R,), f"{what}: next_prev0")
+    if out_tokens is not None:
+        _shape(out_tokens, (R, K + 1), f"{what}: out_tokens")
+    if parent.numel() < n + R or target.numel() < n + R:
+        raise ValueError(f"{what}: parent and target must have an entry for each of {n} drafts and {R} first nodes")
+    st = _on(offsets, what, stream, (ver_tokens, offsets, parent, target, accept_len, path, next_prev0, out_tokens), (status,))
+    _check(lib().dspark_accept_tree(_p(ver_tokens), n, _p(offsets), _p(parent), _p(target), R, K, _p(accept_len), _p(path),
+                                    _p(next_prev0), _p(out_tokens), _p(status), st))
+
+
+def dspark_cache_keep_path(cache: PagedCache, path, accept_len, lead: int, granted=None, status=None, stream=None):
+    """The accepted path's K and V moved together, every layer's; dspark_pages_commit follows."""
+    what = "dspark_cache_keep_path"
+    if path.dim() != 2 or path.shape[0] > cache.rows:
+        raise ValueError(f"{what}: path must be [R, K] with R at most {cache.rows}")
+    R, K = path.shape
+    _shape(accept_len, (R,), f"{what}: accept_len")
+    if granted is not None:
+        _shape(granted, (R,), f"{what}: granted")
+    st = _on(cache, what, stream, (path, accept_len, granted), (status,))
+    _check(lib().dspark_cache_keep_path(cache._ref, _p(path), K, _p(accept_len), _p(granted), lead, R, _p(status), st))
+
+
+def rotary_frequencies(dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, original: float = 0.0,
+                       low: float = 0.0, high: float = 0.0) -> np.ndarray:
+    """Radians a token of each pair of `dim` dims (start-up, host): scaling "none", "linear", "bands" or
+    "ramp" (include/dspark.h, dspark_rotary_frequencies)."""
+    if scaling not in ROTARY_SCALING:
+        raise ValueError(f"rotary_frequencies: scaling must be one of {sorted(ROTARY_SCALING)}")
+    freq = np.zeros(max(dim // 2, 1), dtype=np.float64)
+    _check(lib().dspark_rotary_frequencies(ROTARY_SCALING[scaling], dim, base, factor, original, low, high,
+                                           freq.ctypes.data_as(ctypes.c_void_p)))
+    return freq
+
+
+class Rotary:
+    """Rotary positions of `dim` dims of a head from dim `first` on (include/dspark.h, dspark_rotary_t):
+    frequencies from `base` and `scaling` (rotary_frequencies) or as given in `freq`, radians a token."""
+
+    def __init__(self, dim: int, base: float = 10000.0, first: int = 0, interleaved: bool = False, attention: float = 1.0,
+                 scaling: str = "none", factor: float = 1.0, original: float = 0.0, low: float = 0.0, high: float = 0.0,
+                 freq=None, device="cuda"):
+        torch = _torch()
+        self.freq = rotary_frequencies(dim, base, scaling, factor, original, low, high) if freq is None else \
+            np.ascontiguousarray(freq, dtype=np.float64)
+        if self.freq.shape != (dim // 2,):
+            raise ValueError(f"Rotary: {dim} dims have {dim // 2} frequencies, got {list(self.freq.shape)}")
+        turns = np.zeros(dim // 2, dtype=np.uint64)
+        _check(lib().dspark_rotary_turns(self.freq.ctypes.data_as(ctypes.c_void_p), dim // 2,
+                                         turns.ctypes.data_as(ctypes.c_void_p)))
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+        self.dim, self.first, self.interleaved, self.attention = dim, first, bool(interleaved), float(attention)
+        self.handle = dspark_rotary_t(_p(self.turns), dim, first, int(self.interleaved), self.attention)
+        self._ref = ctypes.byref(self.handle)
+
+
+def dspark_cache_append_rotary(cache: PagedCache, layer: int, rotary: Rotary, q, q_out, k_new, v_new, offsets, lead: int,
+                               max_new: int, depth=None, status=None, stream=None):
+    """dspark_cache_append with queries (into q_out, which may be q) and keys turned to their positions:
+    row j of a request by its length plus j, or plus depth[row] (a tree's rows)."""
+    what = "dspark_cache_append_rotary"
+    R = _offsets_rows(cache, offsets, what)
+    H = q.shape[1] if q.dim() == 3 else 0
+    qs, os_ = _packed(cache, q, H, f"{what}: q"), _packed(cache, q_out, H, f"{what}: q_out")
+    ks = _packed(cache, k_new, cache.n_kv_heads, f"{what}: k_new")
+    vs = _packed(cache, v_new, cache.n_kv_heads, f"{what}: v_new")
+    n = k_new.shape[0]
+    if v_new.shape[0] != n or q.shape[0] != n or q_out.shape[0] != n:
+        raise ValueError(f"{what}: q, q_out, k_new and v_new must have as many rows")
+    if depth is not None and depth.numel() < n:
+        raise ValueError(f"{what}: depth has {depth.numel()} entries for {n} rows")
+    st = _on(cache, what, stream, (offsets, depth), (q, q_out, k_new, v_new, rotary.turns, status))
+    _check(lib().dspark_cache_append_rotary(cache._ref, layer, rotary._ref, _p(q), qs, H, _p(q_out), os_, _p(k_new), ks,
+                                            _p(v_new), vs, n, _p(offsets), lead, R, max_new, _p(depth), _p(status), st))
+
+
+class History:
+    """Which tokens each request has been given and has answered (include/dspark.h, dspark_history_t): `seen`
+    [rows, 2, words] and `count` [rows, V] int32.  Buffers that are not given are allocated, empty."""
+
+    def __init__(self, rows: int, V: int, seen=None, count=None, device="cuda"):
+        torch = _torch()
+        if rows < 0 or V < 1:
+            raise ValueError("History: rows and V must be positive")
+        for t in (seen, count):
+            if t is not None:
+                device = t.device
+        device = torch.device(device)
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        shapes = dict(seen=(rows, 2, int(lib().dspark_history_words(V))), count=(rows, V))
+        for name, given in (("seen", seen), ("count", count)):
+            t = torch.zeros(shapes[name], dtype=torch.int32, device=device) if given is None else given
+            if tuple(t.shape) != shapes[name] or t.dtype != torch.int32 or not t.is_contiguous() or t.device != device:
+                raise ValueError(f"History: {name} must be contiguous int32 {list(shapes[name])} on {device}, "
+                                 f"got {t.dtype} {list(t.shape)} on {t.device}")
+            setattr(self, name, t)
+        self.rows, self.V, self.device = rows, V, device
+        self.handle = dspark_history_t(_p(self.seen), _p(self.count), rows, V)
+        self._ref = ctypes.byref(self.handle)
+
+
+def dspark_history_clear(history: History, rows=None, status=None, stream=None):
+    """History rows (all of them where `rows` is None) emptied."""
+    n = history.rows if rows is None else rows.numel()
+    st = _on(history, "dspark_history_clear", stream, (rows,), (status,))
+    _check(lib().dspark_history_clear(history._ref, _p(rows), n, _p(status), st))
+
+
+def dspark_history_add(history: History, tokens, answered: bool, rows=None, status=None, stream=None):
+    """Tokens [n, width] entered into rows[i] (i where `rows` is None): a prompt's, or answered ones, such as an
+    acceptance's out_tokens.  Negative entries are none."""
+    what = "dspark_history_add"
+    if tokens.dim() != 2:
+        raise ValueError(f"{what}: tokens must be [n, width]")
+    n, width = tokens.shape
+    if rows is not None:
+        _shape(rows, (n,), f"{what}: rows")
+    st = _on(history, what, stream, (tokens, rows), (status,))
+    _check(lib().dspark_history_add(history._ref, _p(tokens), n, width, _p(rows), int(answered), _p(status), st))
+
+
+def target_workspace(n_rows: int, V: int, device="cuda"):
+    """Workspace of dspark_target_tokens for up to n_rows rows of up to V tokens."""
+    nbytes = int(lib().dspark_target_workspace_bytes(n_rows, V))
+    return _torch().empty((nbytes + 15) // 16 * 4, dtype=_torch().int32, device=device)
+
+
+def _logit_rows(t, like, what: str):
+    if t.dim() != 2 or (like is not None and (t.shape != like.shape or t.dtype != like.dtype)):
+        raise ValueError(f"{what} must be [rows, V]" + ("" if like is None else " as logits are"))
+    if t.numel() and t.stride(1) != 1:
+        raise ValueError(f"{what}: each row's values must be densely packed")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def dspark_target_tokens(logits, offsets, lead: int, max_new: int, target, history: Optional[History] = None,
+                         penalties=(None, None, None), node_tokens=None, anc=None, bias=None, allowed=None, allowed_row=None,
+                         adjusted=None, ws=None, status=None, stream=None):
+    """The target's choice at each row of a step from its logits [rows, V], after penalties (repetition,
+    presence, frequency: float32 [R] or None each), biases (bias_off [R+1], bias_tok, bias_val) and the masks
+    allowed [n, words] (row allowed_row[t] binds row t).  `adjusted` [rows, V] receives the processed logits."""
+    what, torch = "dspark_target_tokens", _torch()
+    dtypes = {torch.float32: DSPARK_F32, torch.bfloat16: DSPARK_BF16, torch.float16: DSPARK_F16}
+    if logits.dtype not in dtypes:
+        raise ValueError(f"{what}: logits must be float32, bfloat16 or float16, got {logits.dtype}")
+    stride = _logit_rows(logits, None, f"{what}: logits")
+    out_stride = 0 if adjusted is None else _logit_rows(adjusted, logits, f"{what}: adjusted")
+    n_rows, V = logits.shape
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError(f"{what}: offsets must be [R+1]")
+    R = offsets.shape[0] - 1
+    if target.numel() < n_rows or (anc is not None and anc.numel() < n_rows) or \
+            (allowed_row is not None and allowed_row.numel() < n_rows):
+        raise ValueError(f"{what}: target, anc and allowed_row must have an entry for each of {n_rows} rows")
+    penalties = (None, None, None) if penalties is None else tuple(penalties)
+    off = tok = val = None
+    if bias is not None:
+        off, tok, val = bias
+        _shape(off, (R + 1,), f"{what}: bias_off")
+        _shape(val, tuple(tok.shape), f"{what}: bias_val")
+    for t in (*penalties, val):
+        if t is not None and (t.dtype is not torch.float32 or not t.is_contiguous()):
+            raise ValueError(f"{what}: penalties and bias_val must be contiguous float32")
+    for t in penalties:
+        if t is not None:
+            _shape(t, (R,), f"{what}: penalties")
+    if allowed is not None and (allowed.dim() != 2 or allowed.dtype is not torch.int32 or
+                                (allowed.numel() and allowed.stride(1) != 1)):
+        raise ValueError(f"{what}: allowed must be int32 [masks, words] with densely packed rows")
+    if history is not None and history.device != logits.device:
+        raise ValueError(f"{what}: the history is on {history.device}, logits on {logits.device}")
+    st = _on(logits, what, stream, (offsets, target, node_tokens, off, tok, allowed_row),
+             (*penalties, val, allowed, adjusted, ws, status), (anc,))
+    call = dspark_target_t(
+        _p(logits), stride, n_rows, V, dtypes[logits.dtype], R, lead, max_new, _p(offsets),
+        None if history is None else ctypes.addressof(history.handle), *(_p(t) for t in penalties), _p(node_tokens), _p(anc),
+        _p(off), _p(tok), _p(val), _p(allowed), _p(allowed_row),
+        0 if allowed is None else (allowed.stride(0) if allowed.shape[0] > 1 else allowed.shape[1]),
+        0 if node_tokens is None else node_tokens.numel(), 0 if tok is None else tok.numel(),
+        0 if allowed is None else allowed.shape[0], 0, _p(target), _p(adjusted), out_stride)
+    _check(lib().dspark_target_tokens(ctypes.byref(call), _p(status), _p(ws), _ws_bytes(ws), st))
 
 
 def dspark_set_launch_mode(mode: int):

@@ -11,7 +11,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdspark.so")
 SOURCES = ["chain.hip", "cand.hip", "sched.hip", "step.hip", "accept.hip", "api.hip",
-           "pages.hip", "append.hip", "attend.hip", "cache_api.hip"]
+           "pages.hip", "append.hip", "attend.hip", "cache_api.hip", "tree.hip", "rotary.hip", "target.hip",
+           "target_api.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

@@ -25,7 +25,8 @@
 // matrix and vector units are, and the keys come to LDS once for all waves
 // (attend_wide_kernel).  Each kernel says what it reaches.
 //
-// Masks: only blocks that reach past a column's last key are masked.  What lies in masked
+// Masks: only blocks that reach past a column's last key are masked; for trees, those that reach
+// past the request's tokens, by the bits of each row's word.  What lies in masked
 // places has no say whatever it is: scores are replaced, V past the end is cleared, and a
 // value of V that is not a number in such a block is taken out of the product and handed
 // to the columns that see it by counting (see add_special).
@@ -418,6 +419,7 @@ template <class E>
 __device__ __forceinline__ void store_row(const AttendArgs& a, int f, int h, int c8, float m, float l,
                                           const float (&acc)[8]) {
     const int row = f / a.G, head = h * a.G + f % a.G;
+    if (a.anc && a.anc[row] == 0) l = 0.f;  // a row that sees nothing, its request's tokens neither
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // the one rounding to 16 bits of the result
@@ -579,8 +581,16 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
+// Trees: which of the 64 keys from pos on a row sees (bit i: key pos + i), from its request's tokens
+// and the nodes of its word behind them.
+__device__ __forceinline__ uint64_t tree_keys(uint64_t word, int pos, int tokens) {
+    const int past = pos - tokens;
+    if (past >= 0) return past < 64 ? word >> past : 0;
+    return past > -64 ? word << -past | ((1ull << -past) - 1) : ~0ull;
+}
+
 // A worker's way through its units: the segment at hand, and the item it belongs to.
-template <int kSet, int kTile, int kUnit>
+template <int kSet, int kTile, int kUnit, bool kTree>
 struct Cursor {
     uint32_t u, u_end;
     uint32_t item_u0 = 0, item_u1 = 0;  // units of the item
@@ -620,9 +630,17 @@ struct Cursor {
         u += unit1 - unit0;
         return u < u_end;
     }
-    // The last key that the columns of query row f / G see.
+    // The last key that the columns of query row f / G see, of those that are the launch's (a tree's
+    // row: may see), and the last one of those that they all see.
     __device__ __forceinline__ int last_of(const AttendArgs& a, int f) const {
-        return kSet ? q.ke - 1 : q.ln + f / a.G - q.start;
+        return kSet || kTree ? q.ke - 1 : q.ln + f / a.G - q.start;
+    }
+    __device__ __forceinline__ int solid_of(const AttendArgs& a, int f) const {
+        return kTree ? q.ln - 1 : last_of(a, f);
+    }
+    // A tree's row's nodes (those that the request has).
+    __device__ __forceinline__ uint64_t nodes_of(const AttendArgs& a, int f) const {
+        return kTree ? a.anc[f / a.G] & (q.n < 64 ? (1ull << q.n) - 1 : ~0ull) : 0;
     }
 };
 
@@ -646,7 +664,7 @@ __device__ __forceinline__ void load_q(const AttendArgs& a, s16x8 (&qf)[D / 16],
 // of four waves at each of 2048 segments.  Four single tokens, 1750 tokens in all: 9 us, of
 // which the bytes would take 1.3; the others are loads that wait for each other, from the
 // requests' rows to their page ids, keys, values and the parts.
-template <class E, int D, int kSet, int kTiles>
+template <class E, int D, int kSet, int kTiles, bool kTree>
 __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs a) {
     constexpr int NT = D / 32, NC = D / 16;
     constexpr int kKeyWaves = 4 / kTiles;
@@ -670,13 +688,14 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
     const int head_shift = __builtin_ctz(D) + a.page_shift;          // a head's elements in a page
     const int swapped = (col & 3) | ((col & 4) << 1) | ((col & 8) >> 1);  // key of this lane in its block of 16
 
-    Cursor<kSet, 32 * kTiles, kUnit> cur(split, blockIdx.x, tid == 0);
+    Cursor<kSet, 32 * kTiles, kUnit, kTree> cur(split, blockIdx.x, tid == 0);
     s16x8 qf[NC], kf[NC], vf[NT][2];
     f32x16 o[NT];
     PageIds pages;
     const uint16_t *kp[2], *vp[2];
     bool have[2], bad_page = false;
     int pos, pos_end, last, first_last;
+    uint64_t nodes = 0;
 
     // The two blocks of 16 keys at position p: where K and V lie, and whether they are there.
     const auto locate = [&](int p, bool(&there)[2]) {
@@ -712,7 +731,8 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
         const int f = cur.f0 + min(sub * 32 + col, cur.nf - 1);
         load_q<D>(a, qf, f, cur.h, half);
         last = cur.last_of(a, f);               // the column's last key
-        first_last = cur.last_of(a, cur.f0);  // the earliest of them
+        first_last = cur.solid_of(a, cur.f0);  // the earliest of them
+        nodes = cur.nodes_of(a, f);
         pos = cur.q.kb + (int)(cur.unit0 * kUnit) + key_wave * 32;
         pos_end = sub * 32 < cur.nf ? min(cur.q.ke, cur.q.kb + (int)(cur.unit1 * kUnit)) : 0;
         if (pos < pos_end)
@@ -725,6 +745,12 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
         load_k();
         __builtin_amdgcn_sched_barrier(0);  // K first, as in the loop: its waits count on this order
         load_v();
+    };
+
+    // Whether this lane's column sees the key of its score j of the 32 from position p on; a tree's
+    // by the bits of tree_keys, from the lane's first key on.
+    const auto sees = [&](uint32_t keys, int p, int j) {
+        return kTree ? (keys >> ((j / 8) * 16 + j % 8) & 1) != 0 : p + (j / 8) * 16 + half * 8 + j % 8 <= last;
     };
 
     // What joining a finished segment's waves needs, while the next segment is at hand.
@@ -806,9 +832,10 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
             }
             const bool masked = !kFast && (pos + 31 > first_last || !have[0] || !have[1]);
             if (masked) {
+                const uint32_t keys = kTree ? (uint32_t)tree_keys(nodes, pos, cur.q.ln) >> (half * 8) : 0;
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    if (pos + (j / 8) * 16 + half * 8 + j % 8 > last || !have[j / 8]) s[j] = -kInf;
+                    if (!sees(keys, pos, j) || !have[j / 8]) s[j] = -kInf;
             }
             float mx = s[0];
 #pragma unroll
@@ -873,15 +900,15 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
             pages.settle();
             for (pos = special_from; pos < pos_end; pos += kUnit) {
                 locate(pos, have);
-                s16x8 sees[2];
+                s16x8 there[2];
+                const uint32_t keys = kTree ? (uint32_t)tree_keys(nodes, pos, cur.q.ln) >> (half * 8) : 0;
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    sees[j / 8][j % 8] =
-                        pos + (j / 8) * 16 + half * 8 + j % 8 <= last && have[j / 8] ? (short)E::kOne : (short)0;
+                    there[j / 8][j % 8] = sees(keys, pos, j) && have[j / 8] ? (short)E::kOne : (short)0;
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
                     add_special<E>(o[t], *(const s16x8*)(vp[0] + (t * 32 + col) * 16 + half * 8),
-                                   *(const s16x8*)(vp[1] + (t * 32 + col) * 16 + half * 8), sees[0], sees[1]);
+                                   *(const s16x8*)(vp[1] + (t * 32 + col) * 16 + half * 8), there[0], there[1]);
             }
         }
         ms = m == -kInf ? -kInf : m * a.scale_log2 - E::kRaise;
@@ -924,7 +951,7 @@ struct Wide {
     static constexpr int kBlock = 16 * D;           // elements of a block's K or V
 };
 
-template <class E, int D, int kSet>
+template <class E, int D, int kSet, bool kTree>
 __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::kPerCu) void attend_wide_kernel(AttendArgs a) {
     typedef Wide<D> W;
     constexpr int NT = D / 32, NC = D / 16;
@@ -950,7 +977,7 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
     const int key = lane & 15, k_from = (lane >> 4) * 128 + ((key & 3) | ((key & 4) << 1) | ((key & 8) >> 1)) * 8;
     const int v_from = lane / 2 * 16 + ((lane ^ (lane >> 4)) & 1) * 8, v_at = (col * 2 + (half ^ ((col >> 3) & 1))) * 16;
 
-    Cursor<kSet, W::kTile, W::kUnit> cur(split, me, tid == 0);
+    Cursor<kSet, W::kTile, W::kUnit, kTree> cur(split, me, tid == 0);
     do {
         cur.look(a, split, n, s_cum);
         const Work& q = cur.q;
@@ -959,9 +986,10 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
         s16x8 qf[NC];
         load_q<D>(a, qf, f, h, half);
         // The column's last key; the wave's earliest and latest of them, and the tile's latest.
-        const int last = cur.last_of(a, f), first_last = cur.last_of(a, f0 + min(wave * 32, nf - 1));
+        const int last = cur.last_of(a, f), first_last = cur.solid_of(a, f0 + min(wave * 32, nf - 1));
+        const uint64_t nodes = cur.nodes_of(a, f);
         const int wave_end = wave * 32 >= nf ? 0 : cur.last_of(a, f0 + min(wave * 32 + 31, nf - 1)) + 1;
-        const int tile_end = cur.last_of(a, f0 + nf - 1) + 1, tile_first = cur.last_of(a, f0);
+        const int tile_end = cur.last_of(a, f0 + nf - 1) + 1, tile_first = cur.solid_of(a, f0);
 
         f32x16 o[NT];
 #pragma unroll
@@ -1046,10 +1074,11 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
                 const int4 have = *(const int4*)s_have[t & 3];
                 int left = last - (pos0 + t * W::kUnit) - half * 8;
                 asm volatile("" : "+v"(left));  // so that no key's number takes a register in the loop
+                const uint64_t keys = kTree ? tree_keys(nodes, pos0 + t * W::kUnit, q.ln) >> (half * 8) : 0;
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                    const int there = j < 8 ? have.x : j < 16 ? have.y : j < 24 ? have.z : have.w;
-                    if ((j / 8) * 16 + j % 8 > left || !there) s[j / 16][j % 16] = -kInf;
+                    const int there = j < 8 ? have.x : j < 16 ? have.y : j < 24 ? have.z : have.w, key = (j / 8) * 16 + j % 8;
+                    if ((kTree ? !(keys >> key & 1) : key > left) || !there) s[j / 16][j % 16] = -kInf;
                 }
             }
             float mx = s[0][0];
@@ -1180,9 +1209,12 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
                 s16x8 sees[2];
                 int left = last - pos - half * 8;
                 asm volatile("" : "+v"(left));
+                const uint64_t keys = kTree ? tree_keys(nodes, pos, q.ln) >> (half * 8) : 0;
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    sees[j / 8][j % 8] = (j / 8) * 16 + j % 8 <= left && have[j / 8] ? (short)E::kOne : (short)0;
+                for (int j = 0; j < 16; ++j) {
+                    const int key = (j / 8) * 16 + j % 8;
+                    sees[j / 8][j % 8] = (kTree ? (keys >> key & 1) != 0 : key <= left) && have[j / 8] ? (short)E::kOne : (short)0;
+                }
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
                     add_special<E>(o[t], *(const s16x8*)(a.v + at[0] + t * 512 + col * 16 + half * 8),
@@ -1251,23 +1283,23 @@ __global__ __launch_bounds__(kT) void attend_join_shared_kernel(AttendArgs a) {
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
-template <class E, int D, int kSet>
+template <class E, int D, int kSet, bool kTree>
 hipError_t run_set(const AttendArgs& a, hipStream_t s) {
     const size_t lds = kSet ? (a.n_groups + 1) * sizeof(uint32_t)
                             : (a.R + 1) * sizeof(uint32_t) + std::min(a.R, kCached) * sizeof(Request);
     if (a.tile[kSet] == Wide<D>::kTile)
-        hipLaunchKernelGGL((attend_wide_kernel<E, D, kSet>), dim3(a.workers[kSet]), dim3(Wide<D>::kThreads), lds, s, a);
+        hipLaunchKernelGGL((attend_wide_kernel<E, D, kSet, kTree>), dim3(a.workers[kSet]), dim3(Wide<D>::kThreads), lds, s, a);
     else if (a.tile[kSet] == 64)
-        hipLaunchKernelGGL((attend_kernel<E, D, kSet, 2>), dim3(a.workers[kSet]), dim3(kT), lds, s, a);
+        hipLaunchKernelGGL((attend_kernel<E, D, kSet, 2, kTree>), dim3(a.workers[kSet]), dim3(kT), lds, s, a);
     else
-        hipLaunchKernelGGL((attend_kernel<E, D, kSet, 1>), dim3(a.workers[kSet]), dim3(kT), lds, s, a);
+        hipLaunchKernelGGL((attend_kernel<E, D, kSet, 1, kTree>), dim3(a.workers[kSet]), dim3(kT), lds, s, a);
     return hipGetLastError();
 }
 
 template <class E, int D>
 hipError_t run(const AttendArgs& a, hipStream_t s) {
-    hipError_t e = a.n_groups ? run_set<E, D, 1>(a, s) : hipSuccess;
-    if (e == hipSuccess) e = run_set<E, D, 0>(a, s);
+    hipError_t e = a.n_groups ? run_set<E, D, 1, false>(a, s) : hipSuccess;  // (all of its rows see all of its keys)
+    if (e == hipSuccess) e = a.anc ? run_set<E, D, 0, true>(a, s) : run_set<E, D, 0, false>(a, s);
     if (e != hipSuccess) return e;
     if (a.n_groups)
         hipLaunchKernelGGL(attend_join_shared_kernel<E>,

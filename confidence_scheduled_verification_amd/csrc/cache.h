@@ -83,6 +83,7 @@ struct AttendArgs {
     const int32_t* table;
     const int32_t* len;
     const int32_t* offsets;
+    const uint64_t* anc;  // trees: the nodes that each row sees; else NULL
     int lead, R, rows, max_new, H, Hkv, G, D, dtype, page, page_shift, n_pages, width;
     float scale_log2;  // the scores' scale times log2(e)
     int n_groups, shared_width;

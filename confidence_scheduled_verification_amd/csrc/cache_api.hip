@@ -8,6 +8,7 @@
 
 #include "cache.h"
 #include "dspark.h"
+#include "tree.h"
 
 using dspark::fail;
 using dspark::hip_fail;
@@ -74,6 +75,112 @@ int done(hipError_t e, const char* who) { return e == hipSuccess ? DSPARK_OK : h
 
 size_t layer_elems(const dspark_cache_t* c) {
     return (size_t)c->n_pages * c->n_kv_heads * c->page_size * c->head_dim;
+}
+
+// The rows of an append, checked; any: there are some.
+int append_args(const dspark_cache_t* c, int layer, const void* k_new, int64_t k_stride, const void* v_new,
+                int64_t v_stride, int n_rows, const int32_t* offsets, int lead, int R, int max_new, uint32_t* status,
+                const char* who, dspark::AppendArgs& a, bool& any) {
+    int rc = check_data(c, who);
+    if (rc != DSPARK_OK || (rc = check_requests(c, R, lead, who)) != DSPARK_OK) return rc;
+    if (layer < 0 || layer >= c->layers) return fail(DSPARK_ERANGE, "%s: layer %d outside [0, %d)", who, layer, c->layers);
+    if (n_rows < 0 || max_new < 0) return fail(DSPARK_ERANGE, "%s: n_rows %d, max_new %d", who, n_rows, max_new);
+    if (R == 0 || n_rows == 0 || max_new == 0) return DSPARK_OK;
+    if ((rc = check_rows(k_new, k_stride, c->n_kv_heads, c->head_dim, who, "k_new")) != DSPARK_OK ||
+        (rc = check_rows(v_new, v_stride, c->n_kv_heads, c->head_dim, who, "v_new")) != DSPARK_OK)
+        return rc;
+    if (!offsets) return fail(DSPARK_EINVAL, "%s: offsets is NULL", who);
+    const size_t at = layer * layer_elems(c);
+    a = dspark::AppendArgs{(const uint16_t*)k_new, (const uint16_t*)v_new, k_stride, v_stride, (uint16_t*)c->k + at,
+                           (uint16_t*)c->v + at, c->table, c->len, c->ref, offsets, lead, R, n_rows, max_new,
+                           c->n_kv_heads, c->head_dim, c->page_size, __builtin_ctz(c->page_size), c->n_pages, c->width,
+                           status};
+    any = true;
+    return DSPARK_OK;
+}
+
+// Whether rows of `used` elements at q and at out, as far apart from one another, lie between each other
+// without touching, as parts of the same wider rows do.
+bool interleaves(uintptr_t q, uintptr_t out, int64_t q_stride, int64_t out_stride, int64_t used) {
+    if (q_stride != out_stride) return false;
+    const int64_t row = q_stride * 2, apart = (((int64_t)(out - q)) % row + row) % row;
+    return apart >= used * 2 && row - apart >= used * 2;
+}
+
+int attend(const dspark_cache_t* c, int layer, const void* q, int64_t q_stride, int n_rows, int H,
+           const int32_t* offsets, int lead, int R, int max_new, const uint64_t* anc, float scale, int n_groups,
+           const int32_t* group_off, const int32_t* shared_table, int shared_width, const int32_t* shared_pages,
+           void* out, int64_t out_stride, float* lse, uint32_t* status, void* ws, size_t ws_bytes, void* stream,
+           const char* who) {
+    int rc = check_data(c, who);
+    if (rc != DSPARK_OK || (rc = check_requests(c, R, lead, who)) != DSPARK_OK) return rc;
+    if (layer < 0 || layer >= c->layers) return fail(DSPARK_ERANGE, "%s: layer %d outside [0, %d)", who, layer, c->layers);
+    if (n_rows < 0 || max_new < 0) return fail(DSPARK_ERANGE, "%s: n_rows %d, max_new %d", who, n_rows, max_new);
+    if (H < 1 || H % c->n_kv_heads || H > 65535)
+        return fail(DSPARK_EINVAL, "%s: %d query heads over %d key heads", who, H, c->n_kv_heads);
+    if (!(scale > 0.f) || !isfinite(scale * 1.44269504f))
+        return fail(DSPARK_ERANGE, "%s: scale %g must be positive and finite", who, (double)scale);
+    if (n_groups < 0 || n_groups > DSPARK_CACHE_MAX_GROUPS)
+        return fail(DSPARK_EUNSUPPORTED, "%s: %d groups, at most %d are supported", who, n_groups, DSPARK_CACHE_MAX_GROUPS);
+    if (n_groups > 0 && (!group_off || !shared_table || !shared_pages || shared_width < 1))
+        return fail(DSPARK_EINVAL, "%s: groups need group_off, shared_table and shared_pages", who);
+    if (R == 0 || n_rows == 0 || max_new == 0) return DSPARK_OK;
+    if ((rc = check_rows(q, q_stride, H, c->head_dim, who, "q")) != DSPARK_OK ||
+        (rc = check_rows(out, out_stride, H, c->head_dim, who, "out")) != DSPARK_OK)
+        return rc;
+    if (!offsets) return fail(DSPARK_EINVAL, "%s: offsets is NULL", who);
+    const long long tokens = (long long)c->width * c->page_size, shared_tokens = (long long)shared_width * c->page_size;
+    dspark::AttendArgs a{};
+    a.lead = lead;
+    a.R = R;
+    a.rows = (int)std::min<long long>(n_rows, (long long)R * max_new);  // rows past those belong to no request
+    a.max_new = std::min(max_new, n_rows);                              // (more would not lie in the tensors)
+    a.H = H;
+    a.Hkv = c->n_kv_heads;
+    a.G = H / c->n_kv_heads;
+    a.D = c->head_dim;
+    a.n_groups = n_groups;
+    dspark::attend_forms(a, dspark::num_cu());
+    // The work is numbered with 32 bits: columns, the units of the requests' own keys and those of
+    // the groups', as many as these sizes allow, and the joining launch's grid.
+    const auto tiles = [&](int set, long long columns) { return (columns + a.tile[set] - 1) / a.tile[set]; };
+    const auto units = [&](int set, long long keys) { return (long long)a.Hkv * (keys / a.unit[set] + 1); };
+    const bool fits = (long long)a.rows * H <= INT32_MAX - 1023 && tokens <= dspark::kAttendMaxTokens &&
+                      std::min(R * tiles(0, (long long)a.max_new * a.G), R + tiles(0, (long long)a.rows * a.G)) *
+                              units(0, tokens) <= INT32_MAX;
+    const bool groups_fit =
+        !n_groups || (shared_tokens <= dspark::kAttendMaxTokens &&
+                      (n_groups + tiles(1, (long long)a.rows * a.G)) * units(1, shared_tokens) <= INT32_MAX &&
+                      (long long)a.max_new * a.G * (a.D / 8) <= 65535ll * dspark::kAttendJoinItems);
+    if (!fits || !groups_fit)
+        return fail(DSPARK_EUNSUPPORTED, "%s: %d rows of %d heads over up to %lld tokens are too many for one call", who,
+                    n_rows, H, tokens);
+    if ((rc = check_ws(ws, ws_bytes, dspark::attend_ws_bytes(R, H, a.D, a.rows, n_groups), who)) != DSPARK_OK) return rc;
+    const size_t at = layer * layer_elems(c);
+    a.q = (const uint16_t*)q;
+    a.q_stride = q_stride;
+    a.out_stride = out_stride;
+    a.k = (const uint16_t*)c->k + at;
+    a.v = (const uint16_t*)c->v + at;
+    a.table = c->table;
+    a.len = c->len;
+    a.offsets = offsets;
+    a.anc = anc;
+    a.dtype = c->dtype;
+    a.page = c->page_size;
+    a.page_shift = __builtin_ctz(c->page_size);
+    a.n_pages = c->n_pages;
+    a.width = c->width;
+    a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    a.shared_width = shared_width;
+    a.group_off = group_off;
+    a.shared_table = shared_table;
+    a.shared_pages = shared_pages;
+    a.out = (uint16_t*)out;
+    a.lse = lse;
+    a.status = status;
+    dspark::attend_ws_layout(a, ws);
+    return done(dspark::launch_attend(a, (hipStream_t)stream), who);
 }
 
 }  // namespace
@@ -153,20 +260,10 @@ int dspark_cache_append(const dspark_cache_t* c, int layer, const void* k_new, i
                         int64_t v_stride, int n_rows, const int32_t* offsets, int lead, int R, int max_new,
                         uint32_t* status, void* stream) {
     const char* who = "cache_append";
-    int rc = check_data(c, who);
-    if (rc != DSPARK_OK || (rc = check_requests(c, R, lead, who)) != DSPARK_OK) return rc;
-    if (layer < 0 || layer >= c->layers) return fail(DSPARK_ERANGE, "%s: layer %d outside [0, %d)", who, layer, c->layers);
-    if (n_rows < 0 || max_new < 0) return fail(DSPARK_ERANGE, "%s: n_rows %d, max_new %d", who, n_rows, max_new);
-    if (R == 0 || n_rows == 0 || max_new == 0) return DSPARK_OK;
-    if ((rc = check_rows(k_new, k_stride, c->n_kv_heads, c->head_dim, who, "k_new")) != DSPARK_OK ||
-        (rc = check_rows(v_new, v_stride, c->n_kv_heads, c->head_dim, who, "v_new")) != DSPARK_OK)
-        return rc;
-    if (!offsets) return fail(DSPARK_EINVAL, "%s: offsets is NULL", who);
-    const size_t at = layer * layer_elems(c);
-    const dspark::AppendArgs a{(const uint16_t*)k_new, (const uint16_t*)v_new, k_stride, v_stride,
-                               (uint16_t*)c->k + at, (uint16_t*)c->v + at, c->table, c->len, c->ref, offsets, lead, R, n_rows,
-                               max_new, c->n_kv_heads, c->head_dim, c->page_size, __builtin_ctz(c->page_size),
-                               c->n_pages, c->width, status};
+    dspark::AppendArgs a;
+    bool any = false;
+    const int rc = append_args(c, layer, k_new, k_stride, v_new, v_stride, n_rows, offsets, lead, R, max_new, status, who, a, any);
+    if (rc != DSPARK_OK || !any) return rc;
     return done(dspark::launch_append(a, (hipStream_t)stream), who);
 }
 
@@ -180,75 +277,76 @@ int dspark_cache_attend(const dspark_cache_t* c, int layer, const void* q, int64
                         const int32_t* group_off, const int32_t* shared_table, int shared_width,
                         const int32_t* shared_pages, void* out, int64_t out_stride, float* lse, uint32_t* status,
                         void* ws, size_t ws_bytes, void* stream) {
-    const char* who = "cache_attend";
+    return attend(c, layer, q, q_stride, n_rows, H, offsets, lead, R, max_new, nullptr, scale, n_groups, group_off,
+                  shared_table, shared_width, shared_pages, out, out_stride, lse, status, ws, ws_bytes, stream,
+                  "cache_attend");
+}
+
+int dspark_cache_attend_tree(const dspark_cache_t* c, int layer, const void* q, int64_t q_stride, int n_rows, int H,
+                             const int32_t* offsets, int lead, int R, int max_new, const uint64_t* anc, float scale,
+                             int n_groups, const int32_t* group_off, const int32_t* shared_table, int shared_width,
+                             const int32_t* shared_pages, void* out, int64_t out_stride, float* lse, uint32_t* status,
+                             void* ws, size_t ws_bytes, void* stream) {
+    const char* who = "cache_attend_tree";
+    if (max_new > dspark::kTreeNodes)
+        return fail(DSPARK_EUNSUPPORTED, "%s: trees of %d nodes exceed %d", who, max_new, dspark::kTreeNodes);
+    if (!anc && R > 0 && n_rows > 0 && max_new > 0) return fail(DSPARK_EINVAL, "%s: anc is NULL", who);
+    return attend(c, layer, q, q_stride, n_rows, H, offsets, lead, R, max_new, anc, scale, n_groups, group_off,
+                  shared_table, shared_width, shared_pages, out, out_stride, lse, status, ws, ws_bytes, stream, who);
+}
+
+// One layer's K, V and Q of a step's rows turned to their positions.
+int dspark_cache_append_rotary(const dspark_cache_t* c, int layer, const dspark_rotary_t* rotary, const void* q,
+                               int64_t q_stride, int H, void* q_out, int64_t q_out_stride, const void* k_new,
+                               int64_t k_stride, const void* v_new, int64_t v_stride, int n_rows,
+                               const int32_t* offsets, int lead, int R, int max_new, const int32_t* depth,
+                               uint32_t* status, void* stream) {
+    const char* who = "cache_append_rotary";
+    dspark::RotaryArgs g{};
+    bool any = false;
+    int rc = append_args(c, layer, k_new, k_stride, v_new, v_stride, n_rows, offsets, lead, R, max_new, status, who, g.a, any);
+    if (rc != DSPARK_OK) return rc;
+    if (!rotary) return fail(DSPARK_EINVAL, "%s: rotary is NULL", who);
+    if (rotary->dim < 16 || rotary->dim % 16 || rotary->first < 0 || rotary->first % 8 ||
+        rotary->first > c->head_dim - rotary->dim)
+        return fail(DSPARK_EINVAL, "%s: %d dims from %d on, of %d, cannot be turned", who, rotary->dim, rotary->first, c->head_dim);
+    if (!isfinite(rotary->attention))
+        return fail(DSPARK_ERANGE, "%s: attention %g must be finite", who, (double)rotary->attention);
+    if (H < 1 || H > 65535) return fail(DSPARK_EINVAL, "%s: %d query heads", who, H);
+    if (!any) return DSPARK_OK;
+    if (!rotary->turns) return fail(DSPARK_EINVAL, "%s: turns is NULL", who);
+    if ((rc = check_rows(q, q_stride, H, c->head_dim, who, "q")) != DSPARK_OK ||
+        (rc = check_rows(q_out, q_out_stride, H, c->head_dim, who, "q_out")) != DSPARK_OK)
+        return rc;
+    const uintptr_t q0 = (uintptr_t)q, q1 = (uintptr_t)q_out, q_span = ((uintptr_t)(n_rows - 1) * q_stride + (uintptr_t)H * c->head_dim) * 2,
+                    out_span = ((uintptr_t)(n_rows - 1) * q_out_stride + (uintptr_t)H * c->head_dim) * 2;
+    if (q0 == q1 ? q_stride != q_out_stride && n_rows > 1 : q0 < q1 + out_span && q1 < q0 + q_span && !interleaves(q0, q1, q_stride, q_out_stride, (int64_t)H * c->head_dim))
+        return fail(DSPARK_EINVAL, "%s: q and q_out overlap", who);
+    g.q = (const uint16_t*)q;
+    g.q_out = (uint16_t*)q_out;
+    g.q_stride = q_stride;
+    g.q_out_stride = q_out_stride;
+    g.turns = rotary->turns;
+    g.depth = depth;
+    g.H = H;
+    g.dim = rotary->dim;
+    g.first = rotary->first;
+    g.interleaved = rotary->interleaved != 0;
+    g.dtype = c->dtype;
+    g.attention = rotary->attention;
+    return done(dspark::launch_append_rotary(g, (hipStream_t)stream), who);
+}
+
+int dspark_cache_keep_path(const dspark_cache_t* c, const int32_t* path, int K, const int32_t* accept_len,
+                           const int32_t* granted, int lead, int R, uint32_t* status, void* stream) {
+    const char* who = "cache_keep_path";
     int rc = check_data(c, who);
     if (rc != DSPARK_OK || (rc = check_requests(c, R, lead, who)) != DSPARK_OK) return rc;
-    if (layer < 0 || layer >= c->layers) return fail(DSPARK_ERANGE, "%s: layer %d outside [0, %d)", who, layer, c->layers);
-    if (n_rows < 0 || max_new < 0) return fail(DSPARK_ERANGE, "%s: n_rows %d, max_new %d", who, n_rows, max_new);
-    if (H < 1 || H % c->n_kv_heads || H > 65535)
-        return fail(DSPARK_EINVAL, "%s: %d query heads over %d key heads", who, H, c->n_kv_heads);
-    if (!(scale > 0.f) || !isfinite(scale * 1.44269504f))
-        return fail(DSPARK_ERANGE, "%s: scale %g must be positive and finite", who, (double)scale);
-    if (n_groups < 0 || n_groups > DSPARK_CACHE_MAX_GROUPS)
-        return fail(DSPARK_EUNSUPPORTED, "%s: %d groups, at most %d are supported", who, n_groups, DSPARK_CACHE_MAX_GROUPS);
-    if (n_groups > 0 && (!group_off || !shared_table || !shared_pages || shared_width < 1))
-        return fail(DSPARK_EINVAL, "%s: groups need group_off, shared_table and shared_pages", who);
-    if (R == 0 || n_rows == 0 || max_new == 0) return DSPARK_OK;
-    if ((rc = check_rows(q, q_stride, H, c->head_dim, who, "q")) != DSPARK_OK ||
-        (rc = check_rows(out, out_stride, H, c->head_dim, who, "out")) != DSPARK_OK)
-        return rc;
-    if (!offsets) return fail(DSPARK_EINVAL, "%s: offsets is NULL", who);
-    const long long tokens = (long long)c->width * c->page_size, shared_tokens = (long long)shared_width * c->page_size;
-    dspark::AttendArgs a{};
-    a.lead = lead;
-    a.R = R;
-    a.rows = (int)std::min<long long>(n_rows, (long long)R * max_new);  // rows past those belong to no request
-    a.max_new = std::min(max_new, n_rows);                              // (more would not lie in the tensors)
-    a.H = H;
-    a.Hkv = c->n_kv_heads;
-    a.G = H / c->n_kv_heads;
-    a.D = c->head_dim;
-    a.n_groups = n_groups;
-    dspark::attend_forms(a, dspark::num_cu());
-    // The work is numbered with 32 bits: columns, the units of the requests' own keys and those of
-    // the groups', as many as these sizes allow, and the joining launch's grid.
-    const auto tiles = [&](int set, long long columns) { return (columns + a.tile[set] - 1) / a.tile[set]; };
-    const auto units = [&](int set, long long keys) { return (long long)a.Hkv * (keys / a.unit[set] + 1); };
-    const bool fits = (long long)a.rows * H <= INT32_MAX - 1023 && tokens <= dspark::kAttendMaxTokens &&
-                      std::min(R * tiles(0, (long long)a.max_new * a.G), R + tiles(0, (long long)a.rows * a.G)) *
-                              units(0, tokens) <= INT32_MAX;
-    const bool groups_fit =
-        !n_groups || (shared_tokens <= dspark::kAttendMaxTokens &&
-                      (n_groups + tiles(1, (long long)a.rows * a.G)) * units(1, shared_tokens) <= INT32_MAX &&
-                      (long long)a.max_new * a.G * (a.D / 8) <= 65535ll * dspark::kAttendJoinItems);
-    if (!fits || !groups_fit)
-        return fail(DSPARK_EUNSUPPORTED, "%s: %d rows of %d heads over up to %lld tokens are too many for one call", who,
-                    n_rows, H, tokens);
-    if ((rc = check_ws(ws, ws_bytes, dspark::attend_ws_bytes(R, H, a.D, a.rows, n_groups), who)) != DSPARK_OK) return rc;
-    const size_t at = layer * layer_elems(c);
-    a.q = (const uint16_t*)q;
-    a.q_stride = q_stride;
-    a.out_stride = out_stride;
-    a.k = (const uint16_t*)c->k + at;
-    a.v = (const uint16_t*)c->v + at;
-    a.table = c->table;
-    a.len = c->len;
-    a.offsets = offsets;
-    a.dtype = c->dtype;
-    a.page = c->page_size;
-    a.page_shift = __builtin_ctz(c->page_size);
-    a.n_pages = c->n_pages;
-    a.width = c->width;
-    a.scale_log2 = (float)((double)scale * 1.4426950408889634);
-    a.shared_width = shared_width;
-    a.group_off = group_off;
-    a.shared_table = shared_table;
-    a.shared_pages = shared_pages;
-    a.out = (uint16_t*)out;
-    a.lse = lse;
-    a.status = status;
-    dspark::attend_ws_layout(a, ws);
-    return done(dspark::launch_attend(a, (hipStream_t)stream), who);
+    if (K < 0 || K >= dspark::kTreeNodes) return fail(DSPARK_ERANGE, "%s: K %d outside [0, %d)", who, K, dspark::kTreeNodes);
+    if (c->layers > 65535) return fail(DSPARK_EUNSUPPORTED, "%s: %d layers", who, c->layers);
+    if (R == 0) return DSPARK_OK;
+    if (!accept_len || (K > 0 && !path)) return fail(DSPARK_EINVAL, "%s: a required pointer is NULL", who);
+    return done(dspark::launch_keep_path(*c, path, K, accept_len, granted, lead, R, status, (hipStream_t)stream), who);
 }
 
 }  // extern "C"

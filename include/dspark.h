@@ -59,7 +59,7 @@ typedef enum {
     DSPARK_EHIP = -5          /* HIP runtime error (text in dspark_last_error)    */
 } dspark_status_t;
 
-typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_F16 = 2 /* the paged cache alone */ } dspark_dtype_t;
+typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_F16 = 2 /* the paged cache and dspark_target_tokens */ } dspark_dtype_t;
 
 /* Device-side conditions, OR-ed into *status. */
 #define DSPARK_STATUS_PREV_CLAMPED 1u   /* a prev0 entry was outside [0,V); it was clamped into range      */
@@ -74,10 +74,11 @@ typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_F16 = 2 /* the paged cach
 #define DSPARK_STATUS_BAD_PAGE 32u      /* paged cache: a page id outside [0, n_pages) where a page was needed (its
                                            tokens are left out), a page released more often than it was held, or
                                            a request whose table does not begin with its group's pages      */
-#define DSPARK_STATUS_BAD_ROW 64u       /* paged cache: a request, table row or group whose offsets, length or
-                                           index do not fit (see each call for what becomes of it)          */
+#define DSPARK_STATUS_BAD_ROW 64u       /* paged cache, trees, target tokens: a request, row or group whose offsets,
+                                           length or index do not fit (see each call for what becomes of it) */
 #define DSPARK_STATUS_NO_PAGES 128u     /* paged cache: too few free pages, or no room in the table; the request or
                                            fork was not served                                              */
+#define DSPARK_STATUS_NO_TOKEN 256u     /* dspark_target_tokens: a row's mask allows no token; its target is -1 */
 
 /* Admission rules of stage 4. */
 #define DSPARK_RULE_ARGMAX 0      /* the smallest B with the largest f(B) (vLLM blog, "Scheduling the budget")  */
@@ -619,6 +620,238 @@ int dspark_cache_attend(const dspark_cache_t* cache, int layer, const void* q, i
                         const int32_t* group_off, const int32_t* shared_table, int shared_width,
                         const int32_t* shared_pages, void* out, int64_t out_stride, float* lse, uint32_t* status,
                         void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Trees of drafts.
+ *
+ * Several drafted continuations of a request, verified together: node 0 is the last accepted
+ * token, the others are drafts, and each hangs on the node that it continues.  The rows of a
+ * step are the nodes (lead = 1): node j of request r is row offsets[r] + r + j, its parent
+ * parent[that row] < j (-1 for node 0), and for j >= 1 its token ver_tokens[offsets[r] + j - 1].
+ * A step goes
+ *   dspark_tree_merge          chains drafted for a request (e.g. by dspark_chain_sample under
+ *                              several seeds, each cut to what dspark_schedule gives it) as one tree
+ *   dspark_tree_plan           each row's depth and the nodes it sees, once for all layers
+ *   dspark_pages_reserve       pages for the rows
+ *   per layer: dspark_cache_append_rotary (or dspark_cache_append), dspark_cache_attend_tree
+ *   dspark_target_tokens       the target's choice at each row
+ *   dspark_accept_tree         the accepted path
+ *   dspark_cache_keep_path     the path's K and V moved behind node 0's
+ *   dspark_pages_commit        as for chains
+ * A request has at most DSPARK_TREE_MAX_NODES nodes.
+ */
+#define DSPARK_TREE_MAX_NODES 64
+
+/*
+ * The chains of each request as one tree: tokens that follow equal beginnings are one node.
+ * Node numbers go by chain, then by position; so a parent comes before its children, and the
+ * children of a node have different tokens.
+ *   tokens      [R*S, K] int32: chain s of request r is row r*S + s
+ *   prefix_len  [R*S] int32 tokens of each chain that count, 0 .. K (others count as 0,
+ *               DSPARK_STATUS_BAD_ROW), or NULL (all K)
+ *   counts      [R]      int32 output: the request's drafts
+ *   offsets     [R+1]    int32 output: exclusive running sum of counts
+ *   ver_tokens  [R*S*K]  int32 output: the drafts, request by request (what lies past the last
+ *                        one stays as it was)
+ *   parent      [R*S*K + R] int32 output: request r's 1 + counts[r] entries from offsets[r] + r on
+ * Limits: S*K < DSPARK_TREE_MAX_NODES; R <= DSPARK_CACHE_MAX_REQUESTS.
+ */
+int dspark_tree_merge(const int32_t* tokens, const int32_t* prefix_len, int R, int S, int K, int32_t* counts,
+                      int32_t* offsets, int32_t* ver_tokens, int32_t* parent, uint32_t* status, void* stream);
+
+/*
+ * Depths and visible nodes of a step's rows, from their parents.
+ *   parent   [n_rows] int32: -1 for a node that follows the cache's tokens directly (several may),
+ *            else an earlier node of the request
+ *   offsets  [R+1], lead: the step's rows; max_new >= every n_r, at most DSPARK_TREE_MAX_NODES
+ *   depth    [n_rows] int32 output: nodes between the row's and the cache's tokens
+ *   anc      [n_rows] uint64 output: bit i set if node i is the row's or an ancestor of it
+ * A node with another parent, and every node below it, gets depth 0 and the word 0 (such a row
+ * sees nothing); a request whose rows do not fit is left out (both DSPARK_STATUS_BAD_ROW).  Rows that
+ * belong to no request stay as they are.
+ */
+int dspark_tree_plan(const int32_t* parent, int n_rows, const int32_t* offsets, int lead, int R, int max_new,
+                     int32_t* depth, uint64_t* anc, uint32_t* status, void* stream);
+
+/*
+ * Rotary positions: pairs (a, b) of a head's dims turned by an angle that grows with the position,
+ *   a' = m (a cos t - b sin t),  b' = m (a sin t + b cos t),  t = position * freq[i]
+ * for pair i of `dim` dims from dim `first` on: dims first + 2i and first + 2i + 1 (interleaved),
+ * or first + i and first + dim/2 + i (in halves).  The other dims pass through.
+ *   turns      [dim/2] device: each pair's frequency in turns a token, as a fraction of 2^64
+ *              (dspark_rotary_turns), so that an angle is exact to 2^-32 turns at every position
+ *   m          attention: the factor on both of a pair, 1 for none; finite
+ * dim is a multiple of 16, first one of 8, first + dim <= head_dim.
+ */
+typedef struct dspark_rotary {
+    const uint64_t* turns;
+    int32_t dim, first, interleaved;
+    float attention;
+} dspark_rotary_t;
+
+/* Frequencies freq[i] = base^(-2i/dim), i < dim/2, in radians a token (host memory, start-up),
+ * stretched for contexts longer than the `original` one that the model was trained on:
+ *   DSPARK_ROTARY_NONE    as they are
+ *   DSPARK_ROTARY_LINEAR  freq / factor
+ *   DSPARK_ROTARY_BANDS   with w = original * freq / (2 pi), a pair's turns over the original length,
+ *                         and s = (w - low) / (high - low) clamped to 0 .. 1: freq * (s + (1 - s) / factor)
+ *   DSPARK_ROTARY_RAMP    with d(x) = dim * ln(original / (2 pi x)) / (2 ln base), the pair of x turns,
+ *                         a = max(floor(d(high)), 0), b = min(ceil(d(low)), dim - 1) and s = (i - a) /
+ *                         max(b - a, 0.001) clamped to 0 .. 1: freq * (1 - s + s / factor)
+ * DSPARK_ERANGE unless base > 1, and factor >= 1, original > 0 and 0 < low < high where they are used. */
+#define DSPARK_ROTARY_NONE 0
+#define DSPARK_ROTARY_LINEAR 1
+#define DSPARK_ROTARY_BANDS 2
+#define DSPARK_ROTARY_RAMP 3
+int dspark_rotary_frequencies(int scaling, int dim, double base, double factor, double original, double low,
+                              double high, double* freq);
+/* The same in turns, for dspark_rotary_t (host memory; the caller copies them to the device). */
+int dspark_rotary_turns(const double* freq, int n, uint64_t* turns);
+
+/*
+ * dspark_cache_append with the step's queries and keys turned to their positions: row j of request
+ * r turns by len[r] + j, or by len[r] + depth[row] where depth is given (a tree's rows; its K and V
+ * still go to position len[r] + j).  Products and sums are held in fp32 and rounded once.
+ *   q, q_out  [n_rows] rows of [H, head_dim], q_stride and q_out_stride elements apart, as k_new.
+ *             q_out may be q (with the same stride); otherwise they must not overlap
+ *   depth     [n_rows] int32 or NULL
+ * Queries of vacant requests and of those that are left out stay as they are.  The other
+ * arguments and what is left out are dspark_cache_append's; queries need no pages.
+ */
+int dspark_cache_append_rotary(const dspark_cache_t* cache, int layer, const dspark_rotary_t* rotary, const void* q,
+                               int64_t q_stride, int H, void* q_out, int64_t q_out_stride, const void* k_new,
+                               int64_t k_stride, const void* v_new, int64_t v_stride, int n_rows,
+                               const int32_t* offsets, int lead, int R, int max_new, const int32_t* depth,
+                               uint32_t* status, void* stream);
+
+/*
+ * dspark_cache_attend for the rows of trees: row j of request r sees the positions 0 .. len[r] - 1
+ * of its table row and, of the step's nodes, position len[r] + i where bit i of its word is set.
+ * Bits from n_r on have no say.  A row whose word is 0 sees nothing: zeros, lse -inf.
+ *   anc  [n_rows] uint64 (dspark_tree_plan)
+ * max_new is at most DSPARK_TREE_MAX_NODES.  Everything else, the workspace too, is
+ * dspark_cache_attend's; with the words of a chain (bits 0 .. j) so are the results.
+ */
+int dspark_cache_attend_tree(const dspark_cache_t* cache, int layer, const void* q, int64_t q_stride, int n_rows, int H,
+                             const int32_t* offsets, int lead, int R, int max_new, const uint64_t* anc, float scale,
+                             int n_groups, const int32_t* group_off, const int32_t* shared_table, int shared_width,
+                             const int32_t* shared_pages, void* out, int64_t out_stride, float* lse, uint32_t* status,
+                             void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Greedy verification of trees (lead = 1): from node 0 on, the child whose token is the target's
+ * choice at the node is accepted (the lowest numbered one of several), until there is none or K
+ * are accepted; the target's choice at the last one is the bonus token.
+ *   ver_tokens  [n_nodes]     int32 drafts (dspark_tree_merge); may be NULL when n_nodes == 0
+ *   offsets     [R+1]         int32
+ *   parent      [n_nodes + R] int32; a child comes behind its parent, others are never reached
+ *   target      [n_nodes + R] int32: the target's choice at each row (dspark_target_tokens)
+ *   accept_len  [R]           int32 output: accepted drafts
+ *   path        [R, K]        int32 output: their nodes, then -1; may be NULL when K == 0
+ *   next_prev0  [R]           int32 output: the bonus token
+ *   out_tokens  [R, K+1]      int32 output: the accepted tokens, the bonus token, then -1; or NULL
+ * A row of offsets that falls, passes n_nodes or has DSPARK_TREE_MAX_NODES drafts or more accepts nothing
+ * and gets -1 everywhere (DSPARK_STATUS_BAD_ALLOCATION).  Limit: 0 <= K < DSPARK_TREE_MAX_NODES.
+ */
+int dspark_accept_tree(const int32_t* ver_tokens, int n_nodes, const int32_t* offsets, const int32_t* parent,
+                       const int32_t* target, int R, int K, int32_t* accept_len, int32_t* path, int32_t* next_prev0,
+                       int32_t* out_tokens, uint32_t* status, void* stream);
+
+/*
+ * The accepted path's K and V, every layer's, moved together: position len[r] + path[r, i] to len[r]
+ * + lead + i, i < accept_len[r].  len stays: dspark_pages_commit with the same accept_len follows.
+ * (Keys were turned to len[r] + depth, which is where they go.)
+ *   path        [R, K] int32, rising from lead on below DSPARK_TREE_MAX_NODES; may be NULL when K == 0
+ *   granted     [R] int32 as dspark_pages_reserve wrote it, or NULL: requests with 0 stay as they are
+ * Vacant requests are left out, and so are those whose accept_len does not lie in 0 .. K, whose
+ * path does not rise or reaches past its table (DSPARK_STATUS_BAD_ROW), or one of whose pages is none or,
+ * where something would be written, another row's too (DSPARK_STATUS_BAD_PAGE).
+ */
+int dspark_cache_keep_path(const dspark_cache_t* cache, const int32_t* path, int K, const int32_t* accept_len,
+                           const int32_t* granted, int lead, int R, uint32_t* status, void* stream);
+
+/*
+ * The target's choice at each row of a step, from its logits.
+ *
+ * A history says, for each request, which tokens have been seen:
+ *   seen   [rows, 2, words] uint32, words = dspark_history_words(V): bit v % 32 of word v / 32 of
+ *          [r, 0] is set if token v is in request r's prompt, of [r, 1] if it has been answered
+ *   count  [rows, V] int32: how often it has been answered (0 where its bit is not set)
+ * in buffers that the caller owns and zero-fills once; 16-byte aligned.
+ */
+typedef struct dspark_history {
+    uint32_t* seen;
+    int32_t* count;
+    int32_t rows, V;
+} dspark_history_t;
+size_t dspark_history_words(int V); /* ceil(V / 128) * 4 */
+
+/* History rows emptied: rows[i] for i < n, or rows 0 .. n-1 where rows is NULL.  A rows[i] outside
+ * the history is left out (DSPARK_STATUS_BAD_ROW), here and in dspark_history_add. */
+int dspark_history_clear(const dspark_history_t* history, const int32_t* rows, int n, uint32_t* status, void* stream);
+
+/* Tokens entered: tokens [n, width] int32 into history rows rows[i] (i where rows is NULL), as prompt
+ * tokens or, answered != 0, as answered ones (the out_tokens of an acceptance, as they are).  Negative
+ * entries are none; those from V on are left out (DSPARK_STATUS_BAD_ROW).  A row may be named again. */
+int dspark_history_add(const dspark_history_t* history, const int32_t* tokens, int n, int width, const int32_t* rows,
+                       int answered, uint32_t* status, void* stream);
+
+/*
+ * For every row t of the step, node j of request r:
+ *   c(v) = count[r, v] + how many of the drafts that row t has behind it, its own among them, are v
+ *   x(v) = logits[t, v]
+ *   x(v) = x(v) > 0 ? x(v) / repetition[r] : x(v) * repetition[r]   where v is in the prompt or c(v) > 0
+ *   x(v) = x(v) - frequency[r] * c(v);  x(v) = x(v) - presence[r]   where c(v) > 0
+ *   x(v) = x(v) + bias(r, v)                                        where the request has one for v
+ *   target[t] = the v with the largest x(v) of those that the row's mask allows
+ * in this order and in 64 bits, so that which of two near values is larger does not hang on a
+ * rounding; the largest value wins, NaN counts as larger than every number, the lowest v of equal ones.
+ *   logits       [n_rows] rows of V values, logits_stride elements apart (dtype: f32, bf16, f16);
+ *                aligned to its type alone
+ *   offsets      [R+1], lead: the step's rows; max_new >= every n_r, at most DSPARK_TARGET_MAX_ROWS
+ *   history      or NULL: nothing seen; rows >= R and the same V
+ *   repetition, presence, frequency  [R] fp32, each or NULL: 1, 0 and 0.  Where all are NULL no history is read
+ *   ver_tokens   [n_nodes] int32 or NULL: drafts count for nothing.  Node i >= lead of request r is
+ *                ver_tokens[offsets[r] + i - lead]; tokens outside 0 .. V-1 and entries outside count for nothing
+ *   anc          [n_rows] uint64: the nodes that a row has behind it (dspark_tree_plan; max_new <=
+ *                DSPARK_TREE_MAX_NODES), or NULL: a chain's, nodes 0 .. j
+ *   bias_off     [R+1] int32 or NULL: no biases.  Request r's are entries bias_off[r] .. bias_off[r+1] - 1 of
+ *   bias_tok, bias_val  [n_bias] int32 and fp32, tokens rising within a request.  Entries outside 0 .. V-1
+ *                are left out, some of a request's that do not rise, and all of one whose bias_off do not
+ *                fit (DSPARK_STATUS_BAD_ROW)
+ *   allowed      [n_allowed] rows of at least ceil(V/32) uint32, allowed_stride words apart, bit v % 32 of
+ *                word v / 32 set where token v is allowed; or NULL: all are
+ *   allowed_row  [n_rows] int32: the row of allowed that binds row t, -1 for none; or NULL: row t.  Another
+ *                number allows nothing (DSPARK_STATUS_BAD_ROW)
+ *   target       [n_rows] int32 output; -1 where no token is allowed (DSPARK_STATUS_NO_TOKEN)
+ *   adjusted     [n_rows] rows of V values, adjusted_stride elements apart, in logits' dtype: output x(v),
+ *                rounded once from fp32, -inf where v is not allowed; or NULL
+ * A request with n_r < 0 or > max_new or rows outside the tensors is left out (DSPARK_STATUS_BAD_ROW), and
+ * rows that belong to no request stay as they are.
+ */
+#define DSPARK_TARGET_MAX_ROWS 256
+typedef struct dspark_target {
+    const void* logits;
+    int64_t logits_stride;
+    int32_t n_rows, V, dtype, R, lead, max_new;
+    const int32_t* offsets;
+    const dspark_history_t* history; /* (host) */
+    const float *repetition, *presence, *frequency;
+    const int32_t* ver_tokens;
+    const uint64_t* anc;
+    const int32_t *bias_off, *bias_tok;
+    const float* bias_val;
+    const uint32_t* allowed;
+    const int32_t* allowed_row;
+    int64_t allowed_stride;
+    int32_t n_nodes, n_bias, n_allowed, reserved;
+    int32_t* target;
+    void* adjusted;
+    int64_t adjusted_stride;
+} dspark_target_t;
+/* Bytes of workspace (16-byte aligned) for up to n_rows rows of up to V tokens. */
+size_t dspark_target_workspace_bytes(int n_rows, int V);
+int dspark_target_tokens(const dspark_target_t* call, uint32_t* status, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * How the persistent kernels are launched.  The single-launch step (dspark_step,
