@@ -2,19 +2,17 @@
 // grammar masks, and the argmax, in one pass over the logits; and the record of what has been
 // said, which the penalties read.
 //
-// Few tokens of a row are changed at all: those seen, biased, or drafted on the row's path.  Each
-// of these has one owner, who takes it out of the bits of what is left and computes its value in
-// 64 bits by itself; the others compare as they are, in fp32, eight at a time under eight bits.
-// So the pass over the logits costs what an argmax costs, and the counts are read only at the
-// few tokens that have any.
-//
-// A workgroup takes a part of a row (all of it where there are rows enough):
-//   1. the bits of the tokens that the row's mask allows go to LDS;
-//   2. biased tokens and the path's are owned by their entry in the list;
-//   3. seen ones by their bit: they are gathered in a list in LDS, so that the lanes share them
-//      evenly however they cluster, and several of their loads are under way at a time;
-//   4. the rest is streamed.
-// Every value has an order key, and the largest key with the lowest token wins.
+// Nearly all tokens lose by their logit alone.  While a workgroup streams a row (or a part of one), it
+// knows a value that the row's best has at least, `floor`, and from it a logit below which no token
+// can reach it: floor itself, or less where a penalty below nothing or a repetition below one could
+// lift a token.  So the pass compares the largest of eight logits with that limit, a dozen
+// instructions, and looks at tokens one by one only where it is reached: a few times a row.
+// There the bits in LDS say whether a token is allowed, and whether anything changes it (it is seen,
+// biased or drafted); if not, its logit is its value, and if so it is put on a list, whose values are
+// computed at the end, side by side, in 64 bits and with the counts that only they need.
+// Biases may lift a token as far as they like: those tokens are on the list from the start.  So is
+// every changed one where the processed logits are wanted, or a frequency below nothing lifts tokens
+// by how often they have been said.
 #include <algorithm>
 
 #include "common.h"
@@ -24,11 +22,17 @@ namespace dspark {
 
 namespace {
 
-constexpr int kT = 256;
-constexpr int kGroups = 4;             // of eight logits, that a lane has under way
-constexpr int kMostChunk = 131072;     // tokens of a part: 16 KB of bits in LDS
-constexpr int kList = 2048;            // seen tokens gathered at a time
+#define INLINE __attribute__((always_inline))
+constexpr int kT = 512, kWaves = kT / 64;
+constexpr int kPerSimd = 6;           // waves that the registers leave room for
+constexpr int kGroups = 3;            // of eight logits: a lane's loads under way, twice
+constexpr int kMostChunk = 131072;    // tokens of a part: twice 16 KB of bits in LDS
+constexpr int kLeastChunk = 4096;
+constexpr int kWanted = 2 * kAttendMaxCus;  // workgroups, where there are few rows
+constexpr int kList = 2048;           // changed tokens listed; where there are more, all of them are gone through
+constexpr int kHistoryT = 256;
 constexpr float kInf = __builtin_huge_valf();
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 struct F32 {
     typedef uint32_t T;
@@ -56,6 +60,11 @@ __device__ __forceinline__ uint64_t order_key(double x) {
     return b >> 63 ? ~b : b | 1ull << 63;
 }
 
+// The value of argmax_key's upper half.
+__device__ __forceinline__ float key_value(uint32_t key) {
+    return __uint_as_float(key >> 31 ? (key == ~0u ? 0x7FC00000u : key & 0x7FFFFFFFu) : ~key);
+}
+
 struct Best {
     uint64_t key;
     uint32_t v;
@@ -76,7 +85,18 @@ __device__ __forceinline__ void wave_best(Best& b) {
     }
 }
 
-// Row j of request r, where it is one (the first workgroup of a request says what does not fit).
+// The largest of a wave's numbers, by the data paths within and between rows of 16 lanes.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+    x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x111, 0xF, 0xF, false));
+    x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x112, 0xF, 0xF, false));
+    x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x114, 0xF, 0xF, false));
+    x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x118, 0xF, 0xF, false));
+    x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x142, 0xA, 0xF, false));
+    x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x143, 0xC, 0xF, false));
+    return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+
+// Row j of request r, where it is one.
 __device__ __forceinline__ bool row_of(const dspark_target_t& t, int r, int j, int& o, long long& start, int& n, uint32_t& bad) {
     o = t.offsets[r];
     const long long rows = (long long)t.offsets[r + 1] - o + t.lead;
@@ -89,87 +109,86 @@ __device__ __forceinline__ bool row_of(const dspark_target_t& t, int r, int j, i
     return j < n;
 }
 
-// Where `tok` is in the request's biases [b0, b1), -1 if it is not there.  In a list that does not
-// rise it may not be found; each token has at most one place either way.
-__device__ __forceinline__ int find_bias(const int32_t* bias_tok, int b0, int b1, int tok) {
-    while (b0 < b1) {
-        const int mid = b0 + ((b1 - b0) >> 1), t = bias_tok[mid];
-        if (t == tok) return mid;
-        if (t < tok) b0 = mid + 1; else b1 = mid;
+// Eight logits, wherever they stand (rows of an odd vocabulary are not aligned).
+template <class E>
+struct Eight {
+    typedef typename E::T T;
+    static constexpr int kParts = sizeof(T) / 2;
+    typedef u32x4 __attribute__((aligned(2), may_alias)) any;
+    u32x4 w[kParts];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) w[i] = __builtin_nontemporal_load((const any*)p + i);
     }
-    return -1;
-}
+    __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) __builtin_nontemporal_store(w[i], (any*)p + i);
+    }
+    __device__ __forceinline__ T bits(int k) const {
+        return sizeof(T) == 4 ? (T)w[k / 4][k % 4] : (T)(w[0][k / 2 % 4] >> (k % 2 * 16));
+    }
+    __device__ __forceinline__ float value(int k) const { return E::value(bits(k)); }
+    __device__ __forceinline__ void mask(uint32_t keep) {  // -inf where a bit is not set
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t on = (uint32_t)((int32_t)(keep << (31 - k)) >> 31);
+            if (sizeof(T) == 4) {
+                w[k / 4][k % 4] = (w[k / 4][k % 4] & on) | (0xFF800000u & ~on);
+            } else {
+                const uint32_t off = (0xFFFFu << (k % 2 * 16)) & ~on;
+                w[0][k / 2 % 4] = (w[0][k / 2 % 4] & ~off) | ((uint32_t)E::kNegInf * 0x10001u & off);
+            }
+        }
+    }
+};
 
 template <class E, bool kOut>
-__global__ __launch_bounds__(kT) void target_kernel(TargetArgs a) {
+__global__ __launch_bounds__(kT, kPerSimd) void target_kernel(TargetArgs a) {
     typedef typename E::T T;
     const dspark_target_t& t = a.t;
-    // bits of the part's tokens, with a word before them and one behind: [0] allowed and without an
-    // owner so far; [1] (kOut) owned
-    extern __shared__ uint32_t s_words[];
-    __shared__ uint32_t s_list[kList];
-    __shared__ int s_path[DSPARK_TARGET_MAX_ROWS];
-    __shared__ uint32_t s_count, s_limit;
-    __shared__ Best s_best[kT / 64];
-    const int r = blockIdx.x, j = blockIdx.y, part = blockIdx.z, tid = threadIdx.x;
+    extern __shared__ uint32_t s_words[];  // bits of the part's tokens: changed ones, allowed ones
+    __shared__ uint2 s_list[kList];        // changed tokens, and their logits
+    __shared__ int s_draft[DSPARK_TARGET_MAX_ROWS], s_bias[kT];
+    static_assert(DSPARK_TARGET_MAX_ROWS <= kT, "a draft to a lane");
+    __shared__ uint32_t s_count, s_floor;
+    __shared__ Best s_best[kWaves];
+    const int r = blockIdx.x % t.R, part = blockIdx.x / t.R, j = blockIdx.y, tid = threadIdx.x;
     int o, n;
     long long start;
     uint32_t bad = 0;
     if (!row_of(t, r, j, o, start, n, bad)) {
-        if (bad && j == 0 && part == 0 && tid == 0) raise_status(a.status, bad);
+        if (bad && part == 0 && j == 0 && tid == 0) raise_status(a.status, bad);
         return;
     }
     const size_t row = (size_t)(start + j);
-    const int lo = part * a.chunk, hi = min(t.V, lo + a.chunk), n_words = (hi - lo + 31) / 32;
-    uint32_t *s_left = s_words + 1, *s_owned = s_words + (a.chunk / 32 + 2) + 1;
     const T* logits = (const T*)t.logits + row * t.logits_stride;
     T* out = kOut ? (T*)t.adjusted + row * t.adjusted_stride : nullptr;
+    const int lo = part * a.chunk, hi = min(t.V, lo + a.chunk), n_words = (hi - lo + 31) / 32;
+    const int n_groups = (hi - lo) / 8;                                          // of eight tokens from lo on
+    const int tail = tid < (hi - lo) % 8 ? lo + n_groups * 8 + tid : -1;  // and what is left, a token to a lane
 
-    // 1. what is allowed
+    // What has a say in this row.
     const uint32_t* allowed = nullptr;
-    bool nothing = false;
+    bool nothing = false;  // is allowed
     if (t.allowed) {
-        long long pick = t.allowed_row ? t.allowed_row[row] : (long long)row;
+        const long long pick = t.allowed_row ? t.allowed_row[row] : (long long)row;
         if (pick < -1 || pick >= t.n_allowed) {
             nothing = true;
             bad = kStatusBadRow;
         } else if (pick >= 0) {
-            allowed = t.allowed + (size_t)pick * t.allowed_stride + lo / 32;
+            allowed = t.allowed + (size_t)pick * t.allowed_stride;
         }
     }
-    for (int w = tid; w <= n_words; w += kT) {
-        uint32_t x = 0;
-        if (w < n_words && !nothing) {
-            x = allowed ? allowed[w] : ~0u;
-            const int rest = hi - lo - w * 32;
-            if (rest < 32) x &= (1u << rest) - 1;
-        }
-        s_left[w] = x;
-        if (kOut) s_owned[w] = 0;
-    }
-    if (tid == 0) {
-        s_words[0] = 0;
-        if (kOut) s_owned[-1] = 0;
-    }
-
+    const bool masked = allowed || nothing;
     const bool penalties = t.repetition || t.presence || t.frequency;
+    const float repetition = t.repetition ? t.repetition[r] : 1.f, presence = t.presence ? t.presence[r] : 0.f,
+                frequency = t.frequency ? t.frequency[r] : 0.f;
     const uint32_t *prompt = nullptr, *answered = nullptr;
     const int32_t* count = nullptr;
     if (penalties && a.seen) {
-        prompt = a.seen + (size_t)r * 2 * a.words + lo / 32;
+        prompt = a.seen + (size_t)r * 2 * a.words;
         answered = prompt + a.words;
         count = a.count + (size_t)r * t.V;
-    }
-    const double repetition = t.repetition ? t.repetition[r] : 1.f, presence = t.presence ? t.presence[r] : 0.f,
-                 frequency = t.frequency ? t.frequency[r] : 0.f;
-    const int n_path = penalties && t.ver_tokens ? n : 0;
-    if (n_path) {
-        const uint64_t word = t.anc ? t.anc[row] : 0;
-        for (int i = tid; i < n; i += kT) {
-            const bool on = i >= t.lead && (t.anc ? (word >> (i & 63) & 1) != 0 : i <= j);
-            const int at = o + i - t.lead;
-            s_path[i] = on && at < t.n_nodes ? t.ver_tokens[at] : -1;
-        }
     }
     int b0 = 0, b1 = 0;
     if (t.bias_off) {
@@ -180,192 +199,227 @@ __global__ __launch_bounds__(kT) void target_kernel(TargetArgs a) {
             bad = kStatusBadRow;
         }
     }
-    __syncthreads();
+    const int n_draft = penalties && t.ver_tokens ? n : 0;
+    const bool changes = prompt || n_draft || b1 > b0;  // anything
+    // Every changed token is looked at, whatever its logit: where its value is wanted, or cannot be bounded.
+    const bool every = changes && (kOut || !(frequency >= 0.f) || !(repetition > 0.f) || !(repetition < kInf) ||
+                                   !(fabsf(presence) < kInf) || !(frequency < kInf));
 
-    // 2. biased tokens and the path's
-    Best best{0, ~0u};
-    const auto put = [&](int v, double x) {
-        best.take(order_key(x), (uint32_t)v);
-        if (kOut) out[v] = E::bits((float)x);
-    };
-    const auto penalised = [&](int v, bool seen, int c) {
-        double x = (double)E::value(logits[v]);
-        if (seen || c > 0) x = x > 0.0 ? x / repetition : x * repetition;
-        x = x - frequency * (double)c;
-        if (c > 0) x = x - presence;
-        return x;
-    };
-    // The owner of v takes it; false where it is not allowed.
-    const auto own = [&](int v) {
-        const int w = (v - lo) >> 5;
-        const uint32_t bit = 1u << ((v - lo) & 31);
-        if (kOut) atomicOr(&s_owned[w], bit);
-        if (atomicAnd(&s_left[w], ~bit) & bit) return true;
-        if (kOut) out[v] = E::kNegInf;
-        return false;
-    };
-    const auto on_path = [&](int v) {
-        int c = 0;
-        for (int i = 0; i < n_path; ++i) c += s_path[i] == v;
-        return c;
-    };
-    const auto listed = [&](int v, int c) {  // the value of a token of one of the lists, c times on the path
-        bool seen = false;
-        if (prompt) {
-            const int w = (v - lo) >> 5, bit = (v - lo) & 31;
-            seen = prompt[w] >> bit & 1;
-            if (answered[w] >> bit & 1) c += count[v];
-        }
-        return penalised(v, seen, c);
-    };
-    for (int e = b0 + tid; e < b1; e += kT) {
-        const int v = t.bias_tok[e];
-        if (v < 0 || v >= t.V || (e > b0 && t.bias_tok[e - 1] >= v)) bad = kStatusBadRow;
-        if (v < lo || v >= hi || find_bias(t.bias_tok, b0, b1, v) != e || !own(v)) continue;
-        put(v, listed(v, on_path(v)) + (double)t.bias_val[e]);
+    // The bits.  Their loads go out before the stream's first ones, so as not to wait behind those of all
+    // workgroups.
+    uint32_t *s_changed = s_words, *s_allowed = s_words + (a.seen || t.ver_tokens || t.bias_off ? a.chunk / 32 : 0);
+    constexpr int kWords = kMostChunk / 32 / kT;  // a lane's
+    uint32_t said[kWords], given[kWords], open[kWords];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+        const size_t at = lo / 32 + min(tid + i * kT, n_words - 1);
+        said[i] = prompt ? answered[at] : 0;
+        given[i] = prompt ? prompt[at] : 0;
+        open[i] = allowed ? allowed[at] : 0;
     }
-    for (int i = tid; i < n_path; i += kT) {
-        const int v = s_path[i];
-        if (v < lo || v >= hi) continue;
-        int first = 0;
-        while (s_path[first] != v) ++first;
-        if (first != i || find_bias(t.bias_tok, b0, b1, v) >= 0 || !own(v)) continue;
-        put(v, listed(v, on_path(v)));
+    const bool near = b1 - b0 <= kT;  // biases that are searched in LDS
+    int draft = -1, bias = -1;        // this lane's token of each list
+    if (tid < n_draft) {
+        const bool on = tid >= t.lead && (t.anc ? (t.anc[row] >> (tid & 63) & 1) != 0 : tid <= j);
+        const int at = o + tid - t.lead;
+        if (on && at < t.n_nodes) draft = t.ver_tokens[at];
+    }
+    if (near && tid < b1 - b0) bias = t.bias_tok[b0 + tid];
+    __builtin_amdgcn_sched_barrier(0);
+    Eight<E> now[kGroups], ahead[kGroups];
+    if (n_groups > 0) {
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) now[i].load(logits + lo + min(tid + i * kT, n_groups - 1) * 8);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (tid == 0) s_count = s_floor = 0;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+        if (tid + i * kT < n_words) {
+            if (changes) s_changed[tid + i * kT] = said[i] | given[i];
+            if (masked) s_allowed[tid + i * kT] = open[i];
+        }
+    if (tid < n_draft) s_draft[tid] = draft;
+    if (near && tid < b1 - b0) s_bias[tid] = bias;
+    __syncthreads();
+    const auto change = [&](int v) INLINE {
+        if (v >= lo && v < hi) atomicOr(&s_changed[(v - lo) >> 5], 1u << (v & 31));
+    };
+    const auto bias_at = [&](int e) INLINE { return near ? s_bias[e] : t.bias_tok[b0 + e]; };
+    if (draft >= 0) change(draft);
+    for (int e = tid; e < b1 - b0; e += kT) {
+        const int v = bias_at(e);
+        if (v < 0 || v >= t.V || (e > 0 && bias_at(e - 1) >= v)) bad = kStatusBadRow;
+        change(v);
     }
     if (bad && part == 0) raise_status(a.status, bad);
-
-    // 3. seen tokens, as many at a time as the list takes: words that did not fit come again
-    if (prompt) {
-        for (bool more = true; more;) {
-            __syncthreads();
-            if (tid == 0) {
-                s_count = 0;
-                s_limit = ~0u;
-            }
-            __syncthreads();
-            for (int w = tid; w < n_words; w += kT) {
-                const uint32_t left = s_left[w], said = answered[w] & left, seen = (prompt[w] & left) | said;
-                if (!seen) continue;
-                const uint32_t at = atomicAdd(&s_count, (uint32_t)__popc(seen));
-                if (at + __popc(seen) > kList) {
-                    atomicMin(&s_limit, at);
-                    continue;
-                }
-                s_left[w] = left & ~seen;
-                if (kOut) s_owned[w] |= seen;
-                uint32_t to = at;
-                for (uint32_t x = seen; x; x &= x - 1) {
-                    const int b = __ffs(x) - 1;
-                    s_list[to++] = (uint32_t)(lo + w * 32 + b) | (said >> b & 1) << 31;
-                }
-            }
-            __syncthreads();
-            const uint32_t n_list = min(s_count, s_limit);
-            more = s_limit != ~0u;
-            for (uint32_t i = tid; i < n_list; i += kT) {
-                const int v = (int)(s_list[i] & 0x7FFFFFFFu);
-                put(v, penalised(v, true, s_list[i] >> 31 ? count[v] : 0));
-            }
-        }
-    }
     __syncthreads();
+    const uint8_t *changed_of = (const uint8_t*)s_changed, *allowed_of = (const uint8_t*)s_allowed;
+    const auto is_allowed = [&](int v) { return !masked || (s_allowed[(v - lo) >> 5] >> (v & 31) & 1); };
+    const auto is_changed = [&](int v) { return changes && (s_changed[(v - lo) >> 5] >> (v & 31) & 1); };
 
-    // 4. the others, in groups of eight from the last boundary of eight values in memory on
-    const int before = (int)(((uintptr_t)(logits + lo) / sizeof(T)) & 7), first = lo - before;
-    const int n_groups = (hi - first + 7) / 8;
-    const uint8_t *left = (const uint8_t*)s_left, *owned = (const uint8_t*)s_owned;
-    const auto eight = [&](const uint8_t* bits, int g) {  // of group g's tokens
-        const int at = g * 8 - before;
-        const uint32_t x = bits[at >> 3];
-        return before ? ((x | (uint32_t)bits[(at >> 3) + 1] << 8) >> (at & 7)) & 0xFFu : x;
-    };
-    struct Eight {
-        T x[8];
-    };
-    const auto load = [&](int g) {
-        const int v = first + g * 8;
-        Eight e;
-        if (v >= 0 && v + 8 <= t.V) {
-            typedef uint4 alias __attribute__((may_alias));
-            const alias* p = (const alias*)(logits + v);
-            uint4 w[sizeof(e) / 16];
-#pragma unroll
-            for (int i = 0; i < (int)(sizeof(e) / 16); ++i) w[i] = p[i];
-            __builtin_memcpy(&e, w, sizeof(e));
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) e.x[i] = v + i >= 0 && v + i < t.V ? logits[v + i] : E::kNegInf;
+    // The value of an allowed, changed token of logit `logit`.
+    const auto value_of = [&](int v, float logit) INLINE {
+        int c = 0, e = -1;
+        for (int i = 0; i < n_draft; ++i) c += s_draft[i] == v;
+        bool seen = false;
+        if (prompt) {
+            const int w = v >> 5, b = v & 31;
+            seen = prompt[w] >> b & 1;
+            if (answered[w] >> b & 1) c += count[v];
         }
-        return e;
-    };
-    float top = -kInf;  // of this lane's groups; NaN where there is one
-    int top_group = -1;
-    for (int g0 = tid; g0 < n_groups; g0 += kT * kGroups) {
-        Eight e[kGroups];
-        uint32_t bits[kGroups];
-#pragma unroll
-        for (int i = 0; i < kGroups; ++i) {
-            const int g = g0 + i * kT;
-            bits[i] = g < n_groups ? eight(left, g) : 0;
-            e[i] = load(bits[i] ? g : 0);  // (a group without bits is not read)
-        }
-#pragma unroll
-        for (int i = 0; i < kGroups; ++i) {
-            const int g = g0 + i * kT;
-            float x[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t on = (uint32_t)((int32_t)(bits[i] << (31 - k)) >> 31);
-                x[k] = __uint_as_float((__float_as_uint(E::value(e[i].x[k])) & on) | (0xFF800000u & ~on));
+        for (int x0 = 0, x1 = b1 - b0; x0 < x1;) {  // its bias: at most one entry, in a list that does not rise too
+            const int mid = (x0 + x1) >> 1, at = bias_at(mid);
+            if (at == v) {
+                e = mid;
+                break;
             }
-            float m = x[0];
+            if (at < v) x0 = mid + 1; else x1 = mid;
+        }
+        double x = (double)logit;
+        if (seen || c > 0) x = x > 0.0 ? x / (double)repetition : x * (double)repetition;
+        x = x - (double)frequency * (double)c;
+        if (c > 0) x = x - (double)presence;
+        if (e >= 0) x = x + (double)t.bias_val[b0 + e];
+        if (kOut) out[v] = E::bits((float)x);
+        return x;
+    };
+
+    // The stream.  top: this lane's best unchanged token, as argmax_key has it; best: its best changed one;
+    // floor: what the row's best has at least; limit: what a logit needs to reach it.
+    uint64_t top = 0;
+    Best best{0, ~0u};
+    float limit = -kInf;
+    uint32_t floor_key = 0;
+    const float lift = fmaxf(-presence, 0.f), shrink = fminf(repetition, 1.f);
+    const auto set_floor = [&](uint32_t key) INLINE {
+        floor_key = key;
+        const float floor = key ? key_value(key) : -kInf;
+        limit = floor;
+        if (penalties && !every && floor < kInf) {  // (a NaN stays one: nothing is below it)
+            const float x = floor - lift - (fabsf(floor) + lift) * 0x1p-20f, y = x > 0.f ? x * shrink : x / shrink;
+            limit = fminf(y - fabsf(y) * 0x1p-20f, floor);  // (2^-20 covers these roundings)
+        }
+    };
+    const auto put = [&](int v, float logit) INLINE {
+        const uint32_t at = atomicAdd(&s_count, 1u);
+        if (at < kList) s_list[at] = make_uint2((uint32_t)v, __float_as_uint(logit));
+    };
+    // Of the eight tokens from v on those whose bits are set: to the list.
+    const auto put_all = [&](int v, uint32_t bits, const Eight<E>& e) INLINE {
+        uint32_t at = atomicAdd(&s_count, (uint32_t)__popc(bits));
 #pragma unroll
-            for (int k = 1; k < 8; ++k) m = __builtin_elementwise_maximum(m, x[k]);
-            if (m > top) top_group = g;
-            top = __builtin_elementwise_maximum(top, m);
-            if (kOut && g < n_groups) {
-                const int v = first + g * 8;
-                const uint32_t skip = eight(owned, g);
-                if (!skip && v >= lo && v + 8 <= hi && ((uintptr_t)(out + v) & 15) == 0) {
-                    Eight y;
+        for (int k = 0; k < 8; ++k)
+            if (bits >> k & 1) {
+                if (at < kList) s_list[at] = make_uint2((uint32_t)(v + k), __float_as_uint(e.value(k)));
+                ++at;
+            }
+    };
+    const auto fetch = [&](int g0, Eight<E>(&e)[kGroups]) INLINE {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) y.x[k] = bits[i] >> k & 1 ? e[i].x[k] : E::kNegInf;
-                    typedef uint4 alias __attribute__((may_alias));
-                    uint4 w[sizeof(y) / 16];
-                    __builtin_memcpy(w, &y, sizeof(y));
+        for (int i = 0; i < kGroups; ++i) {
+            const int g = min(g0 + i * kT, n_groups - 1);
+            const bool skip = !kOut && masked && allowed_of[g] == 0;  // nothing allowed: not read
+            e[i].load(logits + lo + (skip ? 0 : g * 8));
+        }
+    };
+    const auto stream = [&](int g0, Eight<E>(&e)[kGroups]) INLINE {
+        float m[kGroups], most = -kInf;
+        if (kOut || every) {
 #pragma unroll
-                    for (int q = 0; q < (int)(sizeof(y) / 16); ++q) ((alias*)(out + v))[q] = w[q];
-                } else {
+            for (int i = 0; i < kGroups; ++i) {
+                const int g = g0 + i * kT, v = lo + g * 8;
+                if (g >= n_groups) continue;
+                if (kOut) {
+                    Eight<E> x = e[i];
+                    if (masked) x.mask(allowed_of[g]);
+                    x.store(out + v);  // the changed ones once more, behind a barrier
+                }
+                const uint32_t changed = changed_of[g] & (masked ? allowed_of[g] : 0xFFu);
+                if (every && changed) put_all(v, changed, e[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            m[i] = e[i].value(0);
+#pragma unroll
+            for (int k = 1; k < 8; ++k) m[i] = __builtin_elementwise_maximum(m[i], e[i].value(k));
+            if (masked && allowed_of[min(g0 + i * kT, n_groups - 1)] == 0) m[i] = -kInf;  // (was not read)
+            most = __builtin_elementwise_maximum(most, m[i]);
+        }
+        if (__ballot(!(most < limit))) {
+            const uint32_t others = *(volatile uint32_t*)&s_floor;
+            if (others > floor_key) set_floor(others);
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+                const int g = g0 + i * kT, v = lo + g * 8;
+                const bool reaches = g < n_groups && !(m[i] < limit) && (!masked || allowed_of[g]);
+                if (!__ballot(reaches)) continue;
+                if (reaches) {
+                    Eight<E> x = e[i];
+#pragma unroll
+                    for (int p = 0; p < Eight<E>::kParts; ++p) asm volatile("" : "+v"(x.w[p]));  // taken apart anew, in few registers
+                    uint32_t bits = 0;  // of the tokens that reach the limit
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) bits |= (!(x.value(k) < limit) ? 1u : 0u) << k;
+                    if (masked) bits &= allowed_of[g];
+                    const uint32_t changed = changes ? changed_of[g] & bits : 0;
+                    bits &= ~changed;
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        if (v + k >= lo && v + k < hi && !(skip >> k & 1)) out[v + k] = bits[i] >> k & 1 ? e[i].x[k] : E::kNegInf;
+                        if (bits >> k & 1) top = max(top, argmax_key(x.value(k), (uint32_t)(v + k)));
+                    if (!every && changed) put_all(v, changed, x);
+                }
+                const uint32_t key = wave_max((uint32_t)(top >> 32));
+                if (key > floor_key) {
+                    set_floor(key);
+                    if ((tid & 63) == 0) atomicMax(&s_floor, key);
                 }
             }
         }
+    };
+    for (int g0 = tid; g0 - tid < n_groups; g0 += 2 * kT * kGroups) {
+        fetch(g0 + kT * kGroups, ahead);
+        stream(g0, now);
+        if (g0 - tid + kT * kGroups >= n_groups) break;
+        fetch(g0 + 2 * kT * kGroups, now);
+        stream(g0 + kT * kGroups, ahead);
     }
-    if (top > -kInf) {
-        const Eight e = load(top_group);
-        const uint32_t bits = eight(left, top_group);
-#pragma unroll
-        for (int k = 7; k >= 0; --k)
-            if ((bits >> k & 1) && E::value(e.x[k]) == top) best.take(order_key((double)top), (uint32_t)(first + top_group * 8 + k));
-    } else {  // a NaN, or nothing above -inf: this lane's groups once more, value by value
-        for (int g = tid; g < n_groups; g += kT) {
-            const uint32_t bits = eight(left, g);
-            for (int k = 0; k < 8; ++k)
-                if (bits >> k & 1) {
-                    const int v = first + g * 8 + k;
-                    best.take(order_key((double)E::value(logits[v])), (uint32_t)v);
-                }
+    if (tail >= 0) {
+        const bool on = is_allowed(tail), changed = is_changed(tail);
+        if (kOut) out[tail] = on ? logits[tail] : E::kNegInf;
+        if (on && changed) put(tail, E::value(logits[tail]));
+        else if (on) top = max(top, argmax_key(E::value(logits[tail]), (uint32_t)tail));
+    }
+    if (!every)
+        for (int e = tid; e < b1 - b0; e += kT) {
+            const int v = bias_at(e);
+            if (v >= lo && v < hi && is_allowed(v)) put(v, E::value(logits[v]));
         }
+    if (kOut) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    // The list; or, where it was too short, every changed token of the part, 64 neighbours to a wave.
+    const bool whole = s_count <= kList;
+    const int many = whole ? (int)s_count : (n_words + 1) / 2 * 64;
+    for (int i = tid; i < many; i += kT) {
+        uint2 e;
+        if (whole) {
+            e = s_list[i];
+        } else {
+            const int v = lo + i;
+            if (v >= hi || !is_changed(v) || !is_allowed(v)) continue;
+            e = make_uint2((uint32_t)v, __float_as_uint(E::value(logits[v])));
+        }
+        best.take(order_key(value_of((int)e.x, __uint_as_float(e.y))), e.x);
     }
+    if (top) best.take(order_key((double)key_value((uint32_t)(top >> 32))), (uint32_t)key_index(top));
 
     wave_best(best);
     if ((tid & 63) == 0) s_best[tid >> 6] = best;
     __syncthreads();
     if (tid == 0) {
 #pragma unroll
-        for (int w = 1; w < kT / 64; ++w) best.take(s_best[w].key, s_best[w].v);
+        for (int w = 1; w < kWaves; ++w) best.take(s_best[w].key, s_best[w].v);
         if (a.parts > 1) {
             a.best[row * a.parts + part] = TargetBest{best.key, best.v, 0};
         } else {
@@ -395,7 +449,7 @@ __global__ __launch_bounds__(64) void target_join_kernel(TargetArgs a) {
 }
 
 // A history row emptied: the counts only where there are any.
-__global__ __launch_bounds__(kT) void history_clear_kernel(dspark_history_t h, size_t words, const int32_t* rows,
+__global__ __launch_bounds__(kHistoryT) void history_clear_kernel(dspark_history_t h, size_t words, const int32_t* rows,
                                                            uint32_t* status) {
     const int i = blockIdx.x, r = rows ? rows[i] : i;
     if (r < 0 || r >= h.rows) {
@@ -404,7 +458,7 @@ __global__ __launch_bounds__(kT) void history_clear_kernel(dspark_history_t h, s
     }
     uint32_t *prompt = h.seen + (size_t)r * 2 * words, *answered = prompt + words;
     int32_t* count = h.count + (size_t)r * h.V;
-    for (size_t w = blockIdx.y * kT + threadIdx.x; w < words; w += (size_t)gridDim.y * kT) {
+    for (size_t w = blockIdx.y * kHistoryT + threadIdx.x; w < words; w += (size_t)gridDim.y * kHistoryT) {
         for (uint32_t x = answered[w]; x; x &= x - 1) {
             const size_t v = w * 32 + __ffs(x) - 1;
             if (v < (size_t)h.V) count[v] = 0;
@@ -415,7 +469,7 @@ __global__ __launch_bounds__(kT) void history_clear_kernel(dspark_history_t h, s
 }
 
 // A bit that is set already needs no atomic: of a prompt's tokens most have been there before.
-__global__ __launch_bounds__(kT) void history_add_kernel(dspark_history_t h, size_t words, const int32_t* tokens,
+__global__ __launch_bounds__(kHistoryT) void history_add_kernel(dspark_history_t h, size_t words, const int32_t* tokens,
                                                          int width, const int32_t* rows, int answered, uint32_t* status) {
     const int i = blockIdx.x, r = rows ? rows[i] : i;
     if (r < 0 || r >= h.rows) {
@@ -425,7 +479,7 @@ __global__ __launch_bounds__(kT) void history_add_kernel(dspark_history_t h, siz
     uint32_t* bits = h.seen + ((size_t)r * 2 + (answered ? 1 : 0)) * words;
     int32_t* count = h.count + (size_t)r * h.V;
     bool bad = false;
-    for (int at = blockIdx.y * kT + threadIdx.x; at < width; at += gridDim.y * kT) {
+    for (int at = blockIdx.y * kHistoryT + threadIdx.x; at < width; at += gridDim.y * kHistoryT) {
         const int v = tokens[(size_t)i * width + at];
         if (v < 0) continue;
         if (v >= h.V) {
@@ -441,10 +495,10 @@ __global__ __launch_bounds__(kT) void history_add_kernel(dspark_history_t h, siz
 
 template <class E>
 hipError_t run(const TargetArgs& a, hipStream_t s) {
-    const size_t lds = (size_t)(a.chunk / 32 + 2) * 4;
-    const dim3 grid(a.t.R, a.t.max_new, a.parts);
+    const dim3 grid((unsigned)a.t.R * (unsigned)a.parts, a.t.max_new);
+    const size_t lds = ((a.seen || a.t.ver_tokens || a.t.bias_off ? 1 : 0) + (a.t.allowed ? 1 : 0)) * (size_t)a.chunk / 8;
     if (a.t.adjusted)
-        hipLaunchKernelGGL((target_kernel<E, true>), grid, dim3(kT), 2 * lds, s, a);
+        hipLaunchKernelGGL((target_kernel<E, true>), grid, dim3(kT), lds, s, a);
     else
         hipLaunchKernelGGL((target_kernel<E, false>), grid, dim3(kT), lds, s, a);
     hipError_t e = hipGetLastError();
@@ -455,18 +509,19 @@ hipError_t run(const TargetArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// About four workgroups a compute unit, none of fewer than 4096 tokens.
-constexpr int kPerCu = 4, kLeastChunk = 4096;
-
-void target_split(int n_rows, int V, int num_cu, int& chunk, int& parts) {
-    const long long want = ((long long)kPerCu * std::min(num_cu, kAttendMaxCus) + n_rows - 1) / n_rows;
+void target_split(int rows, int V, int& chunk, int& parts) {
+    const long long want = ((long long)kWanted + rows - 1) / rows;
     const long long least = std::max<long long>((V + want - 1) / want, std::min(V, kLeastChunk));
     chunk = (int)std::min<long long>((least + 255) / 256 * 256, kMostChunk);
     parts = (int)(((long long)V + chunk - 1) / chunk);
 }
 
-size_t target_ws_parts(int n_rows, int V) {
-    return std::max<size_t>((size_t)kPerCu * kAttendMaxCus + n_rows, (size_t)n_rows * (((size_t)V + kMostChunk - 1) / kMostChunk));
+size_t target_ws_bytes(long long n_rows, int parts) { return (size_t)(n_rows * parts) * sizeof(TargetBest); }
+
+int target_most_parts(int V) {
+    int chunk, parts;
+    target_split(1, V, chunk, parts);
+    return parts;
 }
 
 hipError_t launch_target(const TargetArgs& a, hipStream_t s) {
@@ -475,15 +530,15 @@ hipError_t launch_target(const TargetArgs& a, hipStream_t s) {
 
 hipError_t launch_history_clear(const dspark_history_t& h, const int32_t* rows, int n, uint32_t* status, hipStream_t s) {
     const size_t words = dspark_history_words(h.V);
-    const int slices = (int)std::min<size_t>((words + kT - 1) / kT, 64);
-    hipLaunchKernelGGL(history_clear_kernel, dim3(n, slices), dim3(kT), 0, s, h, words, rows, status);
+    const int slices = (int)std::min<size_t>((words + kHistoryT - 1) / kHistoryT, 64);
+    hipLaunchKernelGGL(history_clear_kernel, dim3(n, slices), dim3(kHistoryT), 0, s, h, words, rows, status);
     return hipGetLastError();
 }
 
 hipError_t launch_history_add(const dspark_history_t& h, const int32_t* tokens, int n, int width, const int32_t* rows,
                               int answered, uint32_t* status, hipStream_t s) {
-    const int slices = std::min((width + kT - 1) / kT, 256);
-    hipLaunchKernelGGL(history_add_kernel, dim3(n, slices), dim3(kT), 0, s, h, dspark_history_words(h.V), tokens, width,
+    const int slices = std::min((width + kHistoryT - 1) / kHistoryT, 256);
+    hipLaunchKernelGGL(history_add_kernel, dim3(n, slices), dim3(kHistoryT), 0, s, h, dspark_history_words(h.V), tokens, width,
                        rows, answered, status);
     return hipGetLastError();
 }

@@ -157,7 +157,7 @@ int dspark_history_add(const dspark_history_t* h, const int32_t* tokens, int n, 
 
 size_t dspark_target_workspace_bytes(int n_rows, int V) {
     if (n_rows < 1 || V < 1 || V > kMostTokens) return 0;
-    return dspark::target_ws_parts(n_rows, V) * sizeof(dspark::TargetBest);
+    return dspark::target_ws_bytes(n_rows, dspark::target_most_parts(V));
 }
 
 int dspark_target_tokens(const dspark_target_t* t, uint32_t* status, void* ws, size_t ws_bytes, void* stream) {
@@ -208,8 +208,8 @@ int dspark_target_tokens(const dspark_target_t* t, uint32_t* status, void* ws, s
         a.count = t->history->count;
         a.words = dspark_history_words(t->V);
     }
-    dspark::target_split(t->n_rows, t->V, dspark::num_cu(), a.chunk, a.parts);
-    const size_t need = a.parts > 1 ? (size_t)t->n_rows * a.parts * sizeof(dspark::TargetBest) : 0;
+    dspark::target_split((int)std::min<long long>(t->n_rows, (long long)t->R * t->max_new), t->V, a.chunk, a.parts);
+    const size_t need = a.parts > 1 ? dspark::target_ws_bytes(t->n_rows, a.parts) : 0;
     if (need > ws_bytes || (need && !ws))
         return fail(DSPARK_EWORKSPACE, "%s: workspace of %zu bytes needed, %zu given%s", who, need, ws_bytes,
                     ws ? "" : " (NULL)");

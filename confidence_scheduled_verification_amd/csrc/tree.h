@@ -41,7 +41,7 @@ hipError_t launch_history_clear(const dspark_history_t& h, const int32_t* rows, 
 hipError_t launch_history_add(const dspark_history_t& h, const int32_t* tokens, int n, int width, const int32_t* rows,
                               int answered, uint32_t* status, hipStream_t s);
 
-// A part of a row's vocabulary done: the order key of its best value and that token (key 0: none).
+// The order key of a part's best value and that token (key 0: none).
 struct TargetBest {
     uint64_t key;
     uint32_t v, pad;
@@ -51,14 +51,14 @@ struct TargetArgs {
     const uint32_t* seen;  // NULL: no history
     const int32_t* count;
     size_t words;      // of a history row's bits
-    int chunk, parts;  // tokens of a part (a multiple of 32), parts of a row
-    TargetBest* best;  // [n_rows, parts] where a row has several parts
+    int chunk, parts;  // tokens of a part of a row (a multiple of 256), and parts of a row
+    TargetBest* best;  // [n_rows, parts] where a row has several
     uint32_t* status;
 };
-// The parts of a row for n_rows rows of V tokens (chunk and parts of the args), and the most
-// parts in all that up to n_rows rows can have.
-void target_split(int n_rows, int V, int num_cu, int& chunk, int& parts);
-size_t target_ws_parts(int n_rows, int V);
+// How as many rows of V tokens are taken apart.
+void target_split(int rows, int V, int& chunk, int& parts);
+size_t target_ws_bytes(long long n_rows, int parts);
+int target_most_parts(int V);  // however many rows there are
 hipError_t launch_target(const TargetArgs& a, hipStream_t s);
 
 }  // namespace dspark

@@ -163,7 +163,7 @@ def test_target_refuses():
     assert L.dspark_target_tokens(None, None, None, 0, None) == -1
     W = L.dspark_target_workspace_bytes
     assert W(0, 5) == W(5, 0) == W(5, (1 << 30) + 1) == 0
-    assert 0 < W(1, 129280) < 1 << 16 and W(2048, 129280) < 1 << 16 and W(8, 1 << 30) >= 8 * 8192 * 16
+    assert 0 < W(1, 129280) < 1 << 16 and W(2048, 129280) < 1 << 25 and W(8, 1 << 30) >= 8 * 8192 * 16
 
 
 def test_binding_refuses():
