@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import numpy as np
@@ -271,9 +272,9 @@ def dspark_get_chain_form() -> int:
     return int(lib().dspark_get_chain_form())
 
 
-def _shape(t, want, what):
-    if tuple(t.shape) != tuple(want):
-        raise ValueError(f"{what} must be {list(want)}, got {list(t.shape)}")
+def _shape(t, want, what, name=None):
+    if t.shape != want:
+        raise ValueError(f"{what if name is None else f'{what}: {name}'} must be {list(want)}, got {list(t.shape)}")
 
 
 def _chain_checks(base, markov: MarkovHead, prev0, tokens, chained_logits, what):
@@ -282,10 +283,10 @@ def _chain_checks(base, markov: MarkovHead, prev0, tokens, chained_logits, what)
     R, K, V = base.shape
     if V != markov.V:
         raise ValueError(f"{what}: base has V={V}, the Markov head V={markov.V}")
-    _shape(prev0, (R,), f"{what}: prev0")
-    _shape(tokens, (R, K), f"{what}: tokens")
+    _shape(prev0, (R,), what, "prev0")
+    _shape(tokens, (R, K), what, "tokens")
     if chained_logits is not None:
-        _shape(chained_logits, (R, K, V), f"{what}: chained_logits")
+        _shape(chained_logits, (R, K, V), what, "chained_logits")
     _contig(base, prev0, tokens, chained_logits)
     _elem_ok(base, markov.dtype, "base")
     if prev0.element_size() != 4 or tokens.element_size() != 4:
@@ -294,7 +295,7 @@ def _chain_checks(base, markov: MarkovHead, prev0, tokens, chained_logits, what)
 
 
 def _ws_bytes(ws):
-    return 0 if ws is None else ws.numel() * ws.element_size()
+    return 0 if ws is None else ws.nbytes
 
 
 def dspark_chain(base, markov: MarkovHead, prev0, tokens, chained_logits=None, status=None, ws=None, stream=None):
@@ -351,7 +352,7 @@ def dspark_allocate(order, b_star, R: int, K: int, prefix_len, offsets, ver_idx,
 def _step_checks(base, markov: MarkovHead, prev0, conf, verify_cost, draft_cost, out: "StepBuffers", ws, status,
                  what, need_ws=True):
     R, K, V = _chain_checks(base, markov, prev0, out.tokens, None, what)
-    _shape(conf, (R, K), f"{what}: conf")
+    _shape(conf, (R, K), what, "conf")
     for t, n in ((conf, "conf"), (verify_cost, "verify_cost"), (draft_cost, "draft_cost")):
         if t.dtype != _torch().float32:
             raise ValueError(f"{what}: {n} must be float32")
@@ -559,9 +560,8 @@ class PagedCache:
         self._ref = ctypes.byref(self.handle)
 
 
-def _on(cache, what: str, stream, ints=(), others=(), words=()) -> int:
-    """The stream of a call on `cache` (or what else has a device): its device is the current one, and
-    every tensor of the call lies there; `ints` are int32, `words` int64, both densely packed."""
+def _misplaced(cache, what: str, ints, others, words):
+    """What is wrong with a call's tensors, for `_on`, which has found that something may be."""
     torch = _torch()
     device = cache.device
     for t in ints:
@@ -577,7 +577,25 @@ def _on(cache, what: str, stream, ints=(), others=(), words=()) -> int:
             raise ValueError(f"{what}: a tensor on {t.device}, the cache is on {device}")
     if device.type != "cuda" or device.index != torch.cuda.current_device():
         raise ValueError(f"{what}: the cache is on {device}, which is not the current GPU")
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
+
+
+def _on(cache, what: str, stream, ints=(), others=(), words=()) -> int:
+    """The stream of a call on `cache` (or what else has a device): its device is the current one, and
+    every tensor of the call lies there; `ints` are int32, `words` int64, both densely packed."""
+    torch = _torch()
+    index, i32, fine = cache.device.index, torch.int32, True
+    for t in ints:
+        if t is not None and (t.dtype is not i32 or t.get_device() != index or not t.is_contiguous()):
+            fine = False
+    for t in others:
+        if t is not None and t.get_device() != index:
+            fine = False
+    for t in words:
+        if t is not None and (t.dtype is not torch.int64 or t.get_device() != index or not t.is_contiguous()):
+            fine = False
+    if not fine or index is None or index != torch._C._cuda_getDevice():
+        _misplaced(cache, what, ints, others, words)
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
 
 
 def pages_workspace(cache: PagedCache, n: int):
@@ -596,9 +614,10 @@ def cache_workspace(cache: PagedCache, R: int, H: int, max_new: int, n_groups: i
 
 
 def _offsets_rows(cache: PagedCache, offsets, what: str) -> int:
-    if offsets.dim() != 1 or not 1 <= offsets.shape[0] <= cache.rows + 1:
+    shape = offsets.shape
+    if len(shape) != 1 or not 1 <= shape[0] <= cache.rows + 1:
         raise ValueError(f"{what}: offsets must be [R+1] with R at most the cache's {cache.rows} rows")
-    return offsets.shape[0] - 1
+    return shape[0] - 1
 
 
 def dspark_pages_reserve(cache: PagedCache, offsets, lead: int, granted, ws, status=None, stream=None):
@@ -650,26 +669,27 @@ def dspark_pages_compact(cache: PagedCache, page_map, n_live, ws, status=None, s
                                       st))
 
 
-def _packed(cache: PagedCache, t, heads, what: str):
+def _packed(cache: PagedCache, t, heads, what: str, name: str):
     """Rows of [heads, head_dim] whose heads are densely packed; the stride between rows."""
-    if t.dim() != 3 or t.shape[1:] != (heads, cache.head_dim) or t.dtype != cache.torch_dtype:
-        raise ValueError(f"{what} must be {cache.torch_dtype} [rows, {heads}, {cache.head_dim}], "
-                         f"got {t.dtype} {list(t.shape)}")
+    shape, D = t.shape, cache.head_dim
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D or t.dtype is not cache.torch_dtype:
+        raise ValueError(f"{what}: {name} must be {cache.torch_dtype} [rows, {heads}, {D}], got {t.dtype} {list(shape)}")
     rows, across, along = t.stride()
-    if t.numel() and (along != 1 or (heads > 1 and across != cache.head_dim)):
-        raise ValueError(f"{what}: each row's heads must be densely packed")
-    return rows if t.shape[0] > 1 else heads * cache.head_dim
+    if (along != 1 or (heads > 1 and across != D)) and t.numel():
+        raise ValueError(f"{what}: {name}: each row's heads must be densely packed")
+    return rows if shape[0] > 1 else heads * D
 
 
 def dspark_cache_append(cache: PagedCache, layer: int, k_new, v_new, offsets, lead: int, max_new: int, status=None,
                         stream=None):
     """One layer's K and V of a step's rows into the reserved pages."""
-    R = _offsets_rows(cache, offsets, "dspark_cache_append")
-    ks = _packed(cache, k_new, cache.n_kv_heads, "dspark_cache_append: k_new")
-    vs = _packed(cache, v_new, cache.n_kv_heads, "dspark_cache_append: v_new")
+    what = "dspark_cache_append"
+    R = _offsets_rows(cache, offsets, what)
+    ks = _packed(cache, k_new, cache.n_kv_heads, what, "k_new")
+    vs = _packed(cache, v_new, cache.n_kv_heads, what, "v_new")
     if v_new.shape[0] != k_new.shape[0]:
         raise ValueError("dspark_cache_append: k_new and v_new must have as many rows")
-    st = _on(cache, "dspark_cache_append", stream, (offsets,), (k_new, v_new, status))
+    st = _on(cache, what, stream, (offsets,), (k_new, v_new, status))
     _check(lib().dspark_cache_append(cache._ref, layer, _p(k_new), ks, _p(v_new), vs, k_new.shape[0], _p(offsets), lead,
                                      R, max_new, _p(status), st))
 
@@ -678,8 +698,8 @@ def _attend(what: str, entry, cache: PagedCache, layer: int, q, offsets, lead: i
             shared, ws, status, stream):
     R = _offsets_rows(cache, offsets, what)
     H = q.shape[1] if q.dim() == 3 else 0
-    qs = _packed(cache, q, H, f"{what}: q")
-    os_ = _packed(cache, out, H, f"{what}: out")
+    qs = _packed(cache, q, H, what, "q")
+    os_ = _packed(cache, out, H, what, "out")
     if out.shape[0] != q.shape[0]:
         raise ValueError(f"{what}: q and out must have as many rows")
     if lse is not None and (tuple(lse.shape) != (q.shape[0], H) or lse.dtype != _torch().float32 or
@@ -692,8 +712,8 @@ def _attend(what: str, entry, cache: PagedCache, layer: int, q, offsets, lead: i
         if table.dim() != 2:
             raise ValueError(f"{what}: shared_table must be [groups, width]")
         n_groups, width = table.shape
-        _shape(off, (n_groups + 1,), f"{what}: group_off")
-        _shape(pages, (n_groups,), f"{what}: shared_pages")
+        _shape(off, (n_groups + 1,), what, "group_off")
+        _shape(pages, (n_groups,), what, "shared_pages")
     if anc is not None and anc.numel() < q.shape[0]:
         raise ValueError(f"{what}: anc has {anc.numel()} words for {q.shape[0]} rows")
     st = _on(cache, what, stream, (offsets, off, table, pages), (q, out, lse, ws, status), (anc,))
@@ -728,9 +748,9 @@ def dspark_tree_merge(tokens, prefix_len, S: int, counts, offsets, ver_tokens, p
         raise ValueError(f"{what}: tokens must be [R*S, K] with S = {S}")
     R, K = tokens.shape[0] // S, tokens.shape[1]
     if prefix_len is not None:
-        _shape(prefix_len, (R * S,), f"{what}: prefix_len")
-    _shape(counts, (R,), f"{what}: counts")
-    _shape(offsets, (R + 1,), f"{what}: offsets")
+        _shape(prefix_len, (R * S,), what, "prefix_len")
+    _shape(counts, (R,), what, "counts")
+    _shape(offsets, (R + 1,), what, "offsets")
     if ver_tokens.numel() < R * S * K or parent.numel() < R * S * K + R:
         raise ValueError(f"{what}: ver_tokens and parent must have room for {R * S * K} drafts of {R} requests")
     st = _on(tokens, what, stream, (tokens, prefix_len, counts, offsets, ver_tokens, parent), (status,))
@@ -757,11 +777,11 @@ def dspark_accept_tree(ver_tokens, offsets, parent, target, accept_len, path, ne
     if path.dim() != 2:
         raise ValueError(f"{what}: path must be [R, K]")
     (R, K), n = path.shape, ver_tokens.numel()
-    _shape(offsets, (R + 1,), f"{what}: offsets")
-    _shape(accept_len, (R,), f"{what}: accept_len")
-    _shape(next_prev0, (R,), f"{what}: next_prev0")
+    _shape(offsets, (R + 1,), what, "offsets")
+    _shape(accept_len, (R,), what, "accept_len")
+    _shape(next_prev0, (R,), what, "next_prev0")
     if out_tokens is not None:
-        _shape(out_tokens, (R, K + 1), f"{what}: out_tokens")
+        _shape(out_tokens, (R, K + 1), what, "out_tokens")
     if parent.numel() < n + R or target.numel() < n + R:
         raise ValueError(f"{what}: parent and target must have an entry for each of {n} drafts and {R} first nodes")
     st = _on(offsets, what, stream, (ver_tokens, offsets, parent, target, accept_len, path, next_prev0, out_tokens), (status,))
@@ -775,9 +795,9 @@ def dspark_cache_keep_path(cache: PagedCache, path, accept_len, lead: int, grant
     if path.dim() != 2 or path.shape[0] > cache.rows:
         raise ValueError(f"{what}: path must be [R, K] with R at most {cache.rows}")
     R, K = path.shape
-    _shape(accept_len, (R,), f"{what}: accept_len")
+    _shape(accept_len, (R,), what, "accept_len")
     if granted is not None:
-        _shape(granted, (R,), f"{what}: granted")
+        _shape(granted, (R,), what, "granted")
     st = _on(cache, what, stream, (path, accept_len, granted), (status,))
     _check(lib().dspark_cache_keep_path(cache._ref, _p(path), K, _p(accept_len), _p(granted), lead, R, _p(status), st))
 
@@ -822,9 +842,9 @@ def dspark_cache_append_rotary(cache: PagedCache, layer: int, rotary: Rotary, q,
     what = "dspark_cache_append_rotary"
     R = _offsets_rows(cache, offsets, what)
     H = q.shape[1] if q.dim() == 3 else 0
-    qs, os_ = _packed(cache, q, H, f"{what}: q"), _packed(cache, q_out, H, f"{what}: q_out")
-    ks = _packed(cache, k_new, cache.n_kv_heads, f"{what}: k_new")
-    vs = _packed(cache, v_new, cache.n_kv_heads, f"{what}: v_new")
+    qs, os_ = _packed(cache, q, H, what, "q"), _packed(cache, q_out, H, what, "q_out")
+    ks = _packed(cache, k_new, cache.n_kv_heads, what, "k_new")
+    vs = _packed(cache, v_new, cache.n_kv_heads, what, "v_new")
     n = k_new.shape[0]
     if v_new.shape[0] != n or q.shape[0] != n or q_out.shape[0] != n:
         raise ValueError(f"{what}: q, q_out, k_new and v_new must have as many rows")
@@ -858,7 +878,7 @@ class History:
             setattr(self, name, t)
         self.rows, self.V, self.device = rows, V, device
         self.handle = dspark_history_t(_p(self.seen), _p(self.count), rows, V)
-        self._ref = ctypes.byref(self.handle)
+        self._ref, self.address = ctypes.byref(self.handle), ctypes.addressof(self.handle)
 
 
 def dspark_history_clear(history: History, rows=None, status=None, stream=None):
@@ -876,23 +896,29 @@ def dspark_history_add(history: History, tokens, answered: bool, rows=None, stat
         raise ValueError(f"{what}: tokens must be [n, width]")
     n, width = tokens.shape
     if rows is not None:
-        _shape(rows, (n,), f"{what}: rows")
+        _shape(rows, (n,), what, "rows")
     st = _on(history, what, stream, (tokens, rows), (status,))
     _check(lib().dspark_history_add(history._ref, _p(tokens), n, width, _p(rows), int(answered), _p(status), st))
 
 
 def target_workspace(n_rows: int, V: int, device="cuda"):
-    """Workspace of dspark_target_tokens for up to n_rows rows of up to V tokens."""
+    """Workspace of dspark_target_tokens for up to n_rows rows of up to V tokens, zero-filled as the library wants it."""
     nbytes = int(lib().dspark_target_workspace_bytes(n_rows, V))
-    return _torch().empty((nbytes + 15) // 16 * 4, dtype=_torch().int32, device=device)
+    return _torch().zeros((nbytes + 15) // 16 * 4, dtype=_torch().int32, device=device)
 
 
-def _logit_rows(t, like, what: str):
-    if t.dim() != 2 or (like is not None and (t.shape != like.shape or t.dtype != like.dtype)):
-        raise ValueError(f"{what} must be [rows, V]" + ("" if like is None else " as logits are"))
-    if t.numel() and t.stride(1) != 1:
-        raise ValueError(f"{what}: each row's values must be densely packed")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _logit_rows(t, like, what: str, name: str):
+    shape = t.shape
+    if len(shape) != 2 or (like is not None and (shape != like.shape or t.dtype is not like.dtype)):
+        raise ValueError(f"{what}: {name} must be [rows, V]" + ("" if like is None else " as logits are"))
+    rows, along = t.stride()
+    if along != 1 and t.numel():
+        raise ValueError(f"{what}: {name}: each row's values must be densely packed")
+    return rows if shape[0] > 1 else shape[1]
+
+
+_TARGET = struct.Struct("=Qq6i12Qq4iQQq")  # dspark_target_t
+assert _TARGET.size == ctypes.sizeof(dspark_target_t)
 
 
 def dspark_target_tokens(logits, offsets, lead: int, max_new: int, target, history: Optional[History] = None,
@@ -902,45 +928,46 @@ def dspark_target_tokens(logits, offsets, lead: int, max_new: int, target, histo
     presence, frequency: float32 [R] or None each), biases (bias_off [R+1], bias_tok, bias_val) and the masks
     allowed [n, words] (row allowed_row[t] binds row t).  `adjusted` [rows, V] receives the processed logits."""
     what, torch = "dspark_target_tokens", _torch()
-    dtypes = {torch.float32: DSPARK_F32, torch.bfloat16: DSPARK_BF16, torch.float16: DSPARK_F16}
-    if logits.dtype not in dtypes:
-        raise ValueError(f"{what}: logits must be float32, bfloat16 or float16, got {logits.dtype}")
-    stride = _logit_rows(logits, None, f"{what}: logits")
-    out_stride = 0 if adjusted is None else _logit_rows(adjusted, logits, f"{what}: adjusted")
+    kind, f32 = logits.dtype, torch.float32
+    dtype = DSPARK_BF16 if kind is torch.bfloat16 else DSPARK_F32 if kind is f32 else DSPARK_F16
+    if dtype == DSPARK_F16 and kind is not torch.float16:
+        raise ValueError(f"{what}: logits must be float32, bfloat16 or float16, got {kind}")
+    stride = _logit_rows(logits, None, what, "logits")
+    out_stride = 0 if adjusted is None else _logit_rows(adjusted, logits, what, "adjusted")
     n_rows, V = logits.shape
-    if offsets.dim() != 1 or offsets.shape[0] < 1:
+    if len(offsets.shape) != 1 or offsets.shape[0] < 1:
         raise ValueError(f"{what}: offsets must be [R+1]")
     R = offsets.shape[0] - 1
     if target.numel() < n_rows or (anc is not None and anc.numel() < n_rows) or \
             (allowed_row is not None and allowed_row.numel() < n_rows):
         raise ValueError(f"{what}: target, anc and allowed_row must have an entry for each of {n_rows} rows")
-    penalties = (None, None, None) if penalties is None else tuple(penalties)
+    repetition, presence, frequency = (None, None, None) if penalties is None else penalties
     off = tok = val = None
     if bias is not None:
         off, tok, val = bias
-        _shape(off, (R + 1,), f"{what}: bias_off")
-        _shape(val, tuple(tok.shape), f"{what}: bias_val")
-    for t in (*penalties, val):
-        if t is not None and (t.dtype is not torch.float32 or not t.is_contiguous()):
+        _shape(off, (R + 1,), what, "bias_off")
+        _shape(val, tok.shape, what, "bias_val")
+    for t in (repetition, presence, frequency, val):
+        if t is not None and (t.dtype is not f32 or not t.is_contiguous()):
             raise ValueError(f"{what}: penalties and bias_val must be contiguous float32")
-    for t in penalties:
-        if t is not None:
-            _shape(t, (R,), f"{what}: penalties")
-    if allowed is not None and (allowed.dim() != 2 or allowed.dtype is not torch.int32 or
-                                (allowed.numel() and allowed.stride(1) != 1)):
-        raise ValueError(f"{what}: allowed must be int32 [masks, words] with densely packed rows")
+        if t is not None and t is not val:
+            _shape(t, (R,), what, "penalties")
+    n_allowed = pitch = 0
+    if allowed is not None:
+        if len(allowed.shape) != 2 or allowed.dtype is not torch.int32 or (allowed.stride(1) != 1 and allowed.numel()):
+            raise ValueError(f"{what}: allowed must be int32 [masks, words] with densely packed rows")
+        n_allowed, words = allowed.shape
+        pitch = allowed.stride(0) if n_allowed > 1 else words
     if history is not None and history.device != logits.device:
         raise ValueError(f"{what}: the history is on {history.device}, logits on {logits.device}")
     st = _on(logits, what, stream, (offsets, target, node_tokens, off, tok, allowed_row),
-             (*penalties, val, allowed, adjusted, ws, status), (anc,))
-    call = dspark_target_t(
-        _p(logits), stride, n_rows, V, dtypes[logits.dtype], R, lead, max_new, _p(offsets),
-        None if history is None else ctypes.addressof(history.handle), *(_p(t) for t in penalties), _p(node_tokens), _p(anc),
-        _p(off), _p(tok), _p(val), _p(allowed), _p(allowed_row),
-        0 if allowed is None else (allowed.stride(0) if allowed.shape[0] > 1 else allowed.shape[1]),
-        0 if node_tokens is None else node_tokens.numel(), 0 if tok is None else tok.numel(),
-        0 if allowed is None else allowed.shape[0], 0, _p(target), _p(adjusted), out_stride)
-    _check(lib().dspark_target_tokens(ctypes.byref(call), _p(status), _p(ws), _ws_bytes(ws), st))
+             (repetition, presence, frequency, val, allowed, adjusted, ws, status), (anc,))
+    call = _TARGET.pack(
+        logits.data_ptr(), stride, n_rows, V, dtype, R, lead, max_new, offsets.data_ptr(), 0 if history is None else history.address,
+        _p(repetition) or 0, _p(presence) or 0, _p(frequency) or 0, _p(node_tokens) or 0, _p(anc) or 0, _p(off) or 0, _p(tok) or 0,
+        _p(val) or 0, _p(allowed) or 0, _p(allowed_row) or 0, pitch, 0 if node_tokens is None else node_tokens.numel(),
+        0 if tok is None else tok.numel(), n_allowed, 0, target.data_ptr(), _p(adjusted) or 0, out_stride)
+    _check(lib().dspark_target_tokens(call, _p(status), _p(ws), _ws_bytes(ws), st))
 
 
 def dspark_set_launch_mode(mode: int):

@@ -30,6 +30,7 @@ constexpr int kMostChunk = 131072;    // tokens of a part: twice 16 KB of bits i
 constexpr int kLeastChunk = 4096;
 constexpr int kWanted = 2 * kAttendMaxCus;  // workgroups, where there are few rows
 constexpr int kList = 2048;           // changed tokens listed; where there are more, all of them are gone through
+constexpr int kCounted = 4096;        // rows whose parts are counted in the workspace
 constexpr int kHistoryT = 256;
 constexpr float kInf = __builtin_huge_valf();
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -417,19 +418,36 @@ __global__ __launch_bounds__(kT, kPerSimd) void target_kernel(TargetArgs a) {
     wave_best(best);
     if ((tid & 63) == 0) s_best[tid >> 6] = best;
     __syncthreads();
-    if (tid == 0) {
+    if (tid >= 64) return;
+    best = s_best[0];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) best.take(s_best[w].key, s_best[w].v);
-        if (a.parts > 1) {
-            a.best[row * a.parts + part] = TargetBest{best.key, best.v, 0};
-        } else {
-            t.target[row] = best.key ? (int32_t)best.v : -1;
-            if (!best.key) raise_status(a.status, kStatusNoToken);
+    for (int w = 1; w < kWaves; ++w) best.take(s_best[w].key, s_best[w].v);
+    if (a.parts > 1) {
+        // The part that comes last joins all of the row's.  What the others have left is there when their
+        // counts are: written through to where all of the device sees it, and waited for.
+        TargetBest* parts = a.best + row * a.parts;
+        int came = 0;
+        if (tid == 0) {
+            __hip_atomic_store(&parts[part].key, best.key, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(&parts[part].v, best.v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            if (a.came) came = (int)__hip_atomic_fetch_add(&a.came[row], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
+        if (!a.came || __builtin_amdgcn_readfirstlane(came) != a.parts - 1) return;
+        asm volatile("" ::: "memory");
+        for (int p = tid; p < a.parts; p += 64)
+            best.take(__hip_atomic_load(&parts[p].key, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT),
+                      __hip_atomic_load(&parts[p].v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+        wave_best(best);
+        if (tid == 0) __hip_atomic_store(&a.came[row], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next call
+    }
+    if (tid == 0) {
+        t.target[row] = best.key ? (int32_t)best.v : -1;
+        if (!best.key) raise_status(a.status, kStatusNoToken);
     }
 }
 
-// The best of a row's parts: a wave to a row.
+// The same in a launch of its own, a wave to a row, for more rows than are counted.
 __global__ __launch_bounds__(64) void target_join_kernel(TargetArgs a) {
     int o, n;
     long long start;
@@ -501,8 +519,8 @@ hipError_t run(const TargetArgs& a, hipStream_t s) {
         hipLaunchKernelGGL((target_kernel<E, true>), grid, dim3(kT), lds, s, a);
     else
         hipLaunchKernelGGL((target_kernel<E, false>), grid, dim3(kT), lds, s, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.parts == 1) return e;
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.parts == 1 || a.came) return e;
     hipLaunchKernelGGL(target_join_kernel, dim3(a.t.R, a.t.max_new), dim3(64), 0, s, a);
     return hipGetLastError();
 }
@@ -516,7 +534,16 @@ void target_split(int rows, int V, int& chunk, int& parts) {
     parts = (int)(((long long)V + chunk - 1) / chunk);
 }
 
-size_t target_ws_bytes(long long n_rows, int parts) { return (size_t)(n_rows * parts) * sizeof(TargetBest); }
+// The counts have a place of their own in every call, whatever its rows, or what another call has left
+// would be taken for them.
+void target_ws_layout(TargetArgs& a, void* ws) {
+    a.came = a.t.n_rows <= kCounted ? (uint32_t*)ws : nullptr;
+    a.best = (TargetBest*)((uint32_t*)ws + kCounted);
+}
+
+size_t target_ws_bytes(long long n_rows, int parts) {
+    return kCounted * sizeof(uint32_t) + (size_t)(n_rows * parts) * sizeof(TargetBest);
+}
 
 int target_most_parts(int V) {
     int chunk, parts;

@@ -214,7 +214,7 @@ int dspark_target_tokens(const dspark_target_t* t, uint32_t* status, void* ws, s
         return fail(DSPARK_EWORKSPACE, "%s: workspace of %zu bytes needed, %zu given%s", who, need, ws_bytes,
                     ws ? "" : " (NULL)");
     if ((uintptr_t)ws & 15u) return fail(DSPARK_EINVAL, "%s: workspace must be 16-byte aligned", who);
-    a.best = (dspark::TargetBest*)ws;
+    if (need) dspark::target_ws_layout(a, ws);
     return done(dspark::launch_target(a, (hipStream_t)stream), who);
 }
 

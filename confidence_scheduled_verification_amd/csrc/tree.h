@@ -52,11 +52,15 @@ struct TargetArgs {
     const int32_t* count;
     size_t words;      // of a history row's bits
     int chunk, parts;  // tokens of a part of a row (a multiple of 256), and parts of a row
-    TargetBest* best;  // [n_rows, parts] where a row has several
+    // where a row has several parts: the parts of each row that have come, 0 between the calls (NULL: a launch
+    // of its own joins them), and what each of them has, [n_rows, parts]
+    uint32_t* came;
+    TargetBest* best;
     uint32_t* status;
 };
 // How as many rows of V tokens are taken apart.
 void target_split(int rows, int V, int& chunk, int& parts);
+void target_ws_layout(TargetArgs& a, void* ws);
 size_t target_ws_bytes(long long n_rows, int parts);
 int target_most_parts(int V);  // however many rows there are
 hipError_t launch_target(const TargetArgs& a, hipStream_t s);

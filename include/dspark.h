@@ -849,7 +849,9 @@ typedef struct dspark_target {
     void* adjusted;
     int64_t adjusted_stride;
 } dspark_target_t;
-/* Bytes of workspace (16-byte aligned) for up to n_rows rows of up to V tokens. */
+/* Bytes of workspace (16-byte aligned) for up to n_rows rows of up to V tokens.  Zero-fill it once,
+ * before its first use: the kernel counts the parts of a row in it, and leaves the counts at zero for
+ * the next call, of whatever sizes. */
 size_t dspark_target_workspace_bytes(int n_rows, int V);
 int dspark_target_tokens(const dspark_target_t* call, uint32_t* status, void* ws, size_t ws_bytes, void* stream);
 

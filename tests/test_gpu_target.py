@@ -101,7 +101,7 @@ class Step:
         self.adjusted = self.out[shift:shift + self.n * self.V].view(self.n, self.V) if adjusted else None
         self.status = torch.zeros(1, dtype=torch.int32, device=cu.DEV)
         ws = B.target_workspace(self.n, self.V)
-        ws.fill_(-1)
+        ws[4096:] = -1  # behind the counts nothing is counted on
         return dict(self.upload(), ws=ws, status=self.status, adjusted=self.adjusted)
 
     def call(self, kw):
@@ -349,6 +349,40 @@ def test_strides_streams_and_captured_calls_share_a_workspace():
         torch.cuda.synchronize()
         for s, w, e in ((a, want[0], eager[0]), (b, want[1], eager[1])):
             assert s.target.tolist() == [w.get(t, -7) for t in range(s.n)] and torch.equal(s.out, e)
+
+
+def test_one_workspace_for_calls_of_all_sizes():
+    # rows in parts, whole rows, more rows than are counted: each call finds the counts as it needs them
+    _say("target, one workspace")
+    big = Step(20, [1] * 4200, 131100, "bf16", lead=1, seen=0, biased=0, masks=0, tree=False, pad=0)
+    big.penalties, big.history, big.drafts = [None] * 3, None, None
+    steps = [Step(21, [3, 1], 60000, "bf16"), Step(22, [1], 129280, "fp32"), Step(23, [7] * 100, 5000, "fp16"), big, Step(24, [40], 9000, "bf16")]
+    ws = B.target_workspace(4200, 131100)
+    want = [s.want()[0] if s is not big else None for s in steps]
+    rows = big.logits.float()
+    want[3] = dict(enumerate(torch.where(rows == rows.amax(1, keepdim=True), torch.arange(131100, device=cu.DEV), 131100).amin(1).tolist()))
+    del rows
+    for order in ((0, 1, 2, 3, 4), (4, 3, 1, 0, 2), (1, 1, 0, 3, 3)):
+        for i in order:
+            s = steps[i]
+            kw = dict(s.prepared(adjusted=False), ws=ws)
+            s.call(kw)
+            torch.cuda.synchronize()
+            assert s.target.tolist() == [want[i].get(t, -7) for t in range(s.n)], i
+    assert not ws[:4096].any()
+
+
+@pytest.mark.parametrize("penalty", [(0.25, 0.0, 0.0), (1.0, -3.0, 0.0), (1.0, 0.0, -0.5), (0.8, -0.5, 0.0), (0.9, 0.25, -0.25), (0.0, 0.0, 0.0),
+                                     (-1.5, 0.0, 0.0), (1e-30, 0.0, 0.0), (1e30, 0.0, 0.0), (1.2, math.inf, 0.0), (1.0, -math.inf, 0.0),
+                                     (math.inf, 0.0, 0.0), (math.nan, 0.0, 0.0), (1.0, math.nan, 0.0)])
+def test_penalties_that_lift_or_are_no_numbers(penalty):
+    # tokens whose logits alone would never win, and every value that a parameter may have
+    _say("target, lifting penalties", penalty)
+    for dtype, V in (("fp32", 5003), ("bf16", 9000)):
+        s = Step(30, [5, 1, 12], V, dtype, seen=60, biased=4)
+        s.logits -= 6.0 if penalty[0] < 1 else 0.0  # negative ones are lifted by a repetition below one
+        s.penalties = [[p] * 3 for p in penalty]
+        s.check()
 
 
 @pytest.mark.parametrize("rows,V,n,width", [(1, 1, 1, 5), (4, 130, 3, 70), (9, 4096, 9, 1), (5, 70001, 40, 3000)])
