@@ -24,8 +24,8 @@ namespace {
 
 #define INLINE __attribute__((always_inline))
 constexpr int kT = 512, kWaves = kT / 64;
-constexpr int kPerSimd = 6;           // waves that the registers leave room for
-constexpr int kGroups = 3;            // of eight logits: a lane's loads under way, twice
+constexpr int kPerSimd = 7;           // waves that the registers leave room for
+constexpr int kGroups = 2;            // of eight logits: a lane's loads under way, twice
 constexpr int kMostChunk = 131072;    // tokens of a part: twice 16 KB of bits in LDS
 constexpr int kLeastChunk = 4096;
 constexpr int kWanted = 2 * kAttendMaxCus;  // workgroups, where there are few rows
@@ -153,7 +153,9 @@ __global__ __launch_bounds__(kT, kPerSimd) void target_kernel(TargetArgs a) {
     static_assert(DSPARK_TARGET_MAX_ROWS <= kT, "a draft to a lane");
     __shared__ uint32_t s_count, s_floor;
     __shared__ Best s_best[kWaves];
-    const int r = blockIdx.x % t.R, part = blockIdx.x / t.R, j = blockIdx.y, tid = threadIdx.x;
+    // (a request's rows on different XCDs, every eighth workgroup being on the same: requests of many rows
+    // would keep one busy longer than the others)
+    const int part = blockIdx.x / t.R, j = blockIdx.y, r = (blockIdx.x % t.R + j) % t.R, tid = threadIdx.x;
     int o, n;
     long long start;
     uint32_t bad = 0;
@@ -259,33 +261,26 @@ __global__ __launch_bounds__(kT, kPerSimd) void target_kernel(TargetArgs a) {
     const auto is_allowed = [&](int v) { return !masked || (s_allowed[(v - lo) >> 5] >> (v & 31) & 1); };
     const auto is_changed = [&](int v) { return changes && (s_changed[(v - lo) >> 5] >> (v & 31) & 1); };
 
-    // The value of an allowed, changed token of logit `logit`.
-    const auto value_of = [&](int v, float logit) INLINE {
-        int c = 0, e = -1;
-        for (int i = 0; i < n_draft; ++i) c += s_draft[i] == v;
-        bool seen = false;
-        if (prompt) {
-            const int w = v >> 5, b = v & 31;
-            seen = prompt[w] >> b & 1;
-            if (answered[w] >> b & 1) c += count[v];
-        }
-        for (int x0 = 0, x1 = b1 - b0; x0 < x1;) {  // its bias: at most one entry, in a list that does not rise too
+    // The place of v among the biases, -1 for none: at most one, in a list that does not rise too.
+    const auto find = [&](int v) INLINE {
+        for (int x0 = 0, x1 = b1 - b0; x0 < x1;) {
             const int mid = (x0 + x1) >> 1, at = bias_at(mid);
-            if (at == v) {
-                e = mid;
-                break;
-            }
+            if (at == v) return mid;
             if (at < v) x0 = mid + 1; else x1 = mid;
         }
+        return -1;
+    };
+    // The value of token v, which is in the prompt (seen) or has been answered c times before the drafts.
+    const auto value_of = [&](int v, float logit, bool seen, int c, bool biased, float by) INLINE {
+        for (int i = 0; i < n_draft; ++i) c += s_draft[i] == v;
         double x = (double)logit;
         if (seen || c > 0) x = x > 0.0 ? x / (double)repetition : x * (double)repetition;
         x = x - (double)frequency * (double)c;
         if (c > 0) x = x - (double)presence;
-        if (e >= 0) x = x + (double)t.bias_val[b0 + e];
+        if (biased) x = x + (double)by;
         if (kOut) out[v] = E::bits((float)x);
         return x;
     };
-
     // The stream.  top: this lane's best unchanged token, as argmax_key has it; best: its best changed one;
     // floor: what the row's best has at least; limit: what a logit needs to reach it.
     uint64_t top = 0;
@@ -293,9 +288,11 @@ __global__ __launch_bounds__(kT, kPerSimd) void target_kernel(TargetArgs a) {
     float limit = -kInf;
     uint32_t floor_key = 0;
     const float lift = fmaxf(-presence, 0.f), shrink = fminf(repetition, 1.f);
-    const auto set_floor = [&](uint32_t key) INLINE {
+    const auto raise = [&](uint32_t key) INLINE {
+        if (key <= floor_key) return;
         floor_key = key;
-        const float floor = key ? key_value(key) : -kInf;
+        if ((tid & 63) == 0) atomicMax(&s_floor, key);
+        const float floor = key_value(key);
         limit = floor;
         if (penalties && !every && floor < kInf) {  // (a NaN stays one: nothing is below it)
             const float x = floor - lift - (fabsf(floor) + lift) * 0x1p-20f, y = x > 0.f ? x * shrink : x / shrink;
@@ -349,33 +346,36 @@ __global__ __launch_bounds__(kT, kPerSimd) void target_kernel(TargetArgs a) {
             most = __builtin_elementwise_maximum(most, m[i]);
         }
         if (__ballot(!(most < limit))) {
-            const uint32_t others = *(volatile uint32_t*)&s_floor;
-            if (others > floor_key) set_floor(others);
+            // Groups without a masked or a changed token have their largest logit for certain: of the wave's
+            // lanes only those with the largest of these are left to be looked at, one as a rule.
+            float sure = -kInf;
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+                const int g = g0 + i * kT;
+                if (g < n_groups && (!masked || allowed_of[g] == 0xFFu) && (!changes || changed_of[g] == 0)) sure = fmaxf(sure, m[i]);
+            }
+            raise(max(wave_max((uint32_t)(argmax_key(sure, 0) >> 32)), *(volatile uint32_t*)&s_floor));
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) {
                 const int g = g0 + i * kT, v = lo + g * 8;
                 const bool reaches = g < n_groups && !(m[i] < limit) && (!masked || allowed_of[g]);
                 if (!__ballot(reaches)) continue;
                 if (reaches) {
-                    Eight<E> x = e[i];
-#pragma unroll
-                    for (int p = 0; p < Eight<E>::kParts; ++p) asm volatile("" : "+v"(x.w[p]));  // taken apart anew, in few registers
                     uint32_t bits = 0;  // of the tokens that reach the limit
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) bits |= (!(x.value(k) < limit) ? 1u : 0u) << k;
+                    for (int k = 0; k < 8; ++k) bits |= (!(e[i].value(k) < limit) ? 1u : 0u) << k;
                     if (masked) bits &= allowed_of[g];
                     const uint32_t changed = changes ? changed_of[g] & bits : 0;
-                    bits &= ~changed;
+                    for (bits &= ~changed; bits; bits &= bits - 1) {
+                        const int at = __ffs(bits) - 1;
+                        float x = e[i].value(0);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (bits >> k & 1) top = max(top, argmax_key(x.value(k), (uint32_t)(v + k)));
-                    if (!every && changed) put_all(v, changed, x);
+                        for (int k = 1; k < 8; ++k) x = at == k ? e[i].value(k) : x;
+                        top = max(top, argmax_key(x, (uint32_t)(v + at)));
+                    }
+                    if (!every && changed) put_all(v, changed, e[i]);
                 }
-                const uint32_t key = wave_max((uint32_t)(top >> 32));
-                if (key > floor_key) {
-                    set_floor(key);
-                    if ((tid & 63) == 0) atomicMax(&s_floor, key);
-                }
+                raise(wave_max((uint32_t)(top >> 32)));
             }
         }
     };
@@ -411,7 +411,14 @@ __global__ __launch_bounds__(kT, kPerSimd) void target_kernel(TargetArgs a) {
             if (v >= hi || !is_changed(v) || !is_allowed(v)) continue;
             e = make_uint2((uint32_t)v, __float_as_uint(E::value(logits[v])));
         }
-        best.take(order_key(value_of((int)e.x, __uint_as_float(e.y))), e.x);
+        const int v = (int)e.x, b = find(v);
+        bool seen = false;
+        int c = 0;
+        if (prompt) {
+            seen = prompt[v >> 5] >> (v & 31) & 1;
+            if (!every || (answered[v >> 5] >> (v & 31) & 1)) c = count[v];  // (few: not worth waiting for their bits)
+        }
+        best.take(order_key(value_of(v, __uint_as_float(e.y), seen, c, b >= 0, b >= 0 ? t.bias_val[b0 + b] : 0.f)), e.x);
     }
     if (top) best.take(order_key((double)key_value((uint32_t)(top >> 32))), (uint32_t)key_index(top));
 
