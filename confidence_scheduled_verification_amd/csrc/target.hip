@@ -31,7 +31,10 @@ constexpr int kLeastChunk = 4096;
 constexpr int kWanted = 2 * kAttendMaxCus;  // workgroups, where there are few rows
 constexpr int kList = 2048;           // changed tokens listed; where there are more, all of them are gone through
 constexpr int kCounted = 4096;        // rows whose parts are counted in the workspace
-constexpr int kHistoryT = 256;
+constexpr int kHistoryT = 256, kWideT = 1024;
+constexpr int kWideFrom = 256;        // tokens of a row that are gathered in LDS
+constexpr int kMostInLds = 1 << 19;   // tokens of a vocabulary whose bits LDS takes, 64 KB (beside the answers' counts, half)
+constexpr int kPromptSlice = 16384, kAnswerSlice = 2048;  // tokens to a workgroup
 constexpr float kInf = __builtin_huge_valf();
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -493,14 +496,43 @@ __global__ __launch_bounds__(kHistoryT) void history_clear_kernel(dspark_history
     }
 }
 
-// A bit that is set already needs no atomic: of a prompt's tokens most have been there before.
-__global__ __launch_bounds__(kHistoryT) void history_add_kernel(dspark_history_t h, size_t words, const int32_t* tokens,
-                                                         int width, const int32_t* rows, int answered, uint32_t* status) {
-    const int i = blockIdx.x, r = rows ? rows[i] : i;
-    if (r < 0 || r >= h.rows) {
-        if (blockIdx.y == 0 && threadIdx.x == 0) raise_status(status, kStatusBadRow);
-        return;
+// Entering tokens.  Few at a time (a step's answers) go to memory one by one; many are first gathered in
+// LDS, a workgroup a slice of a row's tokens, for the frequent ones would have thousands of atomics wait
+// for each other at the same words (128 prompts of 16000 tokens: 107 us one by one, 10 so).  Either way a
+// bit that is set already needs no atomic.
+__device__ __forceinline__ void set_bits(uint32_t* word, uint32_t bits) {
+    if (bits & ~__hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicOr(word, bits);
+}
+
+// A workgroup's bits in LDS, `used` words, four to a lane at a time.
+__device__ __forceinline__ void set_all(uint32_t* to, const uint32_t* s_bits, int used) {
+    for (int w0 = threadIdx.x; w0 < used; w0 += 4 * kWideT) {
+        uint32_t bits[4], have[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int w = w0 + i * kWideT;
+            bits[i] = w < used ? s_bits[w] : 0;
+            have[i] = __hip_atomic_load(to + min(w, used - 1), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (bits[i] & ~have[i]) atomicOr(to + w0 + i * kWideT, bits[i]);
     }
+}
+
+// The history row of tokens' row i; -1 where it is none (the first slice says so).
+__device__ __forceinline__ int history_row(const dspark_history_t& h, const int32_t* rows, int i, bool first, uint32_t* status) {
+    const int r = rows ? rows[i] : i;
+    if (r >= 0 && r < h.rows) return r;
+    if (first && threadIdx.x == 0) raise_status(status, kStatusBadRow);
+    return -1;
+}
+
+__global__ __launch_bounds__(kHistoryT) void history_add_kernel(dspark_history_t h, size_t words, const int32_t* tokens,
+                                                                int width, const int32_t* rows, int answered,
+                                                                uint32_t* status) {
+    const int i = blockIdx.x, r = history_row(h, rows, i, blockIdx.y == 0, status);
+    if (r < 0) return;
     uint32_t* bits = h.seen + ((size_t)r * 2 + (answered ? 1 : 0)) * words;
     int32_t* count = h.count + (size_t)r * h.V;
     bool bad = false;
@@ -511,11 +543,103 @@ __global__ __launch_bounds__(kHistoryT) void history_add_kernel(dspark_history_t
             bad = true;
             continue;
         }
-        const uint32_t bit = 1u << (v & 31);
-        if (!(__hip_atomic_load(bits + (v >> 5), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) & bit)) atomicOr(bits + (v >> 5), bit);
+        set_bits(bits + (v >> 5), 1u << (v & 31));
         if (answered) atomicAdd(count + v, 1);
     }
     if (bad) raise_status(status, kStatusBadRow);
+}
+
+__global__ __launch_bounds__(kWideT) void history_prompt_kernel(dspark_history_t h, size_t words, const int32_t* tokens,
+                                                                int width, const int32_t* rows, uint32_t* status) {
+    extern __shared__ uint32_t s_bits[];  // of V tokens
+    const int i = blockIdx.x, tid = threadIdx.x, r = history_row(h, rows, i, blockIdx.y == 0, status);
+    if (r < 0) return;
+    const int used = (h.V + 31) / 32, end = min(width, ((int)blockIdx.y + 1) * kPromptSlice);
+    for (int w = tid; w < used; w += kWideT) s_bits[w] = 0;
+    __syncthreads();
+    bool bad = false;
+    for (int at = blockIdx.y * kPromptSlice + tid; at < end; at += kWideT) {
+        const int v = tokens[(size_t)i * width + at];
+        if (v < 0) continue;
+        if (v >= h.V) {
+            bad = true;
+            continue;
+        }
+        const uint32_t bit = 1u << (v & 31);
+        if (!(s_bits[v >> 5] & bit)) atomicOr(&s_bits[v >> 5], bit);
+    }
+    if (bad) raise_status(status, kStatusBadRow);
+    __syncthreads();
+    uint32_t* prompt = h.seen + (size_t)r * 2 * words;
+    set_all(prompt, s_bits, used);
+}
+
+// Answers: the bits first; a token's place among the bits that are set, from the bits before it, is then
+// its place in a list of counts, and the lane that comes to a place first adds its count to memory's.
+__global__ __launch_bounds__(kWideT) void history_answer_kernel(dspark_history_t h, size_t words, const int32_t* tokens,
+                                                                int width, const int32_t* rows, uint32_t* status) {
+    constexpr int kMine = kAnswerSlice / kWideT, kWords = kMostInLds / 2 / 32 / kWideT;  // a lane's tokens and words
+    __shared__ uint32_t s_sum[kWideT / 64];
+    __shared__ int s_times[kAnswerSlice];
+    __shared__ uint16_t s_before[kWords * kWideT];  // bits set before each word
+    extern __shared__ uint32_t s_bits[];            // of V tokens, whole pairs of words
+    const int i = blockIdx.x, tid = threadIdx.x, lane = tid & 63, r = history_row(h, rows, i, blockIdx.y == 0, status);
+    if (r < 0) return;
+    const int used = (h.V + 63) / 64 * 2;
+    int mine[kMine];
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+        const int at = blockIdx.y * kAnswerSlice + k * kWideT + tid;
+        mine[k] = at < width ? tokens[(size_t)i * width + at] : -1;
+        if (mine[k] >= h.V) {
+            mine[k] = -1;
+            bad = true;
+        }
+        s_times[k * kWideT + tid] = 0;
+    }
+    if (bad) raise_status(status, kStatusBadRow);
+    for (int w = tid; w < used; w += kWideT) s_bits[w] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kMine; ++k)
+        if (mine[k] >= 0) atomicOr(&s_bits[mine[k] >> 5], 1u << (mine[k] & 31));
+    __syncthreads();
+    uint32_t own = 0, before = 0;
+#pragma unroll
+    for (int k = 0; k < kWords; ++k)
+        if (tid * kWords + k < used) own += __popc(s_bits[tid * kWords + k]);
+    before = own;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t x = __shfl_up(before, d, 64);
+        if (lane >= d) before += x;
+    }
+    if (lane == 63) s_sum[tid >> 6] = before;
+    __syncthreads();
+    before -= own;
+    for (int w = 0; w < tid >> 6; ++w) before += s_sum[w];
+#pragma unroll
+    for (int k = 0; k < kWords; ++k)
+        if (tid * kWords + k < used) {
+            s_before[tid * kWords + k] = (uint16_t)before;
+            before += __popc(s_bits[tid * kWords + k]);
+        }
+    __syncthreads();
+    int place[kMine];
+    bool first[kMine];
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+        first[k] = false;
+        if (mine[k] < 0) continue;
+        place[k] = s_before[mine[k] >> 5] + __popc(s_bits[mine[k] >> 5] & ((1u << (mine[k] & 31)) - 1));
+        first[k] = atomicAdd(&s_times[place[k]], 1) == 0;
+    }
+    set_all(h.seen + ((size_t)r * 2 + 1) * words, s_bits, (h.V + 31) / 32);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kMine; ++k)
+        if (first[k]) atomicAdd(h.count + (size_t)r * h.V + mine[k], s_times[place[k]]);
 }
 
 template <class E>
@@ -571,9 +695,18 @@ hipError_t launch_history_clear(const dspark_history_t& h, const int32_t* rows, 
 
 hipError_t launch_history_add(const dspark_history_t& h, const int32_t* tokens, int n, int width, const int32_t* rows,
                               int answered, uint32_t* status, hipStream_t s) {
-    const int slices = std::min((width + kHistoryT - 1) / kHistoryT, 256);
-    hipLaunchKernelGGL(history_add_kernel, dim3(n, slices), dim3(kHistoryT), 0, s, h, dspark_history_words(h.V), tokens, width,
-                       rows, answered, status);
+    const size_t words = dspark_history_words(h.V);
+    if (width < kWideFrom || h.V > (answered ? kMostInLds / 2 : kMostInLds) || (long long)width > 65535ll * kAnswerSlice) {
+        const int slices = std::min((width + kHistoryT - 1) / kHistoryT, 256);
+        hipLaunchKernelGGL(history_add_kernel, dim3(n, slices), dim3(kHistoryT), 0, s, h, words, tokens, width, rows,
+                           answered, status);
+    } else if (answered) {
+        hipLaunchKernelGGL(history_answer_kernel, dim3(n, (width + kAnswerSlice - 1) / kAnswerSlice), dim3(kWideT),
+                           (h.V + 63) / 64 * 2 * sizeof(uint32_t), s, h, words, tokens, width, rows, status);
+    } else {
+        hipLaunchKernelGGL(history_prompt_kernel, dim3(n, (width + kPromptSlice - 1) / kPromptSlice), dim3(kWideT),
+                           (h.V + 31) / 32 * sizeof(uint32_t), s, h, words, tokens, width, rows, status);
+    }
     return hipGetLastError();
 }
 

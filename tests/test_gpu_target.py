@@ -385,7 +385,8 @@ def test_penalties_that_lift_or_are_no_numbers(penalty):
         s.check()
 
 
-@pytest.mark.parametrize("rows,V,n,width", [(1, 1, 1, 5), (4, 130, 3, 70), (9, 4096, 9, 1), (5, 70001, 40, 3000)])
+@pytest.mark.parametrize("rows,V,n,width", [(1, 1, 1, 5), (4, 130, 3, 70), (9, 4096, 9, 1), (5, 70001, 40, 3000), (2, 600001, 3, 700),
+                                               (3, 1001, 4, 40000), (2, 524288, 2, 256), (2, 262144, 2, 9000), (2, 7, 2, 20000)])
 def test_history(rows, V, n, width):
     _say("history", rows, V, n, width)
     rng = np.random.default_rng(V)
