@@ -7,11 +7,21 @@
 // are the angle to 2^-32 turns at every position, where a product in fp32 is off by up to 2^-8
 // radians at 131072, half a step of bf16.  Sines come from it in fp32.
 //
-// A workgroup takes the 16 tokens of a block of positions and one of three kinds of work: 64 dims
-// of V to a wave, turned over between lanes as in append.hip; some heads of K; or some heads of Q.
-// It computes the sines of its tokens once, into LDS, for all of its heads.  Of K and Q a lane takes
-// both pieces of eight dims that a pair lies in (in halves; interleaved, two neighbouring ones),
-// for K eight tokens side by side, whose pieces make a line of the page, for Q the pieces of a head.
+// A workgroup takes one of three kinds of work: 16 tokens of a block of positions and 64 dims of V to
+// a wave, turned over between lanes as in append.hip; the block's K of a few heads; or the Q of up to
+// eight rows.  Of K and Q a lane takes one token and the two pieces of eight dims that hold both of a
+// pair (in halves; interleaved, two neighbours), and a few heads one after the other with the same
+// sines, the next one's loads under way.  Eight tokens stand side by side in a wave, so that their
+// pieces make a line of the page; of rows that are fewer, more heads.  The workgroup computes its
+// tokens' sines once, into LDS, while the first loads are under way.
+//
+// Bytes bound it, once read, once written.  The workgroups that share rows are neighbours in the grid:
+// 20 thousand fp16 rows of 32 query and 8 key heads of 128 (353 MB) take 78 us (4.5 TB/s; a large copy
+// reaches 4.9), 108 where a kind's workgroups follow each other through all rows.  1152 rows of 64 and 8 heads
+// (47 MB), of requests of up to eight: 22 us, of which 6 are the launch and the loads that wait for each
+// other; a copy of as many bytes takes 10, for which the waves would have to be resident at once.  Eight
+// heads a lane instead of two: 92 and 24 us (fewer waves); a request's blocks walked in a loop in place of a
+// workgroup each: 97 and 28 (twice the registers, half the waves).
 #include <algorithm>
 
 #include "append_dev.h"
@@ -22,176 +32,199 @@ namespace dspark {
 namespace {
 
 constexpr int kT = 256;
-constexpr int kHeads = 16;  // of Q or K, to a workgroup
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4), may_alias));
+constexpr int kPasses = 2;  // heads that a lane takes
 
 struct RBf16 {
+    typedef __bf16 two __attribute__((ext_vector_type(2)));
     static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
     static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-    static __device__ __forceinline__ uint32_t bits(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
+    static __device__ __forceinline__ uint32_t bits(float x, float y) { return __builtin_bit_cast(uint32_t, two{(__bf16)x, (__bf16)y}); }
 };
 struct RF16 {
-    static __device__ __forceinline__ float half(uint32_t h) { return (float)__builtin_bit_cast(_Float16, (uint16_t)h); }
-    static __device__ __forceinline__ float lo(uint32_t w) { return half(w & 0xFFFFu); }
-    static __device__ __forceinline__ float hi(uint32_t w) { return half(w >> 16); }
-    static __device__ __forceinline__ uint32_t bits(float x) { return __builtin_bit_cast(uint16_t, (_Float16)x); }
+    typedef _Float16 two __attribute__((ext_vector_type(2)));
+    static __device__ __forceinline__ float lo(uint32_t w) { return (float)__builtin_bit_cast(two, w)[0]; }
+    static __device__ __forceinline__ float hi(uint32_t w) { return (float)__builtin_bit_cast(two, w)[1]; }
+    static __device__ __forceinline__ uint32_t bits(float x, float y) { return __builtin_bit_cast(uint32_t, two{(_Float16)x, (_Float16)y}); }
 };
 
-// A pair's two values turned by (cosine, sine); the one rounding of each to 16 bits.
-template <class E>
-__device__ __forceinline__ void turn(float x, float y, float2 cs, uint32_t& a, uint32_t& b) {
-    a = E::bits(x * cs.x - y * cs.y);
-    b = E::bits(x * cs.y + y * cs.x);
-}
-
-// Two pieces of eight dims: in halves, dim i of x pairs with dim i of y (cs[0..7]); interleaved, each
-// piece's neighbours pair (x: cs[0..3], y: cs[4..7]).
-template <class E>
-__device__ __forceinline__ void turn_pieces(uint4& x, uint4& y, const float2* cs, bool interleaved) {
+// Two pieces of eight dims turned by cs = (cosine, sine): in halves, dim i of x pairs with dim i of y;
+// interleaved, each piece's neighbours pair (x: cs[0..3], y: cs[4..7]).  Each value is rounded to 16 bits once.
+template <class E, bool kInterleaved>
+__device__ __forceinline__ void turn_pieces(uint4& x, uint4& y, const float2 (&cs)[8]) {
     uint32_t *p = &x.x, *q = &y.x;
+    const auto a = [](float x, float y, float2 cs) { return x * cs.x - y * cs.y; };
+    const auto b = [](float x, float y, float2 cs) { return x * cs.y + y * cs.x; };
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        uint32_t a, b, c, d;
-        if (interleaved) {
-            turn<E>(E::lo(p[i]), E::hi(p[i]), cs[i], a, b);
-            turn<E>(E::lo(q[i]), E::hi(q[i]), cs[4 + i], c, d);
-            p[i] = a | b << 16;
-            q[i] = c | d << 16;
+        __builtin_amdgcn_sched_barrier(0);  // (all at once would take twice the registers)
+        const float x0 = E::lo(p[i]), x1 = E::hi(p[i]), y0 = E::lo(q[i]), y1 = E::hi(q[i]);
+        if (kInterleaved) {
+            p[i] = E::bits(a(x0, x1, cs[i]), b(x0, x1, cs[i]));
+            q[i] = E::bits(a(y0, y1, cs[4 + i]), b(y0, y1, cs[4 + i]));
         } else {
-            turn<E>(E::lo(p[i]), E::lo(q[i]), cs[2 * i], a, c);
-            turn<E>(E::hi(p[i]), E::hi(q[i]), cs[2 * i + 1], b, d);
-            p[i] = a | b << 16;
-            q[i] = c | d << 16;
+            p[i] = E::bits(a(x0, y0, cs[2 * i]), a(x1, y1, cs[2 * i + 1]));
+            q[i] = E::bits(b(x0, y0, cs[2 * i]), b(x1, y1, cs[2 * i + 1]));
         }
     }
 }
 
-// Where item e of a head's D / 16 lies: its two pieces of eight dims, and whether they turn.
-struct Pieces {
-    int x, y;
-    bool turns;
-};
-__device__ __forceinline__ Pieces pieces(const RotaryArgs& a, int e) {
-    const int first = a.first >> 3, n = a.dim >> 4;  // items that turn
-    if (e < n) return a.interleaved ? Pieces{first + 2 * e, first + 2 * e + 1, true} : Pieces{first + e, first + n + e, true};
-    const int u = 2 * (e - n), v = u + 1;  // pieces that pass, counted without those that turn
-    return Pieces{u < first ? u : u + 2 * n, v < first ? v : v + 2 * n, false};
+__device__ __forceinline__ uint4 once(const uint16_t* p) {  // read once
+    return __builtin_bit_cast(uint4, __builtin_nontemporal_load((const u32x4*)p));
 }
 
-template <class E>
-__global__ __launch_bounds__(kT) void append_rotary_kernel(RotaryArgs g, int v_parts, int k_parts) {
-    extern __shared__ __attribute__((aligned(16))) float2 s_cs[];  // [16][dim / 2]
+// (cosine, sine) of 2 pi times the 32-bit fraction of a turn, to 2^-23: the nearest quarter taken off, the
+// series of both on what is left, |x| <= pi / 4, where the first terms left out are 2e-9 and 3e-8.
+__device__ __forceinline__ float2 cos_sin(uint32_t angle, float m) {
+    const uint32_t quarter = angle + 0x20000000u;
+    const float x = (float)(int32_t)(angle - (quarter & 0xC0000000u)) * 0x1.921fb6p-30f, y = x * x;
+    const float s = fmaf(x * y, fmaf(y, fmaf(y, fmaf(y, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), x);
+    const float c = fmaf(y, fmaf(y, fmaf(y, fmaf(y, 1.f / 40320, -1.f / 720), 1.f / 24), -.5f), 1.f);
+    const bool odd = quarter & 0x40000000u;
+    return make_float2(m * __uint_as_float(__float_as_uint(odd ? s : c) ^ ((quarter + 0x40000000u) & 0x80000000u)),
+                       m * __uint_as_float(__float_as_uint(odd ? c : s) ^ (quarter & 0x80000000u)));
+}
+
+struct Split {  // of the work on a block of 16 tokens among workgroups
+    int shift_t;           // Q: 1 << shift_t tokens side by side in a wave
+    int q_halves;          // Q: 1 where the other half of the block has workgroups of its own
+    int v_parts, k_parts;  // Q has the rest of the grid
+    long long first_block;
+};
+
+template <class E, bool kInterleaved>
+__global__ __launch_bounds__(kT, 8) void append_rotary_kernel(RotaryArgs g, Split sp) {
+    extern __shared__ __attribute__((aligned(16))) float2 s_cs[];  // [tokens][dim / 2]
     const AppendArgs& a = g.a;
-    const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int o = a.offsets[r], o1 = a.offsets[r + 1], ln = a.len[r];
-    const long long n = (long long)o1 - o + a.lead, start = (long long)o + (long long)a.lead * r;
+    const int r = blockIdx.z, tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int o = a.offsets[r], o1 = a.offsets[r + 1], ln = a.len[r], shift = a.page_shift;
+    const long long rows = (long long)o1 - o + a.lead, start = (long long)o + (long long)a.lead * r;
     if (ln < 0) return;
-    if (o < 0 || n < 0 || n > a.max_new || start + n > a.rows || (ln + n + a.page - 1) / a.page > a.width) {
-        if (blockIdx.y == 0 && blockIdx.z == 0 && tid == 0) raise_status(a.status, kStatusBadRow);
+    if (o < 0 || rows < 0 || rows > a.max_new || start + rows > a.rows || (ln + rows + (1 << shift) - 1) >> shift > a.width) {
+        if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) raise_status(a.status, kStatusBadRow);
         return;
     }
-    if (n == 0) return;
-    const int shift = a.page_shift, part = blockIdx.z, D = a.D, items = D / 16, pairs = g.dim / 2;
-    const bool is_v = part < v_parts, is_k = !is_v && part < v_parts + k_parts;
-    const long long end = ln + n;
-    for (long long pos = (ln & ~(kBlockTokens - 1)) + (long long)blockIdx.y * kBlockTokens; pos < end;
-         pos += (long long)gridDim.y * kBlockTokens) {
-        size_t block0 = 0;  // the block in the page's first head
-        if (is_v || is_k) {
-            const int page = a.table[(size_t)r * a.width + (pos >> shift)];
-            if (page < 0 || page >= a.n_pages || a.ref[page] > 1) {  // not there, or another row's too
-                if (part == 0 && tid == 0) raise_status(a.status, kStatusBadPage);
-                continue;
-            }
-            block0 = ((size_t)page * a.Hkv << (shift - 4)) + ((pos & ((1 << shift) - 1)) >> 4);
+    const int n = (int)rows, row0 = (int)start, D = a.D;
+    const int part = blockIdx.x;
+    const bool is_q = part >= sp.v_parts + sp.k_parts, is_v = part < sp.v_parts;
+    const int q_part = part - sp.v_parts - sp.k_parts, unit = (is_q ? q_part >> sp.q_halves : is_v ? part : part - sp.v_parts) * 4 + wave;
+    // Rows j0 .. of the request: of a block of positions (V, K), or from the first row on (Q).
+    const long long block = sp.first_block + blockIdx.y, j64 = block * kBlockTokens - (is_q ? -((q_part & sp.q_halves) * 8) : ln & (kBlockTokens - 1));
+    if (n == 0 || j64 >= n) return;  // (with n = 0 the block that the kept tokens end in is not this step's)
+    const int j0 = (int)j64;
+    size_t block0 = 0;  // of the tokens, in the page's first head
+    if (!is_q) {
+        const long long pos = (long long)ln + j0;
+        const int page = a.table[(size_t)r * a.width + (pos >> shift)];
+        if (page < 0 || page >= a.n_pages || a.ref[page] > 1) {  // not there, or another row's too
+            if (part == 0 && tid == 0) raise_status(a.status, kStatusBadPage);
+            return;
         }
-        if (is_v) {
-            const int row8 = (lane >> 5) * 4 + (lane >> 4 & 1) * 2 + (lane & 1);  // token of the eight; afterwards dim of the eight
-            const int c8 = lane >> 1 & 7, item = part * 4 + wave;                // eight dims of the 64
-            if (item >= a.Hkv * (D / 64)) continue;
-            const int h = item / (D / 64), d0 = item % (D / 64) * 64;
-            const size_t block = (block0 + ((size_t)h << (shift - 4))) * (size_t)(kBlockTokens * D);
-            uint4 v[2];
+        block0 = ((size_t)page * a.Hkv << (shift - 4)) + ((int)(pos & ((1 << shift) - 1)) >> 4);
+    }
+    if (is_v) {
+        const int row8 = (lane >> 5) * 4 + (lane >> 4 & 1) * 2 + (lane & 1);  // token of the eight; afterwards dim of the eight
+        const int c8 = lane >> 1 & 7, shift_h = __builtin_ctz(D >> 6);       // eight dims of the 64
+        const int h = unit >> shift_h, d0 = (unit & ((D >> 6) - 1)) * 64;
+        if (h >= a.Hkv) return;
+        uint16_t* block = a.v + (block0 + ((size_t)h << (shift - 4))) * (size_t)(kBlockTokens * D) + (d0 + c8 * 8 + row8) * kBlockTokens;
+        uint4 v[2];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const long long p = pos + half * 8 + row8;
-                v[half] = make_uint4(0, 0, 0, 0);
-                if (p >= ln && p < end)
-                    v[half] = *(const uint4*)(a.v_new + (size_t)(start + p - ln) * a.v_stride + (size_t)h * D + d0 + c8 * 8);
-            }
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const long long p0 = pos + half * 8;
-                if (p0 + 8 <= ln || p0 >= end) continue;
-                const uint4 x = turned(v[half]);
-                uint16_t* to = a.v + block + (size_t)(d0 + c8 * 8 + row8) * kBlockTokens + half * 8;
-                if (p0 >= ln && p0 + 8 <= end) {
-                    *(uint4*)to = x;
-                } else {
-                    const uint32_t* w = &x.x;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (p0 + j >= ln && p0 + j < end) to[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
-                }
-            }
-            continue;
+        for (int half = 0; half < 2; ++half) {
+            const int j = j0 + half * 8 + row8;
+            v[half] = make_uint4(0, 0, 0, 0);
+            if (j >= 0 && j < n) v[half] = once(a.v_new + (size_t)(row0 + j) * a.v_stride + h * D + d0 + c8 * 8);
         }
-        // Tokens [t0, t1) of the block are the step's; their rows begin at row0 + t0.
-        const int t0 = (int)max(ln - pos, 0ll), t1 = (int)min(end - pos, (long long)kBlockTokens);
-        const long long row0 = start + pos - ln;
-        __syncthreads();  // the last block's sines have been read
-        for (int i = tid; i < (t1 - t0) * pairs; i += kT) {
-            const int t = t0 + i / pairs, f = i % pairs;
-            const long long at = g.depth ? (long long)ln + g.depth[row0 + t] : pos + t;
-            const int32_t angle = (int32_t)(((uint64_t)at * g.turns[f]) >> 32);  // of 2^32 a turn
-            float s, c;
-            sincospif((float)angle * 0x1p-31f, &s, &c);
-            s_cs[t * pairs + f] = make_float2(c * g.attention, s * g.attention);
-        }
-        __syncthreads();
-        const int h0 = (is_k ? part - v_parts : part - v_parts - k_parts) * kHeads;
-        const int heads = min(kHeads, (is_k ? a.Hkv : g.H) - h0);
-        const int tokens = t1 - t0;
-        for (int i = tid; i < tokens * heads * items; i += kT) {
-            int t, e, h;
-            if (is_k) {
-                t = t0 + i % tokens;
-                e = i / tokens % items;
-                h = h0 + i / tokens / items;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int j = j0 + half * 8;
+            if (j + 8 <= 0 || j >= n) continue;
+            const uint4 x = turned(v[half]);
+            uint16_t* to = block + half * 8;
+            if (j >= 0 && j + 8 <= n) {
+                *(uint4*)to = x;
             } else {
-                e = i % items;
-                h = h0 + i / items % heads;
-                t = t0 + i / items / heads;
-            }
-            const Pieces p = pieces(g, e);
-            const size_t row = (size_t)(row0 + t);
-            const uint16_t* from = (is_k ? a.k_new + row * a.k_stride : g.q + row * g.q_stride) + (size_t)h * D;
-            uint4 x = *(const uint4*)(from + p.x * 8), y = *(const uint4*)(from + p.y * 8);
-            if (p.turns) turn_pieces<E>(x, y, s_cs + t * pairs + e * 8, g.interleaved);
-            if (is_k) {
-                uint16_t* to = a.k + (block0 + ((size_t)h << (shift - 4))) * (size_t)(kBlockTokens * D) + t * 8;
-                *(uint4*)(to + p.x * (kBlockTokens * 8)) = x;
-                *(uint4*)(to + p.y * (kBlockTokens * 8)) = y;
-            } else {
-                uint16_t* to = g.q_out + row * g.q_out_stride + (size_t)h * D;
-                *(uint4*)(to + p.x * 8) = x;
-                *(uint4*)(to + p.y * 8) = y;
+                const uint32_t* w = &x.x;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (j + i >= 0 && j + i < n) to[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
             }
         }
+        return;
+    }
+    // A lane's token, its item of a head (two pieces of eight dims) and its heads.
+    const int items = D >> 4, shift_items = __builtin_ctz(items), shift_side = 6 - (is_q ? sp.shift_t : 3);
+    const int halves = is_q ? 0 : 1, strips = max(shift_items - shift_side, 0), step = 1 << max(shift_side - shift_items, 0);
+    const int slot = (lane & ((1 << shift_side) - 1)) + ((unit >> halves & ((1 << strips) - 1)) << shift_side);
+    const int e = slot & (items - 1), h0 = (unit >> (halves + strips)) * kPasses * step + (slot >> shift_items);
+    const int t = (is_q ? 0 : (unit & 1) * 8) + (lane >> shift_side), j = j0 + t;
+    int left = min(h0 + kPasses * step, is_q ? g.H : a.Hkv) - h0;  // while > 0
+    if (j < 0 || j >= n) left = 0;
+    // Its two pieces: a pair's, in halves, or two neighbours; behind those that turn, the others.
+    const int first = g.first >> 3, turning = g.dim >> 4, pass = 2 * (e - turning);
+    const bool turns = e < turning;
+    const int px = turns ? first + (kInterleaved ? 2 * e : e) : pass < first ? pass : pass + 2 * turning;
+    const int py = turns ? px + (kInterleaved ? 1 : turning) : pass + 1 < first ? pass + 1 : pass + 1 + 2 * turning;
+    const size_t row = (size_t)(row0 + j);
+    const uint16_t* from = (is_q ? g.q + row * g.q_stride : a.k_new + row * a.k_stride) + h0 * D + px * 8;
+    const int from_y = (py - px) * 8;
+    uint4 x, y;
+    if (left > 0) {
+        x = once(from);
+        y = once(from + from_y);
+    }
+    const int pairs = g.dim >> 1;
+    for (int i = wave; i < (is_q ? 1 << sp.shift_t : kBlockTokens); i += kT / 64) {
+        if (j0 + i < 0 || j0 + i >= n) continue;
+        const long long at = ln + (long long)(g.depth ? g.depth[row0 + j0 + i] : j0 + i);
+        for (int f = lane; f < pairs; f += 64)
+            s_cs[i * pairs + f] = cos_sin((uint32_t)(((uint64_t)at * g.turns[f]) >> 32), g.attention);
+    }
+    __syncthreads();
+    float2 cs[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cs[i] = s_cs[t * pairs + (turns ? e : 0) * 8 + i];
+    const int to_piece = is_q ? 8 : kBlockTokens * 8, to_y = (py - px) * to_piece;
+    const size_t to_step = is_q ? step * D : (size_t)(step * D) << shift;
+    uint16_t* to = (is_q ? g.q_out + row * g.q_out_stride + h0 * D
+                         : a.k + block0 * (size_t)(kBlockTokens * D) + ((size_t)(h0 * D) << shift) + t * 8) + px * to_piece;
+#pragma unroll 1
+    while (left > 0) {
+        uint4 u = x, v = y;
+        left -= step;
+        from += step * D;
+        if (left > 0) {
+            x = once(from);
+            y = once(from + from_y);
+        }
+        if (turns) turn_pieces<E, kInterleaved>(u, v, cs);
+        *(uint4*)to = u;
+        *(uint4*)(to + to_y) = v;
+        to += to_step;
     }
 }
 
 }  // namespace
 
 hipError_t launch_append_rotary(const RotaryArgs& g, hipStream_t s) {
-    // blocks that max_new tokens can touch
-    const int blocks = (int)std::min((g.a.max_new + 2ll * (kBlockTokens - 1)) / kBlockTokens, 4096ll);
-    const int v_parts = (g.a.Hkv * (g.a.D / 64) + 3) / 4, k_parts = (g.a.Hkv + kHeads - 1) / kHeads;
-    const dim3 grid(g.a.R, blocks, v_parts + k_parts + (g.H + kHeads - 1) / kHeads);
+    const int items = g.a.D / 16;
+    Split sp;
+    sp.shift_t = g.a.max_new > 4 ? 3 : g.a.max_new > 2 ? 2 : g.a.max_new > 1 ? 1 : 0;
+    sp.q_halves = g.a.max_new > 8;
+    const auto parts = [&](int side, int heads, int halves) {  // `side` items side by side in a wave
+        const int strips = std::max(items / side, 1), at_once = std::max(side / items, 1) * kPasses;
+        return ((heads + at_once - 1) / at_once * strips * halves + 3) / 4;
+    };
+    sp.v_parts = (g.a.Hkv * (g.a.D / 64) + 3) / 4;
+    sp.k_parts = parts(8, g.a.Hkv, 2);
+    const int all = sp.v_parts + sp.k_parts + (parts(64 >> sp.shift_t, g.H, 1) << sp.q_halves);
+    const long long blocks = (std::min(g.a.max_new, g.a.rows) + 2ll * (kBlockTokens - 1)) / kBlockTokens;  // that the tokens can touch
     const size_t lds = kBlockTokens * (g.dim / 2) * sizeof(float2);
-    if (g.dtype == DSPARK_F16)
-        hipLaunchKernelGGL(append_rotary_kernel<RF16>, grid, dim3(kT), lds, s, g, v_parts, k_parts);
-    else
-        hipLaunchKernelGGL(append_rotary_kernel<RBf16>, grid, dim3(kT), lds, s, g, v_parts, k_parts);
+    const auto kernel = g.dtype == DSPARK_F16 ? g.interleaved ? append_rotary_kernel<RF16, true> : append_rotary_kernel<RF16, false>
+                        : g.interleaved       ? append_rotary_kernel<RBf16, true>
+                                              : append_rotary_kernel<RBf16, false>;
+    for (sp.first_block = 0; sp.first_block < blocks; sp.first_block += 65535)
+        hipLaunchKernelGGL(kernel, dim3(all, (unsigned)std::min(blocks - sp.first_block, 65535ll), g.a.R), dim3(kT), lds, s, g, sp);
     return hipGetLastError();
 }
 
