@@ -367,16 +367,17 @@ __device__ __forceinline__ void join(float& m, float& l, float (&acc)[8], float 
     for (int i = 0; i < 8; ++i) acc[i] = acc[i] * s0 + v[i] * s1;
 }
 
-// Adds the parts that workers wa..wb have left of a segment: column `col` of its tile.  Four
+// Adds the parts that workers wa..wb have left of a segment: column `col` of its tile.  kAtOnce
 // parts are requested at a time, so that a long segment's parts do not wait for each other.
+template <int kAtOnce>
 __device__ __forceinline__ void join_parts(const AttendArgs& a, int set, int wa, int wb, int col, int c8, float& m,
                                            float& l, float (&acc)[8]) {
     const size_t tile = a.tile[set];
-    for (int w0 = wa; w0 <= wb; w0 += 4) {
-        float pm[4], pl[4];
-        float4 x[4], y[4];
+    for (int w0 = wa; w0 <= wb; w0 += kAtOnce) {
+        float pm[kAtOnce], pl[kAtOnce];
+        float4 x[kAtOnce], y[kAtOnce];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kAtOnce; ++i) {
             const int w = min(w0 + i, wb);
             const float* s = slot_of(a, set, w, w == wa);
             pm[i] = s[tile * a.D + col];
@@ -385,7 +386,7 @@ __device__ __forceinline__ void join_parts(const AttendArgs& a, int set, int wa,
             y[i] = *(const float4*)(s + (size_t)col * a.D + c8 * 8 + 4);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kAtOnce; ++i)
             if (w0 + i <= wb) join(m, l, acc, pm[i], pl[i], x[i], y[i]);
     }
 }
@@ -411,7 +412,7 @@ __device__ __forceinline__ void join_item(const AttendArgs& a, int set, const Sp
         const Dense d = dense_of(a, set, f, h);
         join(m, l, acc, *d.m, *d.l, *(const float4*)(d.o + c8 * 8), *(const float4*)(d.o + c8 * 8 + 4));
     } else {
-        join_parts(a, set, wa, wb, c & (a.tile[set] - 1), c8, m, l, acc);
+        join_parts<4>(a, set, wa, wb, c & (a.tile[set] - 1), c8, m, l, acc);
     }
 }
 
@@ -1240,7 +1241,12 @@ __global__ __launch_bounds__(kT) void attend_join_kernel(AttendArgs a) {
     const int chunks = a.D / 8, c = blockIdx.y * (kT / chunks) + threadIdx.x / chunks, c8 = threadIdx.x % chunks;
     if (c >= e.nf) return;
     float m = -kInf, l = 0.f, acc[8] = {};
-    join_parts(a, 0, e.first, e.last, c, c8, m, l, acc);
+    // Two trees of 131072 tokens, 48 parts a segment: 18 us with eight at a time, 22 with four; for four
+    // parts four are 0.5 us the faster.
+    if (e.last - e.first >= 4)
+        join_parts<8>(a, 0, e.first, e.last, c, c8, m, l, acc);
+    else
+        join_parts<4>(a, 0, e.first, e.last, c, c8, m, l, acc);
     store_row<E>(a, e.f0 + c, e.h, c8, m, l, acc);
 }
 
