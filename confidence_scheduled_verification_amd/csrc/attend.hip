@@ -1241,8 +1241,8 @@ __global__ __launch_bounds__(kT) void attend_join_kernel(AttendArgs a) {
     const int chunks = a.D / 8, c = blockIdx.y * (kT / chunks) + threadIdx.x / chunks, c8 = threadIdx.x % chunks;
     if (c >= e.nf) return;
     float m = -kInf, l = 0.f, acc[8] = {};
-    // Two trees of 131072 tokens, 48 parts a segment: 18 us with eight at a time, 22 with four; for four
-    // parts four are 0.5 us the faster.
+    // Two trees of 131072 tokens, 48 parts a segment: 18 us with eight at a time, 22 with four.  Of four
+    // parts and fewer the other half would be loaded for nothing.
     if (e.last - e.first >= 4)
         join_parts<8>(a, 0, e.first, e.last, c, c8, m, l, acc);
     else

@@ -4,6 +4,8 @@
 // A request has at most 64 nodes, so one wave holds a tree, a node (or a chain's token) to a
 // lane, and sets of nodes are 64-bit words: comparing is a ballot, counting a population
 // count, and a number among the set's members the count of those before.
+#include <algorithm>
+
 #include "common.h"
 #include "tree.h"
 
@@ -204,18 +206,34 @@ __global__ __launch_bounds__(kT) void accept_tree_kernel(const int32_t* ver_toke
     if (out_tokens && lane <= K) out_tokens[(size_t)r * (K + 1) + lane] = said;
 }
 
-// A workgroup takes a request and a layer.  Nodes move towards the front and in rising order,
-// so what one takes the place of has been read, or is none of the path's: a thread keeps to its
-// dims, eight of K (16 bytes of a token) or one of V (two bytes), and needs to wait for nobody.
+// A row of V in a block of 16 tokens: the tokens' values of one dim, two to a word.
+typedef uint32_t u32x8 __attribute__((ext_vector_type(8), aligned(16)));
+__device__ __forceinline__ uint32_t value_at(const u32x8& row, int i) { return row[i >> 1] >> (16 * (i & 1)) & 0xFFFFu; }
+__device__ __forceinline__ void put_at(u32x8& row, int i, uint32_t x) {
+    const uint32_t w = row[i >> 1];
+    row[i >> 1] = i & 1 ? (w & 0xFFFFu) | x << 16 : (w & 0xFFFF0000u) | x;
+}
+
+// A workgroup takes a request's K or its V in a layer.  Nodes move towards the front and in rising order, so
+// what one takes the place of has been read, or is none of the path's: a thread keeps to its dims and
+// waits for nobody.  Of K it moves 16 bytes, eight dims of a token; of V it reads the whole row of a dim in
+// the block that tokens come to, 32 bytes, sets their values in it (from the same row, or from other
+// blocks, where they are read alone) and writes it back: the block is this request's own.
+//
+// Waiting bounds it: the page ids come after the path and the lengths, the data after them.  256 requests
+// of up to 28 nodes, 16 layers of 8 key heads of 128: 23 us, of which 67 MB read and written would take 14;
+// with two bytes of V at a time 34, with K and V one after the other 41, with some layers one after the
+// other 76.  The workgroups of a request stand together in the grid: with the layers together it takes 31.
 __global__ __launch_bounds__(kT) void keep_path_kernel(dspark_cache_t c, const int32_t* path, int K,
                                                        const int32_t* accept_len, const int32_t* granted, int lead,
                                                        uint32_t* status) {
+    constexpr int kAtOnce = 4;  // tokens of K, and rows of V, under way
     __shared__ int s_from[kTreeNodes], s_to[kTreeNodes], s_n;
     __shared__ size_t s_from_at[kTreeNodes], s_to_at[kTreeNodes];
-    const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+    const int r = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
     const int ln = c.len[r], n = accept_len[r];
     if (ln < 0 || (granted && granted[r] == 0)) return;
-    const int shift = __builtin_ctz(c.page_size);
+    const int shift = __builtin_ctz(c.page_size), D = c.head_dim;
     if (tid < 64) {
         bool bad = n < 0 || n > K, gone = false;
         int from = 0, to = 0;
@@ -233,14 +251,14 @@ __global__ __launch_bounds__(kT) void keep_path_kernel(dspark_cache_t c, const i
             const long long p = (long long)ln + from, q = (long long)ln + to;
             const int fp = c.table[(size_t)r * c.width + (p >> shift)], tp = c.table[(size_t)r * c.width + (q >> shift)];
             gone = (unsigned)fp >= (unsigned)c.n_pages || (unsigned)tp >= (unsigned)c.n_pages || c.ref[tp] > 1;
-            // the token's block in its page's first head, in tokens
-            from_at = ((size_t)(unsigned)fp * c.n_kv_heads << shift) + (p & (c.page_size - 16));
-            to_at = ((size_t)(unsigned)tp * c.n_kv_heads << shift) + (q & (c.page_size - 16));
+            // the token's block in its page's first head, in values of a head
+            from_at = (((size_t)(unsigned)fp * c.n_kv_heads << shift) + (p & (c.page_size - 16))) * D;
+            to_at = (((size_t)(unsigned)tp * c.n_kv_heads << shift) + (q & (c.page_size - 16))) * D;
             from = (int)(p & 15);
             to = (int)(q & 15);
         }
         gone = __ballot(gone) != 0;
-        if (lane == 0 && blockIdx.y == 0 && (bad || gone)) raise_status(status, bad ? kStatusBadRow : kStatusBadPage);
+        if (lane == 0 && blockIdx.x == 0 && (bad || gone)) raise_status(status, bad ? kStatusBadRow : kStatusBadPage);
         const uint64_t all = bad || gone ? 0 : __ballot(moves);
         if (all >> lane & 1) {
             const int at = __popcll(all & below(lane));
@@ -252,20 +270,52 @@ __global__ __launch_bounds__(kT) void keep_path_kernel(dspark_cache_t c, const i
         if (lane == 0) s_n = __popcll(all);
     }
     __syncthreads();
-    const int moved = s_n, D = c.head_dim;
+    const int moved = __builtin_amdgcn_readfirstlane(s_n);
     if (moved == 0) return;
-    const size_t layer = (size_t)blockIdx.y * c.n_pages * c.n_kv_heads * c.page_size * D;
-    uint16_t *k = (uint16_t*)c.k + layer, *v = (uint16_t*)c.v + layer;
-    for (int e = tid; e < c.n_kv_heads * (D / 8); e += kT) {
-        const size_t head = (size_t)(e / (D / 8)) << shift, in = (size_t)(e % (D / 8)) * 128;
-        for (int i = 0; i < moved; ++i)
-            *(uint4*)(k + (s_to_at[i] + head) * D + in + s_to[i] * 8) =
-                *(const uint4*)(k + (s_from_at[i] + head) * D + in + s_from[i] * 8);
+    const size_t layer = (size_t)(blockIdx.x >> 1) * c.n_pages * c.n_kv_heads * c.page_size * D;
+    if (blockIdx.x & 1) {
+        for (int e = tid; e < c.n_kv_heads * (D / 8); e += kT) {
+            uint16_t* p = (uint16_t*)c.k + layer + ((size_t)(e / (D / 8)) << shift) * D + (size_t)(e % (D / 8)) * 128;
+            for (int i0 = 0; i0 < moved; i0 += kAtOnce) {
+                uint4 x[kAtOnce];
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) {
+                    const int at = min(i0 + i, moved - 1);
+                    x[i] = *(const uint4*)(p + s_from_at[at] + s_from[at] * 8);
+                }
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i)
+                    if (i0 + i < moved) *(uint4*)(p + s_to_at[i0 + i] + s_to[i0 + i] * 8) = x[i];
+            }
+        }
+        return;
     }
-    for (int e = tid; e < c.n_kv_heads * D; e += kT) {
-        const size_t head = (size_t)(e / D) << shift, in = (size_t)(e % D) * 16;
-        for (int i = 0; i < moved; ++i)
-            v[(s_to_at[i] + head) * D + in + s_to[i]] = v[(s_from_at[i] + head) * D + in + s_from[i]];
+    const int rows = c.n_kv_heads * D;
+    for (int e0 = tid; e0 < rows; e0 += kT * kAtOnce) {
+        uint16_t* p[kAtOnce];
+#pragma unroll
+        for (int d = 0; d < kAtOnce; ++d) {
+            const int e = min(e0 + d * kT, rows - 1);
+            p[d] = (uint16_t*)c.v + layer + ((size_t)(e / D) << shift) * D + (size_t)(e % D) * 16;
+        }
+        for (int i = 0; i < moved;) {
+            const size_t block = s_to_at[i];
+            u32x8 x[kAtOnce];
+#pragma unroll
+            for (int d = 0; d < kAtOnce; ++d) x[d] = *(const u32x8*)(p[d] + block);
+            for (; i < moved && s_to_at[i] == block; ++i) {
+                const int from = __builtin_amdgcn_readfirstlane(s_from[i]), to = __builtin_amdgcn_readfirstlane(s_to[i]);
+                const size_t source = s_from_at[i];
+                uint32_t y[kAtOnce];
+#pragma unroll
+                for (int d = 0; d < kAtOnce; ++d) y[d] = source == block ? value_at(x[d], from) : p[d][source + from];
+#pragma unroll
+                for (int d = 0; d < kAtOnce; ++d) put_at(x[d], to, y[d]);
+            }
+#pragma unroll
+            for (int d = 0; d < kAtOnce; ++d)
+                if (e0 + d * kT < rows) *(u32x8*)(p[d] + block) = x[d];
+        }
     }
 }
 
@@ -308,8 +358,7 @@ hipError_t launch_accept_tree(const int32_t* ver_tokens, int n_nodes, const int3
 
 hipError_t launch_keep_path(const dspark_cache_t& c, const int32_t* path, int K, const int32_t* accept_len,
                             const int32_t* granted, int lead, int R, uint32_t* status, hipStream_t s) {
-    hipLaunchKernelGGL(keep_path_kernel, dim3(R, c.layers), dim3(kT), 0, s, c, path, K, accept_len, granted, lead,
-                       status);
+    hipLaunchKernelGGL(keep_path_kernel, dim3(2 * c.layers, R), dim3(kT), 0, s, c, path, K, accept_len, granted, lead, status);
     return hipGetLastError();
 }
 
