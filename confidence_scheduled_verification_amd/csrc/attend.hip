@@ -26,7 +26,8 @@
 // (attend_wide_kernel).  Each kernel says what it reaches.
 //
 // Masks: only blocks that reach past a column's last key are masked; for trees, those that reach
-// past the request's tokens, by the bits of each row's word.  What lies in masked
+// past the request's tokens, by the bits of each row's word (a form of the kernels of its own, so that
+// other calls hold no words; shared keys are seen by all rows and need none).  What lies in masked
 // places has no say whatever it is: scores are replaced, V past the end is cleared, and a
 // value of V that is not a number in such a block is taken out of the product and handed
 // to the columns that see it by counting (see add_special).

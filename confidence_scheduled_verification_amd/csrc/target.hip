@@ -13,6 +13,13 @@
 // Biases may lift a token as far as they like: those tokens are on the list from the start.  So is
 // every changed one where the processed logits are wanted, or a frequency below nothing lifts tokens
 // by how often they have been said.
+//
+// Bytes bound it where rows are many: 1152 bf16 rows of 129280 (298 MB, and 2000 said tokens, 100
+// biases and a mask each) take 71 us, 4.3 TB/s; looking at every changed token took 126.  Groups of eight
+// without an allowed token are not read.  Four such rows, 32 workgroups each, take 11 us, of which the launch and
+// loads that wait for each other (rows, bits, logits, counts) are all but one; a second launch
+// to join the parts made it 16.  About 340 rows of 32771 in fp32, processed and written (89 MB): 41 us, 2.2
+// TB/s: rows of an odd length stand on no line, and a workgroup is through its part in four loads of a lane.
 #include <algorithm>
 
 #include "common.h"
@@ -476,7 +483,7 @@ __global__ __launch_bounds__(64) void target_join_kernel(TargetArgs a) {
     }
 }
 
-// A history row emptied: the counts only where there are any.
+// A history row emptied: the counts only where there are any.  128 rows of 129280: 6.5 us.
 __global__ __launch_bounds__(kHistoryT) void history_clear_kernel(dspark_history_t h, size_t words, const int32_t* rows,
                                                            uint32_t* status) {
     const int i = blockIdx.x, r = rows ? rows[i] : i;
@@ -498,8 +505,8 @@ __global__ __launch_bounds__(kHistoryT) void history_clear_kernel(dspark_history
 
 // Entering tokens.  Few at a time (a step's answers) go to memory one by one; many are first gathered in
 // LDS, a workgroup a slice of a row's tokens, for the frequent ones would have thousands of atomics wait
-// for each other at the same words (128 prompts of 16000 tokens: 107 us one by one, 10 so).  Either way a
-// bit that is set already needs no atomic.
+// for each other at the same words (128 prompts of 16000 tokens: 107 us one by one, 10 so; 128
+// answers of 2000: 15 so).  Either way a bit that is set already needs no atomic.
 __device__ __forceinline__ void set_bits(uint32_t* word, uint32_t bits) {
     if (bits & ~__hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicOr(word, bits);
 }
