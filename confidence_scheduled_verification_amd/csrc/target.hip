@@ -441,7 +441,9 @@ __global__ __launch_bounds__(kT, kPerSimd) void target_kernel(TargetArgs a) {
     for (int w = 1; w < kWaves; ++w) best.take(s_best[w].key, s_best[w].v);
     if (a.parts > 1) {
         // The part that comes last joins all of the row's.  What the others have left is there when their
-        // counts are: written through to where all of the device sees it, and waited for.
+        // counts are: written through to where all of the device sees it, and waited for.  Where two requests
+        // have the row (offsets that fall), every a.parts-th takes a.parts off, so that nothing is left
+        // for the next call, and what is not there yet is no token of this one, or is passed over.
         TargetBest* parts = a.best + row * a.parts;
         int came = 0;
         if (tid == 0) {
@@ -450,13 +452,15 @@ __global__ __launch_bounds__(kT, kPerSimd) void target_kernel(TargetArgs a) {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             if (a.came) came = (int)__hip_atomic_fetch_add(&a.came[row], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
-        if (!a.came || __builtin_amdgcn_readfirstlane(came) != a.parts - 1) return;
+        if (!a.came || (uint32_t)(__builtin_amdgcn_readfirstlane(came) + 1) % (uint32_t)a.parts) return;
         asm volatile("" ::: "memory");
-        for (int p = tid; p < a.parts; p += 64)
-            best.take(__hip_atomic_load(&parts[p].key, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT),
-                      __hip_atomic_load(&parts[p].v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+        for (int p = tid; p < a.parts; p += 64) {
+            const uint64_t key = __hip_atomic_load(&parts[p].key, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            const uint32_t v = __hip_atomic_load(&parts[p].v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (v < (uint32_t)t.V) best.take(key, v);
+        }
         wave_best(best);
-        if (tid == 0) __hip_atomic_store(&a.came[row], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next call
+        if (tid == 0) __hip_atomic_fetch_sub(&a.came[row], (uint32_t)a.parts, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next call
     }
     if (tid == 0) {
         t.target[row] = best.key ? (int32_t)best.v : -1;

@@ -827,7 +827,8 @@ int dspark_history_add(const dspark_history_t* history, const int32_t* tokens, i
  *   adjusted     [n_rows] rows of V values, adjusted_stride elements apart, in logits' dtype: output x(v),
  *                rounded once from fp32, -inf where v is not allowed; or NULL
  * A request with n_r < 0 or > max_new or rows outside the tensors is left out (DSPARK_STATUS_BAD_ROW), and
- * rows that belong to no request stay as they are.
+ * rows that belong to no request stay as they are; a row that two requests have (offsets that fall and
+ * rise again) gets some token or -1.
  */
 #define DSPARK_TARGET_MAX_ROWS 256
 typedef struct dspark_target {
@@ -851,7 +852,7 @@ typedef struct dspark_target {
 } dspark_target_t;
 /* Bytes of workspace (16-byte aligned) for up to n_rows rows of up to V tokens.  Zero-fill it once,
  * before its first use: the kernel counts the parts of a row in it, and leaves the counts at zero for
- * the next call, of whatever sizes. */
+ * the next call, of whatever sizes.  Calls that may run at the same time need one each. */
 size_t dspark_target_workspace_bytes(int n_rows, int V);
 int dspark_target_tokens(const dspark_target_t* call, uint32_t* status, void* ws, size_t ws_bytes, void* stream);
 

@@ -372,6 +372,30 @@ def test_one_workspace_for_calls_of_all_sizes():
     assert not ws[:4096].any()
 
 
+def test_rows_that_two_requests_have():
+    # offsets that fall and rise again: those rows get one of their tokens, the others theirs, and
+    # what the workspace counts does not reach the next call
+    _say("target, shared rows")
+    s, good = Step(25, [6, 1, 6], 60000, "bf16", lead=0, masks=0, pad=0, tree=False), Step(26, [3, 1], 60000, "bf16")
+    s.penalties, s.history, s.drafts, s.bias = [None] * 3, None, None, None
+    want, row = good.want()[0], s.logits.float()
+    best = torch.where(row == row.amax(1, keepdim=True), torch.arange(s.V, device=cu.DEV), s.V).amin(1).tolist()
+    s.offsets, ws = [0, 6, 2, 8], B.target_workspace(s.n, s.V)
+    ws[4096:] = -1
+    for _ in range(40):
+        kw = dict(s.prepared(adjusted=False), ws=ws)
+        s.call(kw)
+        torch.cuda.synchronize()
+        got = s.target.tolist()
+        assert int(s.status.item()) & B.STATUS_BAD_ROW
+        assert got[:2] + got[6:] == best[:2] + best[6:8] + [-7] * 5
+        assert all(-1 <= v < s.V for v in got[2:6])
+        assert not ws[:4096].any()
+        good.call(dict(good.prepared(adjusted=False), ws=ws))
+        torch.cuda.synchronize()
+        assert good.target.tolist() == [want.get(t, -7) for t in range(good.n)]
+
+
 @pytest.mark.parametrize("penalty", [(0.25, 0.0, 0.0), (1.0, -3.0, 0.0), (1.0, 0.0, -0.5), (0.8, -0.5, 0.0), (0.9, 0.25, -0.25), (0.0, 0.0, 0.0),
                                      (-1.5, 0.0, 0.0), (1e-30, 0.0, 0.0), (1e30, 0.0, 0.0), (1.2, math.inf, 0.0), (1.0, -math.inf, 0.0),
                                      (math.inf, 0.0, 0.0), (math.nan, 0.0, 0.0), (1.0, math.nan, 0.0)])
