@@ -99,12 +99,15 @@ int append_args(const dspark_cache_t* c, int layer, const void* k_new, int64_t k
     return DSPARK_OK;
 }
 
-// Whether rows of `used` elements at q and at out, as far apart from one another, lie between each other
-// without touching, as parts of the same wider rows do.
-bool interleaves(uintptr_t q, uintptr_t out, int64_t q_stride, int64_t out_stride, int64_t used) {
-    if (q_stride != out_stride) return false;
-    const int64_t row = q_stride * 2, apart = (((int64_t)(out - q)) % row + row) % row;
-    return apart >= used * 2 && row - apart >= used * 2;
+// Whether n rows of `used` elements at x and of `out_used` at out touch.  Rows as far apart from one another may
+// lie between each other, as parts of the same wider rows do.
+bool touch(int n, const void* x, int64_t stride, int64_t used, const void* out, int64_t out_stride, int64_t out_used) {
+    const uintptr_t x0 = (uintptr_t)x, y0 = (uintptr_t)out, x1 = x0 + ((uintptr_t)(n - 1) * stride + used) * 2,
+                    y1 = y0 + ((uintptr_t)(n - 1) * out_stride + out_used) * 2;
+    if (x0 >= y1 || y0 >= x1) return false;
+    if (stride != out_stride) return true;
+    const int64_t row = stride * 2, apart = (((int64_t)(y0 - x0)) % row + row) % row;
+    return apart < used * 2 || row - apart < out_used * 2;
 }
 
 int attend(const dspark_cache_t* c, int layer, const void* q, int64_t q_stride, int n_rows, int H,
@@ -318,10 +321,12 @@ int dspark_cache_append_rotary(const dspark_cache_t* c, int layer, const dspark_
     if ((rc = check_rows(q, q_stride, H, c->head_dim, who, "q")) != DSPARK_OK ||
         (rc = check_rows(q_out, q_out_stride, H, c->head_dim, who, "q_out")) != DSPARK_OK)
         return rc;
-    const uintptr_t q0 = (uintptr_t)q, q1 = (uintptr_t)q_out, q_span = ((uintptr_t)(n_rows - 1) * q_stride + (uintptr_t)H * c->head_dim) * 2,
-                    out_span = ((uintptr_t)(n_rows - 1) * q_out_stride + (uintptr_t)H * c->head_dim) * 2;
-    if (q0 == q1 ? q_stride != q_out_stride && n_rows > 1 : q0 < q1 + out_span && q1 < q0 + q_span && !interleaves(q0, q1, q_stride, q_out_stride, (int64_t)H * c->head_dim))
+    const int64_t wide = (int64_t)H * c->head_dim, narrow = (int64_t)c->n_kv_heads * c->head_dim;
+    if (q == q_out ? q_stride != q_out_stride && n_rows > 1 : touch(n_rows, q, q_stride, wide, q_out, q_out_stride, wide))
         return fail(DSPARK_EINVAL, "%s: q and q_out overlap", who);
+    if (touch(n_rows, k_new, k_stride, narrow, q_out, q_out_stride, wide) ||
+        touch(n_rows, v_new, v_stride, narrow, q_out, q_out_stride, wide))
+        return fail(DSPARK_EINVAL, "%s: q_out and k_new or v_new overlap", who);
     g.q = (const uint16_t*)q;
     g.q_out = (uint16_t*)q_out;
     g.q_stride = q_stride;

@@ -713,7 +713,8 @@ int dspark_rotary_turns(const double* freq, int n, uint64_t* turns);
  * r turns by len[r] + j, or by len[r] + depth[row] where depth is given (a tree's rows; its K and V
  * still go to position len[r] + j).  Products and sums are held in fp32 and rounded once.
  *   q, q_out  [n_rows] rows of [H, head_dim], q_stride and q_out_stride elements apart, as k_new.
- *             q_out may be q (with the same stride); otherwise they must not overlap
+ *             q_out may be q (with the same stride); otherwise they must not overlap.  Nor must q_out
+ *             and k_new or v_new; all may be parts of the same wider rows
  *   depth     [n_rows] int32 or NULL
  * Queries of vacant requests and of those that are left out stay as they are.  The other
  * arguments and what is left out are dspark_cache_append's; queries need no pages.

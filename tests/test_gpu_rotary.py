@@ -111,6 +111,15 @@ def test_heads_pages_and_lengths(H, Hkv, page, lead, rows):
     Rows(H, [7, 0, 100], rows, H, Hkv, 64, "bf16", page, lead, wide=H == 17).check(rot)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("most", [1, 2, 3, 4, 5, 7, 8, 9, 16, 17])
+def test_few_rows(most, D):
+    # one to eight tokens stand side by side in a wave, and heads or parts of one beside them
+    _say("rotary, few rows", most, D)
+    rows = [most, 1, (most + 1) // 2, most, 0]
+    Rows(most, [5, 0, 13, -1, 40], rows, 21, 7, D, "fp16" if most % 2 else "bf16", lead=0).check(B.Rotary(D, interleaved=most > 4))
+
+
 @pytest.mark.parametrize("scaling", ["none", "linear", "bands", "ramp"])
 def test_far_positions_and_scalings(scaling):
     # angles are as exact at the far end of a long context as at its start

@@ -100,7 +100,10 @@ def test_append_rotary_refuses():
                    (dict(lead=2), -2), (dict(R=9), -2), (dict(most=-1), -2), (dict(rows=-1), -2),
                    # rows of q and q_out in one another
                    (dict(out=p, os_=512), -1), (dict(out=p + 16), -1), (dict(out=p + 512, qs=512, os_=520), -1),
-                   (dict(out=p + 256, qs=512, os_=512), -1), (dict(out=p + 512 * 2 - 256, qs=512, os_=512), -1)):
+                   (dict(out=p + 256, qs=512, os_=512), -1), (dict(out=p + 512 * 2 - 256, qs=512, os_=512), -1),
+                   # rows of q_out in those of keys or values
+                   (dict(k=far), -1), (dict(v=far), -1), (dict(k=far + 3 * 512 + 496), -1), (dict(v=far + 256, ks=512, os_=512, vs=512), -1),
+                   (dict(k=far + 1024 - 240, ks=512, os_=512), -1)):
         assert call(**kw) == rc, (kw, L.dspark_last_error())
     for kw in (dict(R=0), dict(rows=0), dict(most=0)):
         assert call(q=None, out=None, k=None, v=None, off=None, **kw) == 0
