@@ -18,7 +18,7 @@
 // biases and a mask each) take 71 us, 4.3 TB/s; looking at every changed token took 126.  Groups of eight
 // without an allowed token are not read.  Four such rows, 32 workgroups each, take 11 us, of which the launch and
 // loads that wait for each other (rows, bits, logits, counts) are all but one; a second launch
-// to join the parts made it 16.  About 340 rows of 32771 in fp32, processed and written (89 MB): 41 us, 2.2
+// to join the parts made it 16.  About 340 rows of 32771 in fp32, processed and written (89 MB): 34 us, 2.6
 // TB/s: rows of an odd length stand on no line, and a workgroup is through its part in four loads of a lane.
 #include <algorithm>
 
@@ -120,7 +120,9 @@ __device__ __forceinline__ bool row_of(const dspark_target_t& t, int r, int j, i
     return j < n;
 }
 
-// Eight logits, wherever they stand (rows of an odd vocabulary are not aligned).
+// Eight logits, wherever they stand (rows of an odd vocabulary are not aligned).  Of 16 bits they are read and
+// written past the caches (1152 rows: 75 us, 78 through them); of 32 they are two pieces, between which a line's
+// other half has to stay (340 rows processed: 35 us, 42 past the caches).
 template <class E>
 struct Eight {
     typedef typename E::T T;
@@ -129,11 +131,13 @@ struct Eight {
     u32x4 w[kParts];
     __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-        for (int i = 0; i < kParts; ++i) w[i] = __builtin_nontemporal_load((const any*)p + i);
+        for (int i = 0; i < kParts; ++i) w[i] = kParts == 1 ? __builtin_nontemporal_load((const any*)p) : *((const any*)p + i);
     }
     __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
-        for (int i = 0; i < kParts; ++i) __builtin_nontemporal_store(w[i], (any*)p + i);
+        for (int i = 0; i < kParts; ++i)
+            if (kParts == 1) __builtin_nontemporal_store(w[i], (any*)p);
+            else *((any*)p + i) = w[i];
     }
     __device__ __forceinline__ T bits(int k) const {
         return sizeof(T) == 4 ? (T)w[k / 4][k % 4] : (T)(w[0][k / 2 % 4] >> (k % 2 * 16));
