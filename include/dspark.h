@@ -761,7 +761,8 @@ int dspark_accept_tree(const int32_t* ver_tokens, int n_nodes, const int32_t* of
 /*
  * The accepted path's K and V, every layer's, moved together: position len[r] + path[r, i] to len[r]
  * + lead + i, i < accept_len[r].  len stays: dspark_pages_commit with the same accept_len follows.
- * (Keys were turned to len[r] + depth, which is where they go.)
+ * (Keys were turned to len[r] + depth, which is where they go.)  Of the 16 tokens of a page among which one
+ * comes to stand, the others are written back as they are.
  *   path        [R, K] int32, rising from lead on below DSPARK_TREE_MAX_NODES; may be NULL when K == 0
  *   granted     [R] int32 as dspark_pages_reserve wrote it, or NULL: requests with 0 stay as they are
  * Vacant requests are left out, and so are those whose accept_len does not lie in 0 .. K, whose
