@@ -28,22 +28,27 @@ __device__ __forceinline__ uint64_t shfl64(uint64_t x, int lane) {
 // lowest chain that begins with the same i + 1 tokens; `made` are the lanes that are that one
 // themselves.  Chain s agrees with chain t up to token i where a ballot of equal tokens has
 // the bits s K .. s K + i.
+struct Chains {  // a lane's token, and how many of its chain's count
+    int token, len;
+};
+__device__ __forceinline__ Chains chains_of(const int32_t* tokens, const int32_t* prefix_len, int r, int S, int K) {
+    const int lane = threadIdx.x & 63, s = lane / K;
+    const bool in = s < S;
+    return Chains{in ? tokens[(size_t)r * S * K + lane] : 0, in ? prefix_len ? prefix_len[r * S + s] : K : 0};
+}
 struct Merged {
     int token, node, parent;
     uint64_t made;
 };
-__device__ Merged merged(const int32_t* tokens, const int32_t* prefix_len, int r, int S, int K, uint32_t& bad) {
+__device__ __forceinline__ Merged merged(Chains c, int S, int K, uint32_t& bad) {
     const int lane = threadIdx.x & 63, s = lane / K, i = lane % K;
-    const bool in = s < S;
-    int len = K;
-    if (in && prefix_len) len = prefix_len[r * S + s];
-    if (len < 0 || len > K) {
-        len = 0;
+    if (c.len < 0 || c.len > K) {
+        c.len = 0;
         bad = kStatusBadRow;
     }
     Merged m;
-    m.token = in ? tokens[(size_t)r * S * K + lane] : 0;
-    const bool valid = in && i < len;
+    m.token = c.token;
+    const bool valid = i < c.len;
     const uint64_t want = below(i + 1) << (s * K & 63);
     int first = s;
     bool open = valid;
@@ -79,31 +84,34 @@ __device__ __forceinline__ void write_merged(const MergeOut& out, const Merged& 
     }
 }
 
-// Few requests: one workgroup takes kMergeWaves of them at a time.
+// Few requests: one workgroup, kEach requests to a wave, whose chains are all asked for at once.
 constexpr int kMergeWaves = 16;
+template <int kEach>
 __global__ __launch_bounds__(kMergeWaves * 64) void merge_kernel(const int32_t* tokens, const int32_t* prefix_len, int R, int S,
                                                                  int K, MergeOut out, uint32_t* status) {
-    __shared__ int s_n[kMergeWaves];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int base = 0;
-    for (int r0 = 0; r0 < R; r0 += kMergeWaves) {
-        const int r = r0 + wave;
-        uint32_t bad = 0;
-        Merged m{0, 0, 0, 0};
-        if (r < R) m = merged(tokens, prefix_len, r, S, K, bad);
-        if (__ballot(bad != 0) && lane == 0) raise_status(status, kStatusBadRow);
-        if (lane == 0) s_n[wave] = __popcll(m.made);
-        __syncthreads();
-        int before = base;
-        for (int w = 0; w < kMergeWaves; ++w) {
-            const int n = s_n[w];
-            before += w < wave ? n : 0;
-            base += n;
-        }
-        __syncthreads();  // read, before the next requests' come
-        if (r >= R) continue;
-        if (lane == 0) out.counts[r] = __popcll(m.made);
-        write_merged(out, m, r, R, before);
+    __shared__ int s_n[kEach * kMergeWaves];
+    const int lane = threadIdx.x & 63, r0 = (threadIdx.x >> 6) * kEach;
+    Chains c[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) c[k] = r0 + k < R ? chains_of(tokens, prefix_len, r0 + k, S, K) : Chains{0, 0};
+    Merged m[kEach];
+    uint32_t bad = 0;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        m[k] = merged(c[k], S, K, bad);
+        if (lane == 0) s_n[r0 + k] = __popcll(m[k].made);
+    }
+    if (__ballot(bad != 0) && lane == 0) raise_status(status, kStatusBadRow);
+    __syncthreads();
+    int o = lane < r0 ? s_n[lane] : 0;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) o += __shfl_xor(o, d, 64);
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        if (r0 + k >= R) return;
+        if (lane == 0) out.counts[r0 + k] = __popcll(m[k].made);
+        write_merged(out, m[k], r0 + k, R, o);
+        o += __popcll(m[k].made);
     }
 }
 
@@ -112,7 +120,7 @@ __global__ __launch_bounds__(kT) void merge_count_kernel(const int32_t* tokens, 
     const int r = blockIdx.x * kWaves + (threadIdx.x >> 6);
     if (r >= R) return;
     uint32_t bad = 0;
-    const Merged m = merged(tokens, prefix_len, r, S, K, bad);
+    const Merged m = merged(chains_of(tokens, prefix_len, r, S, K), S, K, bad);
     if (__ballot(bad != 0) && (threadIdx.x & 63) == 0) raise_status(status, kStatusBadRow);
     if ((threadIdx.x & 63) == 0) counts[r] = __popcll(m.made);
 }
@@ -134,7 +142,7 @@ __global__ __launch_bounds__(kT) void merge_write_kernel(const int32_t* tokens, 
     for (int i = r0; i < r && i < R; ++i) o += out.counts[i];
     if (r >= R) return;
     uint32_t bad = 0;
-    const Merged m = merged(tokens, prefix_len, r, S, K, bad);
+    const Merged m = merged(chains_of(tokens, prefix_len, r, S, K), S, K, bad);
     write_merged(out, m, r, R, o);
 }
 
@@ -322,9 +330,10 @@ __global__ __launch_bounds__(kT) void keep_path_kernel(dspark_cache_t c, const i
     }
 }
 
-// The requests up to which one workgroup merges them, sixteen at a time: 4.7 us for 16 and 5.8 for 32, where
-// counting and writing, two launches, take 6.6; for 64 they take 6.7 and one workgroup 8.7.
-constexpr int kMergeAtOnce = 32;
+// The requests up to which one workgroup merges them: 4.8 us for 16, 5.1 for 32 and 6.9 for 64, where counting
+// and writing, two launches, take 6.6 to 6.7, and the host 3 more for the second.
+constexpr int kMergeAtOnce = 4 * kMergeWaves;
+static_assert(kMergeAtOnce <= 64, "a request's count to a lane");
 
 int groups(int R) { return (R + kWaves - 1) / kWaves; }
 
@@ -334,7 +343,8 @@ hipError_t launch_tree_merge(const int32_t* tokens, const int32_t* prefix_len, i
                              int32_t* offsets, int32_t* ver_tokens, int32_t* parent, uint32_t* status, hipStream_t s) {
     const MergeOut out{counts, offsets, ver_tokens, parent};
     if (R <= kMergeAtOnce) {
-        hipLaunchKernelGGL(merge_kernel, dim3(1), dim3(kMergeWaves * 64), 0, s, tokens, prefix_len, R, S, K, out, status);
+        const auto kernel = R <= kMergeWaves ? merge_kernel<1> : R <= 2 * kMergeWaves ? merge_kernel<2> : merge_kernel<4>;
+        hipLaunchKernelGGL(kernel, dim3(1), dim3(kMergeWaves * 64), 0, s, tokens, prefix_len, R, S, K, out, status);
         return hipGetLastError();
     }
     hipLaunchKernelGGL(merge_count_kernel, dim3(groups(R)), dim3(kT), 0, s, tokens, prefix_len, R, S, K, counts, status);

@@ -36,7 +36,8 @@ def forest(rng, n, most=4, roots=0.0):
 
 @pytest.mark.parametrize("R,S,K,V", [(1, 1, 1, 2), (3, 9, 7, 2), (5, 63, 1, 40), (7, 1, 63, 3), (130, 4, 7, 5), (1000, 3, 5, 1000),
                                      (8192, 2, 2, 3),
-                                     (16, 9, 7, 2), (17, 4, 7, 3), (32, 21, 3, 2), (33, 3, 15, 2)])  # one workgroup takes 16 at a time, up to 32
+                                     (16, 9, 7, 2), (17, 4, 7, 3), (32, 21, 3, 2), (33, 3, 15, 2),
+                                     (64, 7, 9, 2), (65, 4, 3, 2)])  # one workgroup takes up to 64
 def test_merge(R, S, K, V):
     _say("merge", R, S, K, V)
     rng = np.random.default_rng(R + S)
