@@ -196,3 +196,32 @@ def test_what_does_not_fit_is_left_out():
     c.call(B.Rotary(64))
     assert int(c.status.item()) == B.STATUS_BAD_ROW and (c.q_out == 7).all()
     c.st.assert_data()
+
+
+def test_a_prompt_of_more_blocks_than_a_launch_takes():
+    _say("rotary, a million rows")
+    n, ln, D, page = 65535 * 16 + 37, 5, 64, 256
+    width = (ln + n + page - 1) // page
+    cache = B.PagedCache(1, width, page, 1, D, B.DSPARK_BF16, 1, width, device=cu.DEV)
+    cache.table[0] = torch.arange(width, dtype=torch.int32, device=cu.DEV).flip(0)
+    cache.ref.fill_(1)
+    cache.len.fill_(ln)
+    g = torch.Generator(device=cu.DEV)
+    g.manual_seed(8)
+    q, k, v = (torch.randn((n, 1, D), generator=g, device=cu.DEV).to(torch.bfloat16) for _ in range(3))
+    out, status, rot = torch.full_like(q, 7.0), torch.zeros(1, dtype=torch.int32, device=cu.DEV), B.Rotary(D)
+    B.dspark_cache_append_rotary(cache, 0, rot, q, out, k, v, cu.i32([0, n]), 0, n, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    order = cache.table[0].long()
+    in_v = cache.v[0, order, 0].permute(0, 1, 3, 2).reshape(-1, D)[ln:ln + n]           # blocks as [D][16]
+    in_k = cache.k[0, order, 0].permute(0, 1, 3, 2, 4).reshape(-1, D)[ln:ln + n]        # blocks as [D / 8][16][8]
+    assert torch.equal(in_v, v[:, 0])
+    for x, y in ((q[:, 0], out[:, 0]), (k[:, 0], in_k)):  # a turn leaves each pair as long as it was, but for two roundings
+        a, b = (z.float().view(n, 2, D // 2).norm(dim=1) for z in (x, y))
+        assert ((a - b).abs() <= (2.0 ** -8 + 2.0 ** -18) * a).all()
+    at = torch.tensor([0, 15, 16, 65535 * 16 - 6, 65535 * 16 - 5, 65535 * 16 - 4, 65535 * 16, n - 1])
+    for x, y in ((q, out[:, 0]), (k, in_k)):
+        want, reach = ot.rotate(x[at].cpu().double().numpy(), ln + at.numpy(), rot.freq, D, 0, False, 1.0)
+        bound = 2.0 ** -21 * reach + 2.0 ** -8 * np.abs(want) + 2.0 ** -25
+        assert (np.abs(y[at].cpu().double().numpy()[:, None] - want) <= bound).all()
