@@ -13,15 +13,17 @@
 // pair (in halves; interleaved, two neighbours), and a few heads one after the other with the same
 // sines, the next one's loads under way.  Eight tokens stand side by side in a wave, so that their
 // pieces make a line of the page; of rows that are fewer, more heads.  The workgroup computes its
-// tokens' sines once, into LDS, while the first loads are under way.
+// tokens' sines once, into LDS, while the first loads are under way.  Where no request has more than eight
+// rows, they are one such set for K and V too, whichever one or two blocks they go to: by blocks most
+// workgroups would have few rows or none.
 //
 // Bytes bound it, once read, once written.  The workgroups that share rows are neighbours in the grid:
 // 20 thousand fp16 rows of 32 query and 8 key heads of 128 (353 MB) take 78 us (4.5 TB/s; a large copy
 // reaches 4.9), 108 where a kind's workgroups follow each other through all rows.  1152 rows of 64 and 8 heads
-// (47 MB), of requests of up to eight: 22 us, of which 6 are the launch and the loads that wait for each
-// other; a copy of as many bytes takes 10, for which the waves would have to be resident at once.  Eight
-// heads a lane instead of two: 92 and 24 us (fewer waves); a request's blocks walked in a loop in place of a
-// workgroup each: 97 and 28 (twice the registers, half the waves).
+// (47 MB), of requests of up to eight: 20.6 us (22.4 by blocks), of which 6 are the launch and the loads that
+// wait for each other; a copy of as many bytes takes 10, for which the waves would have to be resident at
+// once.  Eight heads a lane instead of two: 92 and 22 us (fewer waves), one head 22; a request's blocks walked in
+// a loop in place of a workgroup each: 97 and 28 (twice the registers, half the waves).
 #include <algorithm>
 
 #include "append_dev.h"
@@ -85,14 +87,14 @@ __device__ __forceinline__ float2 cos_sin(uint32_t angle, float m) {
                        m * __uint_as_float(__float_as_uint(odd ? c : s) ^ (quarter & 0x80000000u)));
 }
 
-struct Split {  // of the work on a block of 16 tokens among workgroups
-    int shift_t;           // Q: 1 << shift_t tokens side by side in a wave
+struct Split {  // of the work on a block of 16 tokens (few: on all) among workgroups
+    int shift_t;           // Q (few: K too): 1 << shift_t tokens side by side in a wave
     int q_halves;          // Q: 1 where the other half of the block has workgroups of its own
     int v_parts, k_parts;  // Q has the rest of the grid
     long long first_block;
 };
 
-template <class E, bool kInterleaved>
+template <class E, bool kInterleaved, bool kFew>
 __global__ __launch_bounds__(kT, 8) void append_rotary_kernel(RotaryArgs g, Split sp) {
     extern __shared__ __attribute__((aligned(16))) float2 s_cs[];  // [tokens][dim / 2]
     const AppendArgs& a = g.a;
@@ -109,25 +111,46 @@ __global__ __launch_bounds__(kT, 8) void append_rotary_kernel(RotaryArgs g, Spli
     const bool is_q = part >= sp.v_parts + sp.k_parts, is_v = part < sp.v_parts;
     const int q_part = part - sp.v_parts - sp.k_parts, unit = (is_q ? q_part >> sp.q_halves : is_v ? part : part - sp.v_parts) * 4 + wave;
     // Rows j0 .. of the request: of a block of positions (V, K), or from the first row on (Q).
-    const long long block = sp.first_block + blockIdx.y, j64 = block * kBlockTokens - (is_q ? -((q_part & sp.q_halves) * 8) : ln & (kBlockTokens - 1));
+    const int ahead = ln & (kBlockTokens - 1);  // tokens in front of the first one in its block
+    const long long block = sp.first_block + blockIdx.y, j64 = kFew ? 0 : block * kBlockTokens - (is_q ? -((q_part & sp.q_halves) * 8) : ahead);
     if (n == 0 || j64 >= n) return;  // (with n = 0 the block that the kept tokens end in is not this step's)
     const int j0 = (int)j64;
-    size_t block0 = 0;  // of the tokens, in the page's first head
-    if (!is_q) {
-        const long long pos = (long long)ln + j0;
+    // The block of row j's position, in its page's first head; -1 where there is no page to write to.
+    const auto block_of = [&](int j) -> long long {
+        const long long pos = (long long)ln + j;
         const int page = a.table[(size_t)r * a.width + (pos >> shift)];
         if (page < 0 || page >= a.n_pages || a.ref[page] > 1) {  // not there, or another row's too
             if (part == 0 && tid == 0) raise_status(a.status, kStatusBadPage);
-            return;
+            return -1;
         }
-        block0 = ((size_t)page * a.Hkv << (shift - 4)) + ((int)(pos & ((1 << shift) - 1)) >> 4);
+        return ((long long)page * a.Hkv << (shift - 4)) + ((int)(pos & ((1 << shift) - 1)) >> 4);
+    };
+    long long block0 = 0, block1 = 0;  // block1: of the rows behind the first block (few)
+    if (!is_q) {
+        block0 = block1 = block_of(j0);
+        if (kFew && ahead + n > kBlockTokens) block1 = block_of(n - 1);
+        if (block0 < 0 && block1 < 0) return;
     }
     if (is_v) {
         const int row8 = (lane >> 5) * 4 + (lane >> 4 & 1) * 2 + (lane & 1);  // token of the eight; afterwards dim of the eight
         const int c8 = lane >> 1 & 7, shift_h = __builtin_ctz(D >> 6);       // eight dims of the 64
         const int h = unit >> shift_h, d0 = (unit & ((D >> 6) - 1)) * 64;
         if (h >= a.Hkv) return;
-        uint16_t* block = a.v + (block0 + ((size_t)h << (shift - 4))) * (size_t)(kBlockTokens * D) + (d0 + c8 * 8 + row8) * kBlockTokens;
+        const size_t head = (size_t)h << (shift - 4), in = (size_t)(d0 + c8 * 8 + row8) * kBlockTokens;
+        if (kFew) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (row8 < n) v = once(a.v_new + (size_t)(row0 + row8) * a.v_stride + h * D + d0 + c8 * 8);
+            const uint4 x = turned(v);
+            const uint32_t* w = &x.x;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const long long b = ahead + i < kBlockTokens ? block0 : block1;
+                if (i < n && b >= 0)
+                    a.v[((size_t)b + head) * (size_t)(kBlockTokens * D) + in + (ahead + i) % kBlockTokens] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+            }
+            return;
+        }
+        uint16_t* block = a.v + ((size_t)block0 + head) * (size_t)(kBlockTokens * D) + in;
         uint4 v[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -153,13 +176,15 @@ __global__ __launch_bounds__(kT, 8) void append_rotary_kernel(RotaryArgs g, Spli
         return;
     }
     // A lane's token, its item of a head (two pieces of eight dims) and its heads.
-    const int items = D >> 4, shift_items = __builtin_ctz(items), shift_side = 6 - (is_q ? sp.shift_t : 3);
-    const int halves = is_q ? 0 : 1, strips = max(shift_items - shift_side, 0), step = 1 << max(shift_side - shift_items, 0);
+    const int items = D >> 4, shift_items = __builtin_ctz(items), shift_side = 6 - (is_q || kFew ? sp.shift_t : 3);
+    const int halves = is_q || kFew ? 0 : 1, strips = max(shift_items - shift_side, 0), step = 1 << max(shift_side - shift_items, 0);
     const int slot = (lane & ((1 << shift_side) - 1)) + ((unit >> halves & ((1 << strips) - 1)) << shift_side);
     const int e = slot & (items - 1), h0 = (unit >> (halves + strips)) * kPasses * step + (slot >> shift_items);
-    const int t = (is_q ? 0 : (unit & 1) * 8) + (lane >> shift_side), j = j0 + t;
+    const int t = (halves ? (unit & 1) * 8 : 0) + (lane >> shift_side), j = j0 + t;
     int left = min(h0 + kPasses * step, is_q ? g.H : a.Hkv) - h0;  // while > 0
     if (j < 0 || j >= n) left = 0;
+    const long long to_block = kFew && ahead + j >= kBlockTokens ? block1 : block0;
+    if (kFew && to_block < 0) left = 0;
     // Its two pieces: a pair's, in halves, or two neighbours; behind those that turn, the others.
     const int first = g.first >> 3, turning = g.dim >> 4, pass = 2 * (e - turning);
     const bool turns = e < turning;
@@ -174,7 +199,7 @@ __global__ __launch_bounds__(kT, 8) void append_rotary_kernel(RotaryArgs g, Spli
         y = once(from + from_y);
     }
     const int pairs = g.dim >> 1;
-    for (int i = wave; i < (is_q ? 1 << sp.shift_t : kBlockTokens); i += kT / 64) {
+    for (int i = wave; i < (is_q || kFew ? 1 << sp.shift_t : kBlockTokens); i += kT / 64) {
         if (j0 + i < 0 || j0 + i >= n) continue;
         const long long at = ln + (long long)(g.depth ? g.depth[row0 + j0 + i] : j0 + i);
         for (int f = lane; f < pairs; f += 64)
@@ -187,7 +212,7 @@ __global__ __launch_bounds__(kT, 8) void append_rotary_kernel(RotaryArgs g, Spli
     const int to_piece = is_q ? 8 : kBlockTokens * 8, to_y = (py - px) * to_piece;
     const size_t to_step = is_q ? step * D : (size_t)(step * D) << shift;
     uint16_t* to = (is_q ? g.q_out + row * g.q_out_stride + h0 * D
-                         : a.k + block0 * (size_t)(kBlockTokens * D) + ((size_t)(h0 * D) << shift) + t * 8) + px * to_piece;
+                         : a.k + (size_t)to_block * (kBlockTokens * D) + ((size_t)(h0 * D) << shift) + (kFew ? (ahead + j) % kBlockTokens : t) * 8) + px * to_piece;
 #pragma unroll 1
     while (left > 0) {
         uint4 u = x, v = y;
@@ -216,13 +241,20 @@ hipError_t launch_append_rotary(const RotaryArgs& g, hipStream_t s) {
         return ((heads + at_once - 1) / at_once * strips * halves + 3) / 4;
     };
     sp.v_parts = (g.a.Hkv * (g.a.D / 64) + 3) / 4;
-    sp.k_parts = parts(8, g.a.Hkv, 2);
+    // Up to eight rows stand side by side whatever the blocks they go to; more are taken by blocks, whose
+    // rows of V are then written whole.
+    const bool few = g.a.max_new <= 8;
+    sp.k_parts = few ? parts(64 >> sp.shift_t, g.a.Hkv, 1) : parts(8, g.a.Hkv, 2);
     const int all = sp.v_parts + sp.k_parts + (parts(64 >> sp.shift_t, g.H, 1) << sp.q_halves);
-    const long long blocks = (std::min(g.a.max_new, g.a.rows) + 2ll * (kBlockTokens - 1)) / kBlockTokens;  // that the tokens can touch
-    const size_t lds = kBlockTokens * (g.dim / 2) * sizeof(float2);
-    const auto kernel = g.dtype == DSPARK_F16 ? g.interleaved ? append_rotary_kernel<RF16, true> : append_rotary_kernel<RF16, false>
-                        : g.interleaved       ? append_rotary_kernel<RBf16, true>
-                                              : append_rotary_kernel<RBf16, false>;
+    const long long blocks = few ? 1 : (std::min(g.a.max_new, g.a.rows) + 2ll * (kBlockTokens - 1)) / kBlockTokens;  // that the tokens can touch
+    const size_t lds = (few ? 1 << sp.shift_t : kBlockTokens) * (g.dim / 2) * sizeof(float2);
+    const auto pick = [&](auto e) {
+        typedef decltype(e) E;
+        return g.interleaved ? few ? append_rotary_kernel<E, true, true> : append_rotary_kernel<E, true, false>
+               : few         ? append_rotary_kernel<E, false, true>
+                             : append_rotary_kernel<E, false, false>;
+    };
+    const auto kernel = g.dtype == DSPARK_F16 ? pick(RF16{}) : pick(RBf16{});
     for (sp.first_block = 0; sp.first_block < blocks; sp.first_block += 65535)
         hipLaunchKernelGGL(kernel, dim3(all, (unsigned)std::min(blocks - sp.first_block, 65535ll), g.a.R), dim3(kT), lds, s, g, sp);
     return hipGetLastError();

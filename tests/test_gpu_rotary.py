@@ -191,6 +191,12 @@ def test_what_does_not_fit_is_left_out():
     st = c.st
     st.len = [n if n < 1_000_000 else -1 for n in st.len]  # (out of all tables: left out)
     c.check(B.Rotary(64), status=B.STATUS_BAD_PAGE | B.STATUS_BAD_ROW)
+    for most in (6, 9):  # rows over two pages of which one is missing or another's
+        c = Rows(most, [13, 13, 13, 10, 13], [6, 6, 6, most, 6], 5, 3, 128, "fp16")
+        c.st.table[0][1] = c.st.table[1][0] = -1
+        c.st.ref[c.st.table[2][1]] = c.st.ref[c.st.table[4][0]] = 2
+        c.st.upload()
+        c.check(B.Rotary(64, first=32), status=B.STATUS_BAD_PAGE)
     c = Rows(7, [10, 10, 10], [6, 6, 6], 4, 2, 64)
     c.offsets = [0, 7, 2, 2_000_000_000]       # more rows than max_new, fewer than none, past the tensors
     c.call(B.Rotary(64))
