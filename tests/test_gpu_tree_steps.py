@@ -189,7 +189,7 @@ def test_tree_steps():
             b_out, b_lse = cu.attend_bounds(want, "bf16", 300, D)
             seen = np.isfinite(lse)
             assert (np.abs(got - out)[seen] <= (b_out + (2 * off[..., None]) * spread * 1.2)[seen]).all()
-            assert (np.abs(glse - lse)[seen] <= (b_lse + off)[seen]).all() and (got[~seen] == 0).all()
+            assert (np.abs(glse[seen] - lse[seen]) <= (b_lse + off)[seen]).all() and (got[~seen] == 0).all()
         st.k[:], st.v[:] = moved_k, moved_v
         bad |= oc.commit(st.table, st.len, st.ref, accept, 1, PAGE, granted)
         e.said.add(emitted, True, range(R))
