@@ -467,7 +467,7 @@ __global__ __launch_bounds__(kT, kPerSimd) void target_kernel(TargetArgs a) {
         if (tid == 0) __hip_atomic_fetch_sub(&a.came[row], (uint32_t)a.parts, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next call
     }
     if (tid == 0) {
-        t.target[row] = best.key ? (int32_t)best.v : -1;
+        t.target[row] = best.key ? (int32_t)best.v : 0;  // 0: the argmax of values that are all -inf
         if (!best.key) raise_status(a.status, kStatusNoToken);
     }
 }
@@ -486,7 +486,7 @@ __global__ __launch_bounds__(64) void target_join_kernel(TargetArgs a) {
     }
     wave_best(best);
     if (threadIdx.x == 0) {
-        a.t.target[row] = best.key ? (int32_t)best.v : -1;
+        a.t.target[row] = best.key ? (int32_t)best.v : 0;
         if (!best.key) raise_status(a.status, kStatusNoToken);
     }
 }

@@ -78,7 +78,7 @@ typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_F16 = 2 /* the paged cach
                                            length or index do not fit (see each call for what becomes of it) */
 #define DSPARK_STATUS_NO_PAGES 128u     /* paged cache: too few free pages, or no room in the table; the request or
                                            fork was not served                                              */
-#define DSPARK_STATUS_NO_TOKEN 256u     /* dspark_target_tokens: a row's mask allows no token; its target is -1 */
+#define DSPARK_STATUS_NO_TOKEN 256u     /* dspark_target_tokens: a row's mask allows no token; its target is 0 */
 
 /* Admission rules of stage 4. */
 #define DSPARK_RULE_ARGMAX 0      /* the smallest B with the largest f(B) (vLLM blog, "Scheduling the budget")  */
@@ -825,12 +825,13 @@ int dspark_history_add(const dspark_history_t* history, const int32_t* tokens, i
  *                word v / 32 set where token v is allowed; or NULL: all are
  *   allowed_row  [n_rows] int32: the row of allowed that binds row t, -1 for none; or NULL: row t.  Another
  *                number allows nothing (DSPARK_STATUS_BAD_ROW)
- *   target       [n_rows] int32 output; -1 where no token is allowed (DSPARK_STATUS_NO_TOKEN)
+ *   target       [n_rows] int32 output; 0 where no token is allowed, as the argmax of values that are all
+ *                -inf (DSPARK_STATUS_NO_TOKEN)
  *   adjusted     [n_rows] rows of V values, adjusted_stride elements apart, in logits' dtype: output x(v),
  *                rounded once from fp32, -inf where v is not allowed; or NULL
  * A request with n_r < 0 or > max_new or rows outside the tensors is left out (DSPARK_STATUS_BAD_ROW), and
  * rows that belong to no request stay as they are; a row that two requests have (offsets that fall and
- * rise again) gets some token or -1.
+ * rise again) gets some token.
  */
 #define DSPARK_TARGET_MAX_ROWS 256
 typedef struct dspark_target {

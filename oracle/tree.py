@@ -224,7 +224,8 @@ class History:
 
 def choose(logits, path, prompt=(), count=None, repetition=1.0, presence=0.0, frequency=0.0, bias=None, allowed=None):
     """One row: logits [V] float64, path the drafts that it has behind it, prompt a set, count and bias dicts,
-    allowed [V] truth values or None.  Returns (token or -1, processed logits)."""
+    allowed [V] truth values or None.  Returns (token, processed logits); token 0 where nothing is
+    allowed, the lowest of values that are all -inf."""
     x = logits.copy()
     times = dict(count or {})
     for v in path:
@@ -243,7 +244,7 @@ def choose(logits, path, prompt=(), count=None, repetition=1.0, presence=0.0, fr
     y = np.full_like(x, -np.inf)
     y[free] = x[free]
     if not len(free):
-        return -1, y
+        return 0, y
     nan = free[np.isnan(x[free])]
     best = nan[0] if len(nan) else free[np.argmax(x[free])]
     return int(best), y

@@ -91,7 +91,7 @@ def test_worked_choices():
     assert ot.choose(x, [], bias={4: 5.0})[0] == 4
     t, y = ot.choose(x, [], allowed=np.array([0, 0, 1, 0, 1], bool))
     assert t == 4 and y.tolist() == [-np.inf, -np.inf, -1.0, -np.inf, 0.0]
-    assert ot.choose(x, [], allowed=np.zeros(5, bool))[0] == -1
+    assert ot.choose(x, [], allowed=np.zeros(5, bool))[0] == 0
     assert ot.choose(np.array([1.0, np.nan, np.nan]), [])[0] == 1
     assert ot.choose(np.array([1.0, np.nan]), [], allowed=np.array([1, 0], bool))[0] == 0
     assert ot.choose(np.array([-np.inf, -np.inf]), [], allowed=np.array([0, 1], bool))[0] == 1
