@@ -369,12 +369,14 @@ __device__ __forceinline__ void join(float& m, float& l, float (&acc)[8], float 
 }
 
 // Adds the parts that workers wa..wb have left of a segment: column `col` of its tile.  kAtOnce
-// parts are requested at a time, so that a long segment's parts do not wait for each other.
+// parts are requested at a time, so that a long segment's parts do not wait for each other; the last
+// four or fewer of eight at a time by themselves, so that no part is asked for again.
 template <int kAtOnce>
 __device__ __forceinline__ void join_parts(const AttendArgs& a, int set, int wa, int wb, int col, int c8, float& m,
-                                           float& l, float (&acc)[8]) {
+                                           float& l, float (&acc)[8], int from = 0) {
     const size_t tile = a.tile[set];
-    for (int w0 = wa; w0 <= wb; w0 += kAtOnce) {
+    for (int w0 = wa + from; w0 <= wb; w0 += kAtOnce) {
+        if (kAtOnce > 4 && wb - w0 < 4) return join_parts<4>(a, set, wa, wb, col, c8, m, l, acc, w0 - wa);
         float pm[kAtOnce], pl[kAtOnce];
         float4 x[kAtOnce], y[kAtOnce];
 #pragma unroll
@@ -417,11 +419,11 @@ __device__ __forceinline__ void join_item(const AttendArgs& a, int set, const Sp
     }
 }
 
-template <class E>
+template <class E, bool kTree>
 __device__ __forceinline__ void store_row(const AttendArgs& a, int f, int h, int c8, float m, float l,
                                           const float (&acc)[8]) {
     const int row = f / a.G, head = h * a.G + f % a.G;
-    if (a.anc && a.anc[row] == 0) l = 0.f;  // a row that sees nothing, its request's tokens neither
+    if (kTree && a.anc[row] == 0) l = 0.f;  // a row that sees nothing, its request's tokens neither
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // the one rounding to 16 bits of the result
@@ -482,11 +484,11 @@ __device__ __forceinline__ uint32_t clear_masked(s16x8& v, int valid) {
 // Column c of the tile at f0 is done as far as this worker goes: eight dims of it, from 8 c8
 // on.  The result, where the segment ends here and has all of its keys (final); else the
 // part, for whoever joins it.
-template <class E, int kSet>
+template <class E, int kSet, bool kTree>
 __device__ __forceinline__ void finish(const AttendArgs& a, int worker, bool final, bool whole, bool begins, int f0, int c,
                                        int h, int c8, float m, float l, const float (&acc)[8]) {
     if (kSet == 0 && final) {
-        store_row<E>(a, f0 + c, h, c8, m, l, acc);
+        store_row<E, kTree>(a, f0 + c, h, c8, m, l, acc);
         return;
     }
     Dense d;
@@ -510,7 +512,7 @@ __device__ __forceinline__ void finish(const AttendArgs& a, int worker, bool fin
 // lane.  m and l are the lanes' columns'.
 constexpr int kPitch = 36;
 
-template <class E, int kSet, int NT>
+template <class E, int kSet, bool kTree, int NT>
 __device__ __forceinline__ void finish_wave(const AttendArgs& a, float* s_o, int worker, bool final, bool whole,
                                             bool begins, int f0, int c0, int nf, int h, float m, float l, const f32x16 (&o)[NT]) {
     const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
@@ -527,7 +529,7 @@ __device__ __forceinline__ void finish_wave(const AttendArgs& a, float* s_o, int
             const float jm = __shfl(m, c, 64), jl = __shfl(l, c, 64);
             const float4 x = *(const float4*)&s_o[c * kPitch + c8 * 8], y = *(const float4*)&s_o[c * kPitch + c8 * 8 + 4];
             const float acc[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-            if (c0 + c < nf) finish<E, kSet>(a, worker, final, whole, begins, f0, c0 + c, h, t * 4 + c8, jm, jl, acc);
+            if (c0 + c < nf) finish<E, kSet, kTree>(a, worker, final, whole, begins, f0, c0 + c, h, t * 4 + c8, jm, jl, acc);
         }
         __builtin_amdgcn_wave_barrier();
     }
@@ -786,7 +788,7 @@ __global__ __launch_bounds__(kT, D <= 128 ? 2 : 1) void attend_kernel(AttendArgs
                 join(jm, jl, acc, s_m[from][c % 32], s_l[from][c % 32], *(const float4*)&s_o[from][c % 32][c8 * 8],
                      *(const float4*)&s_o[from][c % 32][c8 * 8 + 4]);
             }
-            finish<E, kSet>(a, blockIdx.x, final, whole, begins, f0, c, h, d0 / 8 + c8, jm, jl, acc);
+            finish<E, kSet, kTree>(a, blockIdx.x, final, whole, begins, f0, c, h, d0 / 8 + c8, jm, jl, acc);
         }
     };
 
@@ -1227,34 +1229,29 @@ __global__ __launch_bounds__(Wide<D>::kThreads, Wide<D>::kWaves / 4 * Wide<D>::k
 
         const bool whole = cur.whole();
         __syncthreads();  // LDS is free
-        finish_wave<E, kSet, NT>(a, (float*)s_mem + wave * (32 * kPitch), me, whole && q.kb == 0, whole, cur.unit0 == 0, f0, wave * 32, nf,
+        finish_wave<E, kSet, kTree, NT>(a, (float*)s_mem + wave * (32 * kPitch), me, whole && q.kb == 0, whole, cur.unit0 == 0, f0, wave * 32, nf,
                                  h, m, l, o);
     } while (cur.step());
 }
 
 // Joins the parts of the segments that were split, where no prefix is shared.  Where worker w
 // goes on with a segment that worker w - 1 began, workgroup (w, .) joins it, eight dims of a
-// column to a thread.
-template <class E>
+// column to a thread.  kMany: eight parts at a time, else four (see joins_many).
+template <class E, bool kTree, bool kMany>
 __global__ __launch_bounds__(kT) void attend_join_kernel(AttendArgs a) {
     const AttendEnd e = a.ends[blockIdx.x];
     if (e.units == 0 || e.first != (int)blockIdx.x - 1) return;
     const int chunks = a.D / 8, c = blockIdx.y * (kT / chunks) + threadIdx.x / chunks, c8 = threadIdx.x % chunks;
     if (c >= e.nf) return;
     float m = -kInf, l = 0.f, acc[8] = {};
-    // Two trees of 131072 tokens, 48 parts a segment: 18 us with eight at a time, 22 with four.  Of four
-    // parts and fewer the other half would be loaded for nothing.
-    if (e.last - e.first >= 4)
-        join_parts<8>(a, 0, e.first, e.last, c, c8, m, l, acc);
-    else
-        join_parts<4>(a, 0, e.first, e.last, c, c8, m, l, acc);
-    store_row<E>(a, e.f0 + c, e.h, c8, m, l, acc);
+    join_parts<kMany ? 8 : 4>(a, 0, e.first, e.last, c, c8, m, l, acc);
+    store_row<E, kTree>(a, e.f0 + c, e.h, c8, m, l, acc);
 }
 
 // Joins everything where prefixes are shared: a workgroup the columns of a request with one
 // key head (up to kAttendJoinItems of eight dims), from its own launch and its group's.
 static_assert(kAttendJoinItems % kT == 0, "as many items to every thread");
-template <class E>
+template <class E, bool kTree>
 __global__ __launch_bounds__(kT) void attend_join_shared_kernel(AttendArgs a) {
     const int r = blockIdx.x, h = blockIdx.y, chunks = a.D / 8;
     Request q;
@@ -1284,7 +1281,7 @@ __global__ __launch_bounds__(kT) void attend_join_shared_kernel(AttendArgs a) {
         if (g.ke > 0)
             join_item(a, 1, common, g_u0, tiles_in(a, 1, g.n), units_in(a, 1, g.ke), f0 + c, f0 + c - g.start * a.G, h, c8, m,
                       l, acc);
-        store_row<E>(a, f0 + c, h, c8, m, l, acc);
+        store_row<E, kTree>(a, f0 + c, h, c8, m, l, acc);
     }
 }
 
@@ -1303,23 +1300,38 @@ hipError_t run_set(const AttendArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <class E, int D>
+// Whether the segments, as many as these sizes allow, are so few that each is in four parts or more on
+// average: then a joining thread waits less often with eight parts under way (the whole call, one token behind
+// 131072, 32/8 heads of 128: 121 to 116 us; 16 behind up to 700: 14.9 to 14.5).  Else the registers for
+// them, 114 in place of 65, keep out workgroups that join a part or two (prompts of 300 rows at head_dim 256:
+// 66.4 us with four, 68.6 with eight; 32 requests of eight rows behind up to 500: 27.5 and 28.0).
+bool joins_many(const AttendArgs& a) {
+    const auto tiles = [&](long long rows) { return (rows * a.G + a.tile[0] - 1) >> a.tile_shift[0]; };
+    return 4 * a.Hkv * std::min(a.R * tiles(a.max_new), a.R + tiles(a.rows)) <= a.workers[0];
+}
+
+template <class E, int D, bool kTree>
 hipError_t run(const AttendArgs& a, hipStream_t s) {
     hipError_t e = a.n_groups ? run_set<E, D, 1, false>(a, s) : hipSuccess;  // (all of its rows see all of its keys)
-    if (e == hipSuccess) e = a.anc ? run_set<E, D, 0, true>(a, s) : run_set<E, D, 0, false>(a, s);
+    if (e == hipSuccess) e = run_set<E, D, 0, kTree>(a, s);
     if (e != hipSuccess) return e;
     if (a.n_groups)
-        hipLaunchKernelGGL(attend_join_shared_kernel<E>,
+        hipLaunchKernelGGL((attend_join_shared_kernel<E, kTree>),
                            dim3(a.R, a.Hkv, ((size_t)a.max_new * a.G * (D / 8) + kAttendJoinItems - 1) / kAttendJoinItems), dim3(kT), 0,
                            s, a);
     else
-        hipLaunchKernelGGL(attend_join_kernel<E>, dim3(a.workers[0], a.tile[0] / (kT / (D / 8))), dim3(kT), 0, s, a);
+        hipLaunchKernelGGL((joins_many(a) ? attend_join_kernel<E, kTree, true> : attend_join_kernel<E, kTree, false>),
+                           dim3(a.workers[0], a.tile[0] / (kT / (D / 8))), dim3(kT), 0, s, a);
     return hipGetLastError();
 }
 
-template <class E>
+template <class E, bool kTree>
 hipError_t run_dim(const AttendArgs& a, hipStream_t s) {
-    return a.D == 64 ? run<E, 64>(a, s) : a.D == 128 ? run<E, 128>(a, s) : run<E, 256>(a, s);
+    return a.D == 64 ? run<E, 64, kTree>(a, s) : a.D == 128 ? run<E, 128, kTree>(a, s) : run<E, 256, kTree>(a, s);
+}
+template <class E>
+hipError_t run_form(const AttendArgs& a, hipStream_t s) {
+    return a.anc ? run_dim<E, true>(a, s) : run_dim<E, false>(a, s);
 }
 
 // Two parts a worker, of as many columns a compute unit as the forms have.
@@ -1379,7 +1391,7 @@ void attend_forms(AttendArgs& a, int cus) {
 }
 
 hipError_t launch_attend(const AttendArgs& a, hipStream_t s) {
-    return a.dtype == DSPARK_F16 ? run_dim<F16>(a, s) : run_dim<Bf16>(a, s);
+    return a.dtype == DSPARK_F16 ? run_form<F16>(a, s) : run_form<Bf16>(a, s);
 }
 
 }  // namespace dspark

@@ -189,3 +189,38 @@ def test_row_strides_streams_and_a_captured_call():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(eager, out)
+
+
+def _as_a_chain(c, rows):
+    """The tree's call with the words of chains, and the causal call: the same bits."""
+    c.anc = sum(([(2 << j) - 1 for j in range(n)] for n in rows), [])
+    p = c.check()
+    out, lse = torch.full_like(p["out"], 7.0), torch.full_like(p["lse"], 7.0)
+    B.dspark_cache_attend(c.st.cache, 0, p["q"], p["offsets"], 1, c.max_new, c.scale, out, lse=lse, shared=p["shared"], ws=p["ws"])
+    torch.cuda.synchronize()
+    assert torch.equal(out, p["out"]) and torch.equal(lse, p["lse"])
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64), ("bf16", 256)])
+def test_segments_in_any_number_of_parts(dtype, D):
+    # one segment of 1 to 18 units of 128 keys, most of them in as many parts: joined eight at a time, the
+    # last ones four at a time
+    for parts in range(1, 19):
+        _say("tree, parts", dtype, D, parts)
+        Tree(parts, [128 * parts - 4], [4], 4, 1, D, dtype).check()
+        _as_a_chain(Tree(parts, [128 * parts - 4], [4], 4, 1, D, dtype), [4])
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64), ("bf16", 256)])
+def test_long_segments_among_many_short_ones(dtype, D):
+    # so many segments that they are joined four at a time, one of them in many parts
+    _say("tree, many short", dtype, D)
+    rng = np.random.default_rng(D)
+    rows = rng.integers(1, 5, 40).tolist()
+    lens = rng.integers(0, 60, 40).tolist()
+    lens[7], lens[31] = 5003, 700
+    Tree(31, lens, rows, 8, 8, D, dtype).check()
+    _as_a_chain(Tree(32, lens, rows, 8, 8, D, dtype), rows)
+    rows = [64] * 9      # and the form of many rows
+    lens = [1000, 0, 31, 5, 17, 900, 2500, 64, 1]
+    Tree(33, lens, rows, 16, 8, D, dtype).check()
