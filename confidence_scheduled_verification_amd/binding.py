@@ -957,6 +957,8 @@ def dspark_target_tokens(logits, offsets, lead: int, max_new: int, target, histo
         if len(allowed.shape) != 2 or allowed.dtype is not torch.int32 or (allowed.stride(1) != 1 and allowed.numel()):
             raise ValueError(f"{what}: allowed must be int32 [masks, words] with densely packed rows")
         n_allowed, words = allowed.shape
+        if words * 32 < V:
+            raise ValueError(f"{what}: allowed has rows of {words} words, {V} tokens need {(V + 31) // 32}")
         pitch = allowed.stride(0) if n_allowed > 1 else words
     if history is not None and history.device != logits.device:
         raise ValueError(f"{what}: the history is on {history.device}, logits on {logits.device}")

@@ -257,3 +257,14 @@ def test_turns_are_exact():
         want = Fraction(f) / two_pi % 1
         far = abs(Fraction(got, 1 << 64) - want)
         assert min(far, 1 - far) <= Fraction(max(abs(f), 1.0)) / (1 << 63)
+
+
+def test_binding_refuses_masks_narrower_than_the_vocabulary():
+    # a mask's words, not only how far its rows lie apart: the kernel reads ceil(V / 32) of each
+    off, t = _i32(5), _i32(4)
+    for V, words in ((7000, 10), (7000, 218), (33, 1), (32, 0)):
+        x, big = torch.zeros((4, V)), _i32(4, 1000)
+        for allowed, match in ((big[:, 1000 - words:], "words"), (big[:1, :words], "words"), (_i32(4, words), "words"),
+                               (_i32(0, words), "words"), (big[:, :(V + 31) // 32], "not the current GPU"), (big, "not the current GPU")):
+            with pytest.raises(ValueError, match=match):
+                B.dspark_target_tokens(x, off, 1, 1, t, allowed=allowed)
