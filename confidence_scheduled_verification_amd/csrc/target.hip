@@ -551,7 +551,7 @@ __global__ __launch_bounds__(kHistoryT) void history_add_kernel(dspark_history_t
     uint32_t* bits = h.seen + ((size_t)r * 2 + (answered ? 1 : 0)) * words;
     int32_t* count = h.count + (size_t)r * h.V;
     bool bad = false;
-    for (int at = blockIdx.y * kHistoryT + threadIdx.x; at < width; at += gridDim.y * kHistoryT) {
+    for (size_t at = blockIdx.y * kHistoryT + threadIdx.x; at < (size_t)width; at += gridDim.y * kHistoryT) {
         const int v = tokens[(size_t)i * width + at];
         if (v < 0) continue;
         if (v >= h.V) {
@@ -712,7 +712,7 @@ hipError_t launch_history_add(const dspark_history_t& h, const int32_t* tokens, 
                               int answered, uint32_t* status, hipStream_t s) {
     const size_t words = dspark_history_words(h.V);
     if (width < kWideFrom || h.V > (answered ? kMostInLds / 2 : kMostInLds) || (long long)width > 65535ll * kAnswerSlice) {
-        const int slices = std::min((width + kHistoryT - 1) / kHistoryT, 256);
+        const int slices = std::min((width - 1) / kHistoryT + 1, 256);
         hipLaunchKernelGGL(history_add_kernel, dim3(n, slices), dim3(kHistoryT), 0, s, h, words, tokens, width, rows,
                            answered, status);
     } else if (answered) {

@@ -461,3 +461,19 @@ def test_history_past_32_bits():
     B.dspark_history_clear(h, cu.i32([rows - 1]))
     torch.cuda.synchronize()
     assert not h.seen.any() and int(h.count.sum()) == 0
+
+
+def test_history_of_the_widest_rows():
+    # entry numbers up to the last one that 32 bits hold (8 GiB of tokens)
+    _say("history, widest rows")
+    width = (1 << 31) - 1
+    tokens = torch.full((1, width), -1, dtype=torch.int32, device=cu.DEV)
+    for at, v in ((0, 3), (width // 2, 3), (width - 65536, 4), (width - 1, 5)):
+        tokens[0, at] = v
+    h, status = B.History(2, 40, device=cu.DEV), torch.zeros(1, dtype=torch.int32, device=cu.DEV)
+    B.dspark_history_add(h, tokens, True, rows=cu.i32([1]), status=status)
+    B.dspark_history_add(h, tokens, False, rows=cu.i32([0]), status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    assert h.count[1].tolist() == [0, 0, 0, 2, 1, 1] + [0] * 34 and not h.count[0].any()
+    assert h.seen[:, :, 0].tolist() == [[0b111000, 0], [0, 0b111000]] and not h.seen[:, :, 1:].any()
