@@ -691,10 +691,12 @@ size_t target_ws_bytes(long long n_rows, int parts) {
     return kCounted * sizeof(uint32_t) + (size_t)(n_rows * parts) * sizeof(TargetBest);
 }
 
+// Of every vocabulary up to V, however many rows: a larger one may have fewer (2097152 tokens of one row
+// are 512 parts, 2097153 are 482).  Parts are as many as are wanted at most, and parts of kLeastChunk or
+// more, unless kMostChunk makes them more.
 int target_most_parts(int V) {
-    int chunk, parts;
-    target_split(1, V, chunk, parts);
-    return parts;
+    const auto parts = [&](int chunk) { return (int)(((long long)V + chunk - 1) / chunk); };
+    return std::max(std::min(kWanted, parts(kLeastChunk)), parts(kMostChunk));
 }
 
 hipError_t launch_target(const TargetArgs& a, hipStream_t s) {

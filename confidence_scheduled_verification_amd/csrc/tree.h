@@ -62,7 +62,7 @@ struct TargetArgs {
 void target_split(int rows, int V, int& chunk, int& parts);
 void target_ws_layout(TargetArgs& a, void* ws);
 size_t target_ws_bytes(long long n_rows, int parts);
-int target_most_parts(int V);  // however many rows there are
+int target_most_parts(int V);  // of up to V tokens, however many rows there are
 hipError_t launch_target(const TargetArgs& a, hipStream_t s);
 
 }  // namespace dspark

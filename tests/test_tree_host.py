@@ -268,3 +268,26 @@ def test_binding_refuses_masks_narrower_than_the_vocabulary():
                                (_i32(0, words), "words"), (big[:, :(V + 31) // 32], "not the current GPU"), (big, "not the current GPU")):
             with pytest.raises(ValueError, match=match):
                 B.dspark_target_tokens(x, off, 1, 1, t, allowed=allowed)
+
+
+def test_a_target_workspace_serves_every_smaller_call():
+    # what is promised: rows and tokens up to those that the size was asked for
+    L, p, ws = B.lib(), _fake(1 << 14), _fake(4096)
+    W = L.dspark_target_workspace_bytes
+    sizes = sorted({1, 2, 255, 256, 4095, 4096, 4097, 8193, 100000, 129280, 131072, 131073, 262145}
+                   | {512 * 4096 + d for d in (-4096, -1, 0, 1, 255, 256, 257, 4096, 100000)}
+                   | {512 * 131072 + d for d in (-1, 0, 1, 131072)} | {513 * 4352, 3 << 20, 1 << 22, (1 << 22) + 1, 1 << 30})
+    for n in (1, 2, 3, 100, 4096, 4097, 100000):
+        got = [W(n, V) for V in sizes]
+        assert got == sorted(got) and got[0] > 0, (n, got)
+        assert all(W(n, V) <= W(n + 1, V) for V in sizes)
+
+    def call(V, rows, n):  # the workspace is not aligned, so that one which is large enough is refused for that
+        c = B.dspark_target_t(logits=p, logits_stride=V, n_rows=rows, V=V, dtype=1, R=rows, lead=1, max_new=1, offsets=p, target=p)
+        return L.dspark_target_tokens(ctypes.byref(c), None, ws + 8, n, None)
+    for large in sizes:
+        for V in sizes:
+            if V <= large:
+                for rows in (1, 2, 3, 100, 600, 4097):
+                    assert call(V, rows, W(rows, large)) == -1, (V, large, rows)
+                assert call(V, 3, W(100, large)) == -1
