@@ -289,8 +289,10 @@ __global__ __launch_bounds__(kT, kPerSimd) void target_kernel(TargetArgs a) {
         for (int i = 0; i < n_draft; ++i) c += s_draft[i] == v;
         double x = (double)logit;
         if (seen || c > 0) x = x > 0.0 ? x / (double)repetition : x * (double)repetition;
-        x = x - (double)frequency * (double)c;
-        if (c > 0) x = x - (double)presence;
+        if (c > 0) {
+            x = x - (double)frequency * (double)c;
+            x = x - (double)presence;
+        }
         if (biased) x = x + (double)by;
         if (kOut) out[v] = E::bits((float)x);
         return x;

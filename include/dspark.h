@@ -803,7 +803,8 @@ int dspark_history_add(const dspark_history_t* history, const int32_t* tokens, i
  *   c(v) = count[r, v] + how many of the drafts that row t has behind it, its own among them, are v
  *   x(v) = logits[t, v]
  *   x(v) = x(v) > 0 ? x(v) / repetition[r] : x(v) * repetition[r]   where v is in the prompt or c(v) > 0
- *   x(v) = x(v) - frequency[r] * c(v);  x(v) = x(v) - presence[r]   where c(v) > 0
+ *   x(v) = x(v) - frequency[r] * c(v)                               where c(v) > 0
+ *   x(v) = x(v) - presence[r]                                       where c(v) > 0
  *   x(v) = x(v) + bias(r, v)                                        where the request has one for v
  *   target[t] = the v with the largest x(v) of those that the row's mask allows
  * in this order and in 64 bits, so that which of two near values is larger does not hang on a

@@ -235,8 +235,8 @@ def choose(logits, path, prompt=(), count=None, repetition=1.0, presence=0.0, fr
         for v in set(prompt) | set(times):
             n = times.get(v, 0)
             x[v] = x[v] / repetition if x[v] > 0 else x[v] * repetition
-            x[v] = x[v] - np.float64(frequency) * n
             if n > 0:
+                x[v] = x[v] - np.float64(frequency) * n
                 x[v] = x[v] - presence
         for v, b in (bias or {}).items():
             x[v] = x[v] + b

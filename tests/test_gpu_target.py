@@ -477,3 +477,24 @@ def test_history_of_the_widest_rows():
     assert int(status.item()) == 0
     assert h.count[1].tolist() == [0, 0, 0, 2, 1, 1] + [0] * 34 and not h.count[0].any()
     assert h.seen[:, :, 0].tolist() == [[0b111000, 0], [0, 0b111000]] and not h.seen[:, :, 1:].any()
+
+
+@pytest.mark.parametrize("frequency", [math.inf, -math.inf, math.nan])
+def test_frequencies_that_are_no_numbers_reach_what_was_answered_alone(frequency):
+    # not the prompt's tokens, nor those that only a bias changes
+    _say("target, frequency", frequency)
+    for dtype, V, seen in (("fp32", 5003, 0), ("bf16", 9000, 1), ("bf16", 5003, 60)):
+        s = Step(40, [5, 1, 12], V, dtype, seen=seen, biased=6)
+        s.penalties = [[1.0] * 3, [0.25] * 3, [frequency] * 3]
+        if seen < 2:  # and nothing has been answered
+            s.drafts = None
+        s.check()
+
+
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan, 3.4e38, -3.4e38])
+def test_biases_of_any_value(value):
+    _say("target, biases", value)
+    for dtype, V in (("fp32", 5003), ("fp16", 9000)):
+        s = Step(41, [5, 1, 12], V, dtype, biased=6)
+        s.bias = [[(v, value if i % 2 else b) for i, (v, b) in enumerate(x)] for x in s.bias]
+        s.check()
