@@ -30,7 +30,7 @@ namespace dspark {
 namespace {
 
 #define INLINE __attribute__((always_inline))
-constexpr int kT = 512, kWaves = kT / 64;
+constexpr int kT = kTargetThreads, kWaves = kT / 64;
 constexpr int kPerSimd = 7;           // waves that the registers leave room for
 constexpr int kGroups = 2;            // of eight logits: a lane's loads under way, twice
 constexpr int kMostChunk = 131072;    // tokens of a part: twice 16 KB of bits in LDS

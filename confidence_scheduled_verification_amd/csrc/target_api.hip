@@ -17,6 +17,8 @@ using dspark::kTreeNodes;
 namespace {
 
 constexpr int kMostTokens = 1 << 30;  // of a vocabulary
+constexpr long long kMostThreads = (1ll << 32) - 1;  // of a launch along its requests
+constexpr int kMostHistoryRows = (int)(kMostThreads / 1024);
 
 int done(hipError_t e, const char* who) { return e == hipSuccess ? DSPARK_OK : hip_fail(e, who); }
 
@@ -139,6 +141,7 @@ int dspark_history_clear(const dspark_history_t* h, const int32_t* rows, int n, 
     const int rc = check_history(h, who);
     if (rc != DSPARK_OK) return rc;
     if (n < 0 || (!rows && n > h->rows)) return fail(DSPARK_ERANGE, "%s: %d rows, the history has %d", who, n, h->rows);
+    if (n > kMostHistoryRows) return fail(DSPARK_EUNSUPPORTED, "%s: %d rows exceed %d", who, n, kMostHistoryRows);
     if (n == 0) return DSPARK_OK;
     return done(dspark::launch_history_clear(*h, rows, n, status, (hipStream_t)stream), who);
 }
@@ -150,6 +153,7 @@ int dspark_history_add(const dspark_history_t* h, const int32_t* tokens, int n, 
     if (rc != DSPARK_OK) return rc;
     if (n < 0 || (!rows && n > h->rows)) return fail(DSPARK_ERANGE, "%s: %d rows, the history has %d", who, n, h->rows);
     if (width < 0) return fail(DSPARK_ERANGE, "%s: width %d", who, width);
+    if (n > kMostHistoryRows) return fail(DSPARK_EUNSUPPORTED, "%s: %d rows exceed %d", who, n, kMostHistoryRows);
     if (n == 0 || width == 0) return DSPARK_OK;
     if (!tokens) return fail(DSPARK_EINVAL, "%s: tokens is NULL", who);
     return done(dspark::launch_history_add(*h, tokens, n, width, rows, answered, status, (hipStream_t)stream), who);
@@ -214,6 +218,8 @@ int dspark_target_tokens(const dspark_target_t* t, uint32_t* status, void* ws, s
         return fail(DSPARK_EWORKSPACE, "%s: workspace of %zu bytes needed, %zu given%s", who, need, ws_bytes,
                     ws ? "" : " (NULL)");
     if ((uintptr_t)ws & 15u) return fail(DSPARK_EINVAL, "%s: workspace must be 16-byte aligned", who);
+    if ((long long)t->R * a.parts > kMostThreads / dspark::kTargetThreads)
+        return fail(DSPARK_EUNSUPPORTED, "%s: %d requests of %d parts each are too many for one call", who, t->R, a.parts);
     if (need) dspark::target_ws_layout(a, ws);
     return done(dspark::launch_target(a, (hipStream_t)stream), who);
 }

@@ -58,6 +58,7 @@ struct TargetArgs {
     TargetBest* best;
     uint32_t* status;
 };
+constexpr int kTargetThreads = 512;  // of a workgroup
 // How as many rows of V tokens are taken apart.
 void target_split(int rows, int V, int& chunk, int& parts);
 void target_ws_layout(TargetArgs& a, void* ws);

@@ -789,7 +789,7 @@ typedef struct dspark_history {
 size_t dspark_history_words(int V); /* ceil(V / 128) * 4 */
 
 /* History rows emptied: rows[i] for i < n, or rows 0 .. n-1 where rows is NULL.  A rows[i] outside
- * the history is left out (DSPARK_STATUS_BAD_ROW), here and in dspark_history_add. */
+ * the history is left out (DSPARK_STATUS_BAD_ROW), here and in dspark_history_add.  n < 2^22 in both. */
 int dspark_history_clear(const dspark_history_t* history, const int32_t* rows, int n, uint32_t* status, void* stream);
 
 /* Tokens entered: tokens [n, width] int32 into history rows rows[i] (i where rows is NULL), as prompt
@@ -833,6 +833,8 @@ int dspark_history_add(const dspark_history_t* history, const int32_t* tokens, i
  * A request with n_r < 0 or > max_new or rows outside the tensors is left out (DSPARK_STATUS_BAD_ROW), and
  * rows that belong to no request stay as they are; a row that two requests have (offsets that fall and
  * rise again) gets some token.
+ * Limits: R <= DSPARK_CACHE_MAX_REQUESTS, V <= 2^30, and R times the parts that a row is taken in (1 of up to
+ * 4096 tokens; at most the larger of 512 and V / 131072, rounded up) below 2^23.
  */
 #define DSPARK_TARGET_MAX_ROWS 256
 typedef struct dspark_target {

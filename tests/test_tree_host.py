@@ -291,3 +291,21 @@ def test_a_target_workspace_serves_every_smaller_call():
                 for rows in (1, 2, 3, 100, 600, 4097):
                     assert call(V, rows, W(rows, large)) == -1, (V, large, rows)
                 assert call(V, 3, W(100, large)) == -1
+
+
+def test_more_than_a_launch_holds_is_refused():
+    # a launch has fewer than 2^32 threads along the requests (rows of tokens), 1024 or 512 to each
+    L, p, ws = B.lib(), _fake(1 << 14), _fake(4096)
+    h = B.dspark_history_t(p, p, 4, 100)
+    KEEP.append(h)
+    for n in (1 << 22, (1 << 31) - 1):
+        assert L.dspark_history_clear(ctypes.byref(h), p, n, None, None) == -3
+        for answered in (0, 1):
+            assert L.dspark_history_add(ctypes.byref(h), p, n, 300, p, answered, None, None) == -3
+
+    def target(V, R, rows, ws):
+        c = B.dspark_target_t(logits=p, logits_stride=V, n_rows=rows, V=V, dtype=1, R=R, lead=1, max_new=1, offsets=p, target=p)
+        return L.dspark_target_tokens(ctypes.byref(c), None, ws, 1 << 40, None)
+    assert target(1 << 30, 8192, 1, ws) == -3 == target(1 << 30, 1024, 1024, ws)
+    for V, R, rows in ((1 << 30, 1023, 1023), (129280, 8192, 1), (1 << 22, 8192, 1)):  # (not aligned: nothing is launched)
+        assert target(V, R, rows, ws + 8) == -1
