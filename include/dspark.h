@@ -858,7 +858,9 @@ typedef struct dspark_target {
 } dspark_target_t;
 /* Bytes of workspace (16-byte aligned) for up to n_rows rows of up to V tokens.  Zero-fill it once,
  * before its first use: the kernel counts the parts of a row in it, and leaves the counts at zero for
- * the next call, of whatever sizes.  Calls that may run at the same time need one each. */
+ * the next call, of whatever sizes.  Calls that may run at the same time need one each, and nothing else
+ * may be kept in it between calls (it is not a scratch buffer that other entry points could share): with
+ * other counts than these, rows of several parts get a wrong token or none, without a status. */
 size_t dspark_target_workspace_bytes(int n_rows, int V);
 int dspark_target_tokens(const dspark_target_t* call, uint32_t* status, void* ws, size_t ws_bytes, void* stream);
 
