@@ -85,7 +85,7 @@ class dspark_history_t(ctypes.Structure):
 
 
 class dspark_target_t(ctypes.Structure):
-    """The arguments of dspark_target_tokens (include/dspark.h)."""
+    """The arguments of dspark_target_tokens (include/dspark.h, where `reserved` is no_token)."""
     _fields_ = [("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_int64)] + \
         [(n, ctypes.c_int32) for n in ("n_rows", "V", "dtype", "R", "lead", "max_new")] + \
         [(n, ctypes.c_void_p) for n in ("offsets", "history", "repetition", "presence", "frequency", "ver_tokens", "anc",
@@ -923,10 +923,11 @@ assert _TARGET.size == ctypes.sizeof(dspark_target_t)
 
 def dspark_target_tokens(logits, offsets, lead: int, max_new: int, target, history: Optional[History] = None,
                          penalties=(None, None, None), node_tokens=None, anc=None, bias=None, allowed=None, allowed_row=None,
-                         adjusted=None, ws=None, status=None, stream=None):
+                         adjusted=None, ws=None, status=None, stream=None, no_token: int = 0):
     """The target's choice at each row of a step from its logits [rows, V], after penalties (repetition,
     presence, frequency: float32 [R] or None each), biases (bias_off [R+1], bias_tok, bias_val) and the masks
-    allowed [n, words] (row allowed_row[t] binds row t).  `adjusted` [rows, V] receives the processed logits."""
+    allowed [n, words] (row allowed_row[t] binds row t).  `adjusted` [rows, V] receives the processed logits;
+    `no_token` is the target of rows whose mask allows nothing: 0, or -1 for none, which no draft is."""
     what, torch = "dspark_target_tokens", _torch()
     kind, f32 = logits.dtype, torch.float32
     dtype = DSPARK_BF16 if kind is torch.bfloat16 else DSPARK_F32 if kind is f32 else DSPARK_F16
@@ -968,7 +969,7 @@ def dspark_target_tokens(logits, offsets, lead: int, max_new: int, target, histo
         logits.data_ptr(), stride, n_rows, V, dtype, R, lead, max_new, offsets.data_ptr(), 0 if history is None else history.address,
         _p(repetition) or 0, _p(presence) or 0, _p(frequency) or 0, _p(node_tokens) or 0, _p(anc) or 0, _p(off) or 0, _p(tok) or 0,
         _p(val) or 0, _p(allowed) or 0, _p(allowed_row) or 0, pitch, 0 if node_tokens is None else node_tokens.numel(),
-        0 if tok is None else tok.numel(), n_allowed, 0, target.data_ptr(), _p(adjusted) or 0, out_stride)
+        0 if tok is None else tok.numel(), n_allowed, no_token, target.data_ptr(), _p(adjusted) or 0, out_stride)
     _check(lib().dspark_target_tokens(call, _p(status), _p(ws), _ws_bytes(ws), st))
 
 

@@ -469,7 +469,7 @@ __global__ __launch_bounds__(kT, kPerSimd) void target_kernel(TargetArgs a) {
         if (tid == 0) __hip_atomic_fetch_sub(&a.came[row], (uint32_t)a.parts, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next call
     }
     if (tid == 0) {
-        t.target[row] = best.key ? (int32_t)best.v : 0;  // 0: the argmax of values that are all -inf
+        t.target[row] = best.key ? (int32_t)best.v : t.no_token;
         if (!best.key) raise_status(a.status, kStatusNoToken);
     }
 }
@@ -488,7 +488,7 @@ __global__ __launch_bounds__(64) void target_join_kernel(TargetArgs a) {
     }
     wave_best(best);
     if (threadIdx.x == 0) {
-        a.t.target[row] = best.key ? (int32_t)best.v : 0;
+        a.t.target[row] = best.key ? (int32_t)best.v : a.t.no_token;
         if (!best.key) raise_status(a.status, kStatusNoToken);
     }
 }

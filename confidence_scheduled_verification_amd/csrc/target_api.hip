@@ -175,6 +175,8 @@ int dspark_target_tokens(const dspark_target_t* t, uint32_t* status, void* ws, s
         return fail(DSPARK_EINVAL, "%s: unknown dtype %d", who, t->dtype);
     if (t->n_nodes < 0 || t->n_bias < 0 || t->n_allowed < 0)
         return fail(DSPARK_ERANGE, "%s: n_nodes %d, n_bias %d, n_allowed %d", who, t->n_nodes, t->n_bias, t->n_allowed);
+    if (t->no_token < -1 || t->no_token >= t->V)
+        return fail(DSPARK_ERANGE, "%s: no_token %d outside -1 .. %d", who, t->no_token, t->V - 1);
     if (t->history) {
         const int bad = check_history(t->history, who);
         if (bad != DSPARK_OK) return bad;

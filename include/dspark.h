@@ -78,7 +78,7 @@ typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_F16 = 2 /* the paged cach
                                            length or index do not fit (see each call for what becomes of it) */
 #define DSPARK_STATUS_NO_PAGES 128u     /* paged cache: too few free pages, or no room in the table; the request or
                                            fork was not served                                              */
-#define DSPARK_STATUS_NO_TOKEN 256u     /* dspark_target_tokens: a row's mask allows no token; its target is 0 */
+#define DSPARK_STATUS_NO_TOKEN 256u     /* dspark_target_tokens: a row's mask allows no token (see no_token) */
 
 /* Admission rules of stage 4. */
 #define DSPARK_RULE_ARGMAX 0      /* the smallest B with the largest f(B) (vLLM blog, "Scheduling the budget")  */
@@ -826,8 +826,10 @@ int dspark_history_add(const dspark_history_t* history, const int32_t* tokens, i
  *                word v / 32 set where token v is allowed; or NULL: all are
  *   allowed_row  [n_rows] int32: the row of allowed that binds row t, -1 for none; or NULL: row t.  Another
  *                number allows nothing (DSPARK_STATUS_BAD_ROW)
- *   target       [n_rows] int32 output; 0 where no token is allowed, as the argmax of values that are all
- *                -inf (DSPARK_STATUS_NO_TOKEN)
+ *   target       [n_rows] int32 output; no_token where no token is allowed (DSPARK_STATUS_NO_TOKEN)
+ *   no_token     -1 .. V-1.  0 is the argmax of values that are all -inf, but a token like others: a draft 0 is
+ *                accepted there, or 0 answered, though the mask forbids it.  -1 is none: no draft is it, a path
+ *                ends there, and as an answer dspark_history_add passes it over; so a caller sees which rows they are
  *   adjusted     [n_rows] rows of V values, adjusted_stride elements apart, in logits' dtype: output x(v),
  *                rounded once from fp32, -inf where v is not allowed; or NULL
  * A request with n_r < 0 or > max_new or rows outside the tensors is left out (DSPARK_STATUS_BAD_ROW), and
@@ -851,7 +853,7 @@ typedef struct dspark_target {
     const uint32_t* allowed;
     const int32_t* allowed_row;
     int64_t allowed_stride;
-    int32_t n_nodes, n_bias, n_allowed, reserved;
+    int32_t n_nodes, n_bias, n_allowed, no_token;
     int32_t* target;
     void* adjusted;
     int64_t adjusted_stride;

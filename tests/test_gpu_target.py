@@ -498,3 +498,65 @@ def test_biases_of_any_value(value):
         s = Step(41, [5, 1, 12], V, dtype, biased=6)
         s.bias = [[(v, value if i % 2 else b) for i, (v, b) in enumerate(x)] for x in s.bias]
         s.check()
+
+
+@pytest.mark.parametrize("V,rows,dtype", [(700, [3, 3, 2], "bf16"), (40000, [2, 1], "fp32"), (9000, [64] * 8, "fp16")])
+def test_rows_without_a_token_can_have_none(V, rows, dtype):
+    # whole rows, rows in parts, many rows
+    _say("target, none", V, len(rows), dtype)
+    s = Step(50, rows, V, dtype, masks=3, biased=0, seen=3, tree=False)
+    s.allowed[1] = False
+    s.pick = [(1, 0, 2, -1, 3)[t * 7 % 5] for t in range(s.n)]
+    for token in (-1, 0, 5, V - 1):
+        kw = s.prepared(adjusted=False)
+        s.call(dict(kw, no_token=token))
+        torch.cuda.synchronize()
+        if token == -1:
+            want = s.want()[0]
+            empty = {t for t in want if s.pick[t] in (1, 3)}
+            assert empty and len(empty) < len(want)
+        assert s.target.tolist() == [token if t in empty else want.get(t, -7) for t in range(s.n)]
+        assert int(s.status.item()) == B.STATUS_NO_TOKEN | B.STATUS_BAD_ROW
+
+
+def test_a_draft_does_not_pass_a_mask_that_allows_nothing():
+    # a path ends at a row without a token, whose answer is none: for trees, chains and the history
+    _say("target, none accepted")
+    V, off = 50, cu.i32([0, 3])
+    x = torch.zeros((4, V), device=cu.DEV)
+    x[0, 4], x[1, 0], x[2, 0], x[3, 9] = 1.0, 1.0, 1.0, 1.0   # the drafts 4, 0, 0 and then 9 without masks
+    drafts, parent = cu.i32([4, 0, 0]), cu.i32([-1, 0, 1, 2])
+    allowed = _pack(np.stack([np.ones(V, bool), np.zeros(V, bool)]))
+    new = lambda *n: torch.full(n, 7, dtype=torch.int32, device=cu.DEV)  # noqa: E731
+    for token, out in ((0, [4, 0, 0, 9]), (-1, [4, -1, -1, -1])):
+        target, status = new(4), torch.zeros(1, dtype=torch.int32, device=cu.DEV)
+        B.dspark_target_tokens(x, off, 1, 4, target, allowed=allowed, allowed_row=cu.i32([0, 1, 0, 0]), status=status, no_token=token,
+                               ws=B.target_workspace(4, V))
+        accept, path, bonus, answer = new(1), new(1, 3), new(1), new(1, 4)
+        B.dspark_accept_tree(drafts, off, parent, target, accept, path, bonus, out_tokens=answer, status=status)
+        h = B.History(1, V, device=cu.DEV)
+        B.dspark_history_add(h, answer, True, status=status)
+        torch.cuda.synchronize()
+        assert target.tolist() == [4, token, 0, 9] and int(status.item()) == B.STATUS_NO_TOKEN
+        assert answer.tolist() == [out] and accept.item() == sum(v >= 0 for v in out) - (token == 0) and bonus.item() == (9 if token == 0 else -1)
+        counts = [0] * V
+        for v in out:
+            if v >= 0:
+                counts[v] += 1
+        assert h.count[0].tolist() == counts
+
+
+def test_more_rows_than_are_counted_can_have_none():
+    # their parts are joined by a kernel of its own
+    _say("target, none of many")
+    n, V = 4100, 131100
+    x = torch.zeros((n, V), dtype=torch.bfloat16, device=cu.DEV)
+    x[:, V - 1] = 1.0
+    pick = np.arange(n) % 3 - 1
+    target, status = torch.full((n,), -7, dtype=torch.int32, device=cu.DEV), torch.zeros(1, dtype=torch.int32, device=cu.DEV)
+    allowed = _pack(np.stack([np.arange(V) < V - 1, np.zeros(V, bool)]))
+    for token in (-1, 0):
+        B.dspark_target_tokens(x, cu.i32(np.zeros(n + 1)), 1, 1, target, allowed=allowed, allowed_row=cu.i32(pick), status=status,
+                               no_token=token, ws=B.target_workspace(n, V))
+        torch.cuda.synchronize()
+        assert target.tolist() == [(V - 1, 0, token)[p + 1] for p in pick.tolist()] and int(status.item()) == B.STATUS_NO_TOKEN

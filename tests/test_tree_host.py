@@ -309,3 +309,14 @@ def test_more_than_a_launch_holds_is_refused():
     assert target(1 << 30, 8192, 1, ws) == -3 == target(1 << 30, 1024, 1024, ws)
     for V, R, rows in ((1 << 30, 1023, 1023), (129280, 8192, 1), (1 << 22, 8192, 1)):  # (not aligned: nothing is launched)
         assert target(V, R, rows, ws + 8) == -1
+
+
+def test_target_of_rows_without_a_token_is_a_token_or_none():
+    L, p, ws = B.lib(), _fake(1 << 14), _fake(4096)
+
+    def call(V, token):
+        c = B.dspark_target_t(logits=p, logits_stride=V, n_rows=2, V=V, dtype=1, R=2, lead=1, max_new=1, offsets=p, target=p, reserved=token)
+        return L.dspark_target_tokens(ctypes.byref(c), None, ws + 8, 1 << 40, None)  # (not aligned: nothing is launched)
+    for V, token, rc in ((100, 0, -1), (100, -1, -1), (100, 99, -1), (1, 0, -1), (100, -2, -2), (100, 100, -2), (1, 1, -2),
+                         (100, -(1 << 31), -2), (100, (1 << 31) - 1, -2)):
+        assert call(V, token) == rc, (V, token)
