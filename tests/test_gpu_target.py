@@ -560,3 +560,48 @@ def test_more_rows_than_are_counted_can_have_none():
                                no_token=token, ws=B.target_workspace(n, V))
         torch.cuda.synchronize()
         assert target.tolist() == [(V - 1, 0, token)[p + 1] for p in pick.tolist()] and int(status.item()) == B.STATUS_NO_TOKEN
+
+
+@pytest.mark.parametrize("V,rows", [(5003, [2, 1, 3, 1]), (40001, [1, 1, 1, 1]), (9000, [8] * 4)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_many_biases(V, rows, dtype):
+    # as many as stand in LDS, one fewer and more; in whole rows and in parts
+    _say("target, many biases", V, rows, dtype)
+    for masks in (0, 2):
+        s = Step(60, rows, V, dtype, masks=masks)
+        s.bias = [[(int(v), float(np.float32(s.rng.standard_normal()))) for v in np.sort(s.rng.choice(V, n, replace=False))]
+                  for n in (511, 512, 513, 2000)]
+        s.check()
+
+
+def test_a_late_bias_that_does_not_rise():
+    # beyond those that stand in LDS: reported; other requests are served
+    _say("target, late bias")
+    V = 3001
+    s = Step(61, [2, 3], V, "fp32", masks=0)
+    tok = list(range(0, 1400, 2))
+    s.bias = [[(v, 0.25) for v in tok], [(3, 1.0), (9, 2.0)]]
+    want = s.want()[0]
+    kw = s.prepared(adjusted=False)
+    for at, v in ((699, 1396), (600, 5), (513, -1), (512, V), (699, 1 << 30)):
+        bad = list(tok)
+        bad[at] = v
+        s.status.zero_()
+        kw["bias"] = (cu.i32([0, 700, 702]), cu.i32(bad + [3, 9]), torch.tensor([0.25] * 700 + [1.0, 2.0], device=cu.DEV))
+        s.call(kw)
+        torch.cuda.synchronize()
+        assert int(s.status.item()) == B.STATUS_BAD_ROW, (at, v)
+        got = s.target.tolist()
+        assert got[2:5] == [want[t] for t in (2, 3, 4)] and all(0 <= x < V for x in got[:2]) and got[5:] == [-7] * (s.n - 5)
+
+
+@pytest.mark.parametrize("lead", [0, 1])
+@pytest.mark.parametrize("V,rows,dtype", [(3001, [256, 65, 1], "bf16"), (2003, [200, 64, 128], "fp32"), (40001, [100, 1, 66], "fp16")])
+def test_long_chains(V, rows, dtype, lead):
+    # up to 256 rows of a request, each with the drafts before it, many of them more than once
+    _say("target, long chains", V, rows, dtype, lead)
+    s = Step(62, rows, V, dtype, lead, tree=False, masks=2, biased=20)
+    s.drafts = [int(v) for v in s.rng.choice(s.rng.choice(V, 40, replace=False), s.n)]
+    s.check()
+    s.penalties = [[0.8, 1.2, 1.0], [-0.5, 0.25, 0.0], [0.05, -0.05, 0.5]]
+    s.check()
