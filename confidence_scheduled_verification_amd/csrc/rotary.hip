@@ -18,12 +18,13 @@
 // workgroups would have few rows or none.
 //
 // Bytes bound it, once read, once written.  The workgroups that share rows are neighbours in the grid:
-// 20 thousand fp16 rows of 32 query and 8 key heads of 128 (353 MB) take 78 us (4.5 TB/s; a large copy
-// reaches 4.9), 108 where a kind's workgroups follow each other through all rows.  1152 rows of 64 and 8 heads
-// (47 MB), of requests of up to eight: 20.6 us (22.4 by blocks), of which 6 are the launch and the loads that
-// wait for each other; a copy of as many bytes takes 10, for which the waves would have to be resident at
-// once.  Eight heads a lane instead of two: 92 and 22 us (fewer waves), one head 22; a request's blocks walked in
-// a loop in place of a workgroup each: 97 and 28 (twice the registers, half the waves).
+// 14351 fp16 rows of 32 query and 8 key heads of 128 (353 MB) take 76 us a call (4.6 TB/s; a large copy
+// reaches 4.9); when it was tried, 108 where a kind's workgroups follow each other through all rows, against 78.
+// 1152 rows of 64 and 8 heads (47 MB), of requests of up to eight: 18.5 us a call, 19.0 in a graph (21.6 by
+// blocks), of which 6 are the launch and the loads that wait for each other; a copy of as many bytes takes 10,
+// for which the waves would have to be resident at once.  An earlier form of both took 78 and 21 us; with eight heads
+// a lane instead of two 92 and 22 (fewer waves), one head 22; a request's blocks walked in a loop in place of a
+// workgroup each: 97 and 28 (twice the registers, half the waves).
 #include <algorithm>
 
 #include "append_dev.h"

@@ -15,11 +15,14 @@
 // by how often they have been said.
 //
 // Bytes bound it where rows are many: 1152 bf16 rows of 129280 (298 MB, and 2000 said tokens, 100
-// biases and a mask each) take 71 us, 4.3 TB/s; looking at every changed token took 126.  Groups of eight
-// without an allowed token are not read.  Four such rows, 32 workgroups each, take 11 us, of which the launch and
-// loads that wait for each other (rows, bits, logits, counts) are all but one; a second launch
-// to join the parts made it 16.  About 340 rows of 32771 in fp32, processed and written (89 MB): 34 us, 2.6
-// TB/s: rows of an odd length stand on no line, and a workgroup is through its part in four loads of a lane.
+// biases and a mask each) take 70 us, 4.4 TB/s; looking at every changed token took 126.  Without penalties,
+// biases and masks the same rows take 57; of 151936 tokens, in two parts of which the second is small, 97 and
+// 70, of 262144 132 and 107.  Groups of eight without an allowed token are not read, past a part's first 8192
+// tokens (whose loads go out before the mask is there) and unless the processed logits are wanted.  Four rows of
+// 129280, 32 workgroups each, take 12 us, of which the launch and loads that wait for each other (rows, bits,
+// logits, counts) are all but one; a second launch to join the parts made it 16.  336 rows of 32771 in fp32,
+// processed and written (89 MB): 34 us, 2.6 TB/s: rows of an odd length stand on no line, and a workgroup is
+// through its part in four loads of a lane and a fifth for the last 32 groups.
 #include <algorithm>
 
 #include "common.h"

@@ -5,8 +5,9 @@
 // lane, and sets of nodes are 64-bit words: comparing is a ballot, counting a population
 // count, and a number among the set's members the count of those before.
 //
-// Merging, planning and accepting are a launch and its loads, which wait for each other: 3 us each for 16
-// requests, 3 to 5 for 256, whatever the trees.
+// Merging, planning and accepting are launches and their loads, which wait for each other: 2.8, 2.7 and 3.0 us
+// for 16 requests (kernels, under the profiler), 3.2 and 3.7 for planning and accepting 256, whatever the
+// trees. More than 64 requests are merged in two launches, counts and then writes: 4.2 and 3.5 us for 256.
 #include <algorithm>
 
 #include "common.h"
@@ -330,8 +331,9 @@ __global__ __launch_bounds__(kT) void keep_path_kernel(dspark_cache_t c, const i
     }
 }
 
-// The requests up to which one workgroup merges them: 4.8 us for 16, 5.1 for 32 and 6.9 for 64, where counting
-// and writing, two launches, take 6.6 to 6.7, and the host 3 more for the second.
+// The requests up to which one workgroup merges them. Whole calls, one after the other in a graph: 3.4 us for 16
+// requests, 4.2 for 32 and 6.2 for 64, where counting and writing, two launches, take 5.4, 5.6 and 5.7, and
+// outside a graph the host 3 more for the second.
 constexpr int kMergeAtOnce = 4 * kMergeWaves;
 static_assert(kMergeAtOnce <= 64, "a request's count to a lane");
 
