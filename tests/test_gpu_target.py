@@ -605,3 +605,82 @@ def test_long_chains(V, rows, dtype, lead):
     s.check()
     s.penalties = [[0.8, 1.2, 1.0], [-0.5, 0.25, 0.0], [0.05, -0.05, 0.5]]
     s.check()
+
+
+def test_the_largest_vocabulary():
+    _say("target, 2^30 tokens")
+    V = 1 << 30
+    x = torch.zeros((1, V), dtype=torch.bfloat16, device=cu.DEV)
+    at = [5, 131072 * 4000 + 17, V - 131072, V - 9, V - 1]
+    x[0, at] = torch.tensor([1.0, 3.0, 2.0, 4.0, 5.0], dtype=torch.bfloat16, device=cu.DEV)
+    h, status = B.History(1, V, device=cu.DEV), torch.zeros(1, dtype=torch.int32, device=cu.DEV)
+    B.dspark_history_add(h, cu.i32([[V - 1, V - 1, V - 9, V]]), True, status=status)
+    B.dspark_history_add(h, cu.i32([[5] * 300]), False, status=status)
+    target, out = torch.full((1,), -7, dtype=torch.int32, device=cu.DEV), torch.full_like(x, 7.0)
+    one = lambda v: torch.full((1,), v, device=cu.DEV)  # noqa: E731
+    ws = B.target_workspace(1, V)
+    for adjusted in (None, out):
+        target.fill_(-7)
+        B.dspark_target_tokens(x, cu.i32([0, 0]), 1, 1, target, history=h, penalties=(one(2.0), one(0.25), one(0.5)), adjusted=adjusted, ws=ws,
+                               bias=(cu.i32([0, 2]), cu.i32([7, V - 131072]), torch.tensor([2.9, 1.5], device=cu.DEV)), status=status)
+        torch.cuda.synchronize()
+        assert target.item() == V - 131072 and int(status.item()) == B.STATUS_BAD_ROW  # 3.5, of 0.5, 3.0, 3.5, 1.25 and 1.25
+    assert out[0, at].tolist() == [0.5, 3.0, 3.5, 1.25, 1.25] and abs(out[0, 7].item() - 2.9) <= 2.9 * 2.0 ** -8
+    out[0, at + [7]] = 0
+    assert not out.any()
+
+
+def test_the_most_rows():
+    # as many requests as there may be, of as many rows, each with the drafts before it
+    _say("target, 8192 requests of 256 rows")
+    R, n, V = 8192, 256, 11
+    g = torch.Generator(device=cu.DEV).manual_seed(1)
+    x = torch.randint(0, 9, (R * n, V), generator=g, device=cu.DEV).to(torch.float16)
+    drafts = torch.randint(0, V, (R, n), generator=g, device=cu.DEV, dtype=torch.int32)
+    target = torch.full((R * n,), -7, dtype=torch.int32, device=cu.DEV)
+    off = (torch.arange(R + 1, device=cu.DEV) * n).int()
+    B.dspark_target_tokens(x, off, 0, n, target, penalties=(None, None, torch.full((R,), 0.25, device=cu.DEV)), node_tokens=drafts.view(-1),
+                           ws=B.target_workspace(R * n, V))
+    said = torch.nn.functional.one_hot(drafts.long(), V).cumsum(1).view(R * n, V)
+    want = x.float() - 0.25 * said  # exact
+    best = torch.where(want == want.amax(1, keepdim=True), torch.arange(V, device=cu.DEV), V).amin(1)
+    torch.cuda.synchronize()
+    assert torch.equal(target, best.int())
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_processed_rows_of_a_wider_tensor(dtype):
+    _say("target, wide adjusted", dtype)
+    for V, gap, first in ((3001, 5, 3), (40000, 7, 1), (64, 1, 0)):
+        s = Step(70, [3, 1, 6], V, dtype)
+        want = s.want()
+        kw = s.prepared(adjusted=False)
+        wide = torch.full((s.n, V + gap), 7.0, dtype=DT[dtype], device=cu.DEV)
+        kw["adjusted"] = wide[:, first:first + V]
+        s.call(kw)
+        torch.cuda.synchronize()
+        assert s.target.tolist() == [want[0].get(t, -7) for t in range(s.n)]
+        for t in range(s.n):
+            y = np.full(V + gap, 7.0, np.float32)
+            if t in want[1]:
+                y[first:first + V] = torch.from_numpy(want[1][t]).float().to(DT[dtype]).float().numpy()
+            np.testing.assert_array_equal(wide[t].float().cpu().numpy(), y)
+
+
+def test_two_calls_at_once():
+    # on two streams, with a workspace each: one history and one set of logits read by both
+    _say("target, two streams")
+    s = Step(71, [3, 1, 6], 60000, "bf16")
+    want = [s.want()[0].get(t, -7) for t in range(s.n)]
+    kw, off = s.prepared(adjusted=False), cu.i32(s.offsets)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [torch.full_like(s.target, -7) for _ in streams]
+    ws = [B.target_workspace(s.n, s.V) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for i, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                got[i].fill_(-7)
+                B.dspark_target_tokens(s.logits, off, s.lead, s.max_new, got[i], **dict(kw, ws=ws[i]))
+    torch.cuda.synchronize()
+    assert [x.tolist() for x in got] == [want, want]
