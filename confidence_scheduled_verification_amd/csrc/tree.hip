@@ -236,6 +236,7 @@ __device__ __forceinline__ void put_at(u32x8& row, int i, uint32_t x) {
 // of up to 28 nodes, 16 layers of 8 key heads of 128: 23 us, of which 67 MB read and written would take 14;
 // with two bytes of V at a time 34, with K and V one after the other 41, with some layers one after the
 // other 76.  The workgroups of a request stand together in the grid: with the layers together it takes 31.
+// (The compiler keeps the rows of V that a thread has under way in LDS, 16 KB of a workgroup's 17.5.)
 __global__ __launch_bounds__(kT) void keep_path_kernel(dspark_cache_t c, const int32_t* path, int K,
                                                        const int32_t* accept_len, const int32_t* granted, int lead,
                                                        uint32_t* status) {
